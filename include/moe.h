@@ -1,8 +1,8 @@
 /*
  * moe.h -- C ABI of one GPU's MoE feed-forward layer on AMD Instinct MI355X
  * (gfx950): router top-k and route map, rowwise dispatch (permute), grouped
- * SwiGLU GEMM forward and backward, weighted un-permute/combine, and the
- * MXFP8 block quantiser.
+ * SwiGLU GEMM forward and backward, weighted un-permute/combine, the MXFP8
+ * and MXFP4 block quantisers, and the router's balance loss.
  *
  * The operations follow the pages describing the OLMo-core 3 MoE training
  * stack ("OLMo-core 3: MoE 训练栈..." tutorial; "Ai2 Olmo-core 3: The Secret
@@ -39,8 +39,8 @@
  *     Results are bitwise reproducible for identical inputs (no
  *     floating-point atomics anywhere).
  *   - Limits: 1 <= E <= 1024, 1 <= k <= min(E, 8), row widths d and f
- *     multiples of 8 (MXFP8: 32 for the permute / quantiser, 128 for the
- *     grouped GEMMs), all pointers 16-byte aligned, n_rows < 2^31.
+ *     multiples of 8 (MXFP8, MXFP4: 32 for the permute / quantiser, 128 for
+ *     the grouped GEMMs), all pointers 16-byte aligned, n_rows < 2^31.
  */
 #ifndef MOE_MI355X_H
 #define MOE_MI355X_H
@@ -73,7 +73,8 @@ enum moe_status {
 enum moe_dtype {
     MOE_F32 = 0,            /* fp32 activations and weights, fp32 accumulate */
     MOE_BF16 = 1,           /* bf16 storage, fp32 accumulate */
-    MOE_MXFP8 = 2           /* E4M3FN codes + one E8M0 scale per 32 elements, fp32 accumulate */
+    MOE_MXFP8 = 2,          /* E4M3FN codes + one E8M0 scale per 32 elements, fp32 accumulate */
+    MOE_MXFP4 = 3           /* E2M1 codes, two per byte, + one E8M0 scale per 32, fp32 accumulate (forward only) */
 };
 
 enum moe_dev_err_bits {
@@ -140,14 +141,16 @@ MOE_API int moe_route_topk_noalloc(const float* logits, int T, int E, int k, int
  * in   dtype      MOE_F32: x, x_perm fp32.  MOE_BF16: x, x_perm bf16 (an exact
  *                 copy).  MOE_MXFP8: x bf16; x_perm receives E4M3FN codes
  *                 [n_rows, d] and x_perm_scales E8M0 [n_rows, d/32] (dispatch
- *                 payload in MXFP8, tutorial MXFP8 section).
+ *                 payload in MXFP8, tutorial MXFP8 section).  MOE_MXFP4: x bf16;
+ *                 x_perm receives E2M1 codes [n_rows, d/2] and x_perm_scales
+ *                 E8M0 [n_rows, d/32], as moe_quantize_mxfp4 writes them.
  * in   x          [T, d].
  * in   dst_row    [T*k] from moe_route_topk.
  * in   src_slot   [n_rows]; required when n_rows != T*k (padded): rows with
  *                 src_slot < 0 are zero-filled.  May be NULL otherwise.
  * in   row_scale  NULL, or [T*k] fp32: row (t, j) is written as
  *                 round(row_scale[t*k+j] * x[t]) (the backward of the weighted
- *                 combine).  Not combined with MOE_MXFP8.
+ *                 combine).  Not combined with MOE_MXFP8 or MOE_MXFP4.
  * out  x_perm     [n_rows, d].
  * out  dev_err    optional; MOE_ERR_ROW_RANGE.
  */
@@ -158,7 +161,8 @@ MOE_API int moe_permute(int dtype, const void* x, int T, int d, int k, const int
 /* Bytes of scratch the grouped GEMM calls need: MOE_F32 none; MOE_BF16 the
  * weight-gradient stage's control words (256 bytes: a small kernel ahead of
  * that stage decides there how its tiles go to the XCDs); MOE_MXFP8 those
- * plus the quantised operands of every stage.  A workspace is 16-byte
+ * plus the quantised operands of every stage; MOE_MXFP4 the h that the
+ * gate/up stage hands to the down stage.  A workspace is 16-byte
  * aligned and used by one call at a time: calls that share one must run in
  * order on one stream. */
 MOE_API size_t moe_gemm_workspace_bytes(int dtype, int E, int64_t n_rows, int d, int f);
@@ -170,6 +174,13 @@ MOE_API size_t moe_gemm_workspace_bytes(int dtype, int E, int64_t n_rows, int d,
  * h = silu(g) * u, y = h Wd^T.  Two launches (gate/up with the SwiGLU
  * epilogue, then down); the tile schedule is built on the device from the
  * group offsets, the grid comes from host-known bounds.
+ *
+ * MOE_MXFP4 computes h = bf16(silu(g) * u) and quantises that h to MXFP4
+ * row-wise for the down projection; x_perm, w13 and w2 are codes of two
+ * elements per byte ([n_rows, d/2], [E, 2f, d/2], [E, d, f/2]) with scales of
+ * the shapes below, d and f are multiples of 128 and at most 2^20, and gu and
+ * h may each be NULL (then not written: what a forward without a backward
+ * needs).  An operand row with a NaN scale (255) gives NaN.
  *
  * in   x_perm     [n_rows, d]   (MXFP8: codes, with x_perm_scales [n_rows, d/32])
  * in   w13        [E, 2f, d]: rows 0..f-1 = Wg, f..2f-1 = Wu of each expert
@@ -211,6 +222,10 @@ MOE_API int moe_grouped_gemm_fwd(int dtype, const void* x_perm, const uint8_t* x
  * out  dw13       [E, 2f, d], dw2 [E, d, f].
  * in   ws         workspace of moe_gemm_workspace_bytes() bytes (MOE_BF16 and
  *                 MOE_MXFP8; MOE_EWORKSPACE when missing or smaller).
+ * MOE_MXFP4 has no backward of its own (MOE_EUNSUPPORTED): 4 bits do not hold
+ * gradients.  The gradient of its forward with the quantisers taken as the
+ * identity is the MOE_BF16 backward on moe_dequantize_mxfp4 of x_perm, w13
+ * and w2 (the values are exact in bf16) and the gu, h the forward saved.
  */
 MOE_API int moe_grouped_gemm_bwd(int dtype, const void* dy_perm, const void* x_perm,
                          const uint8_t* x_perm_scales, const void* gu, const void* h,
@@ -222,7 +237,9 @@ MOE_API int moe_grouped_gemm_bwd(int dtype, const void* dy_perm, const void* x_p
 
 /* The grouped GEMM stages: one kernel launch each for MOE_F32 / MOE_BF16;
  * for MOE_MXFP8 the quantisation of the stage's bf16 operands into the
- * workspace, then one block-scaled GEMM launch. */
+ * workspace, then one block-scaled GEMM launch; for MOE_MXFP4 one launch of
+ * GATE_UP or DOWN, which hands h on through the workspace as MOE_MXFP8 does
+ * (DOWN reads that copy, not the h tensor), and no other stage. */
 enum moe_gemm_op {
     MOE_GEMM_GATE_UP = 0,        /* gu = x [Wg | Wu]^T, h = silu(g) * u               */
     MOE_GEMM_DOWN = 1,           /* y = h Wd^T                                        */
@@ -322,6 +339,37 @@ MOE_API int moe_quantize_mxfp8(const void* src, int64_t rows, int K, int colwise
                        uint8_t* scales, moe_stream_t stream);
 
 /*
+ * MXFP4 block quantiser (the OCP microscaling format beside MXFP8): E2M1
+ * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6, with a sign bit above) with one E8M0
+ * scale per 32 elements along K.  scale = 2^e with e the smallest integer
+ * such that block_max / 2^e <= 6 (clamped to [-127, 127]; an all-zero block
+ * gets e = -127), stored as e + 127; codes = round-to-nearest-even(v / 2^e).
+ * E2M1 has no infinity and no NaN: a block with an element that is not finite
+ * gets the NaN scale 255 and zero codes, so that what is computed from it is
+ * NaN rather than an ordinary number.
+ *
+ * in   src        [rows, K] bf16, K a multiple of 32.
+ * out  codes      [rows, K/2]: element 2i of a row in the low four bits of
+ *                 its byte i, element 2i + 1 in the high four.
+ * out  scales     [rows, K/32].
+ * Errors: MOE_EINVAL (sizes, null pointers), MOE_EALIGN (K % 32; src or codes
+ * not 16-byte aligned).
+ */
+MOE_API int moe_quantize_mxfp4(const void* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                       moe_stream_t stream);
+
+/*
+ * The bf16 values of MXFP4 codes, the inverse of moe_quantize_mxfp4:
+ * dst[r, i] = code * 2^(scale - 127), which bf16 holds exactly (a value of
+ * 2^128 or more, possible under scales 253 and 254, is infinite: the largest
+ * bf16 numbers round up to 2^128); the 32 elements of a NaN scale are NaN.
+ * in   codes [rows, K/2], scales [rows, K/32];  out  dst [rows, K] bf16.
+ * Errors as moe_quantize_mxfp4.
+ */
+MOE_API int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* dst,
+                         moe_stream_t stream);
+
+/*
  * Shared experts (the speed-read's training-recipe paragraph, the report's
  * section on the model recipe: ungated experts every token also uses, whose
  * merge with the routed output matters; several of them equal one wider
@@ -391,6 +439,69 @@ MOE_API int moe_gate_grad(const void* dout, const void* y_perm, const int32_t* t
                           const float* topk_w, const int32_t* dst_row, int T, int E, int k, int d,
                           int64_t n_rows, float* dlogits, float* dw, void* dy_perm,
                           int32_t* dev_err, moe_stream_t stream);
+
+/* Bytes of scratch moe_balance_loss needs (0 for invalid sizes). */
+MOE_API size_t moe_balance_workspace_bytes(int T, int E, int n_seg);
+
+/*
+ * The losses that keep a router balanced, and the per-expert counts they are
+ * made of, over the packed sequences of a batch (the pages measure under even
+ * expert load; the losses themselves are the usual ones and the pages do not
+ * spell them out).  With p_t = softmax(logits[t]) over all E experts,
+ * lse_t = log sum_e exp(logits[t, e]), n_s the counted tokens of sequence s
+ * and N = sum_s n_s:
+ *   f_se      = counts[s, e] / sum_j counts[s, j]      (0 for an empty sequence)
+ *   probs_se  = mean over the counted tokens of s of p_te
+ *   losses[0] = balance_coef * E * sum_s (n_s / N) sum_e f_se * probs_se
+ *   losses[1] = z_coef * (1 / N) * sum_t lse_t^2
+ * and both 0 when N = 0.  One sequence (n_seg = 1, seg_off = NULL) gives the
+ * loss over the whole batch; balance_coef * 1 is its value at even load.
+ * in   logits     [T, E] fp32.  A logit that is not finite counts as -infinity
+ *                 (as in the route; flagged); a token with no finite logit
+ *                 has p = 0 and lse = 0.
+ * in   topk_idx   [T, k] from moe_route_topk; an index outside [0, E) counts
+ *                 for no expert.
+ * in   mask       [T] bytes, 0 = padding: not counted, no gradient.  May be NULL.
+ * in   seg_off    [n_seg + 1] device int32, ascending: sequence s owns tokens
+ *                 [seg_off[s], seg_off[s+1]); tokens before the first or behind
+ *                 the last belong to none and are not counted.  NULL: one
+ *                 sequence of all T tokens (n_seg = 1).
+ * out  losses     [2] fp32.
+ * out  counts     [n_seg, E] int32, probs [n_seg, E] fp32.
+ * out  lse        [T] fp32, 0 for tokens not counted.  May be NULL.
+ * out  tokens     [n_seg + 1] int32: n_s, then N.
+ * in   ws         device scratch of moe_balance_workspace_bytes(T, E, n_seg), 16-byte aligned.
+ * out  dev_err    optional; MOE_ERR_NONFINITE_LOGIT.
+ * T = 0 is allowed.  Two kernels.  Errors: MOE_EINVAL (sizes: 1 <= k <= 8,
+ * k <= E <= 1024, 1 <= n_seg <= 2^20, n_seg = 1 without seg_off; null
+ * pointers), MOE_EWORKSPACE.
+ */
+MOE_API int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask,
+                             const int32_t* seg_off, int n_seg, int T, int E, int k, float balance_coef,
+                             float z_coef, float* losses, int32_t* counts, float* probs, float* lse,
+                             int32_t* tokens, void* ws, size_t ws_bytes, int32_t* dev_err, moe_stream_t stream);
+
+/*
+ * Gradient of dlosses[0] * losses[0] + dlosses[1] * losses[1] with respect to
+ * the logits (the counts do not depend on them smoothly and are constants):
+ *   g[t, e] = p_te * (dlosses[0] * balance_coef * E / N * (f_se - sum_j f_sj p_tj)
+ *                     + dlosses[1] * z_coef * 2 / N * lse_t)
+ * and 0 for tokens not counted.
+ * in   logits, mask, seg_off, n_seg, the coefficients: as for the forward.
+ * in   counts, tokens  as the forward wrote them (or summed over the ranks of
+ *                 a data-parallel job: then g is the gradient of the loss of
+ *                 the joint batch, whose p of other ranks is constant here).
+ * in   dlosses    [2] fp32 on the device, or NULL for (1, 1).
+ * in   add        [T, E] fp32 or NULL: dlogits = add + g, for instance the
+ *                 dlogits of moe_gate_grad.  May be dlogits itself.
+ * out  dlogits    [T, E] fp32, every entry written.  Must not overlap logits,
+ *                 and add only as a whole.
+ * One kernel.  Errors: MOE_EINVAL (sizes, null pointers).
+ */
+MOE_API int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, const int32_t* seg_off, int n_seg,
+                                 int T, int E, const int32_t* counts, const int32_t* tokens, float balance_coef,
+                                 float z_coef, const float* dlosses, const float* add, float* dlogits,
+                                 moe_stream_t stream);
 
 /* Static text naming a status code. */
 MOE_API const char* moe_status_string(int status);

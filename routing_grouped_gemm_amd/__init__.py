@@ -15,7 +15,7 @@ import os
 import torch
 
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4, -5
-MOE_F32, MOE_BF16, MOE_MXFP8 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_MXFP8, MOE_MXFP4 = 0, 1, 2, 3
 MOE_ERR_NONFINITE_LOGIT, MOE_ERR_ROW_RANGE = 1, 2
 
 MOE_GEMM_GATE_UP, MOE_GEMM_DOWN, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD = \
@@ -24,8 +24,9 @@ MOE_GEMM_GATE_UP, MOE_GEMM_DOWN, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MO
 ABI_FUNCTIONS = ("moe_route_workspace_bytes", "moe_route_topk", "moe_route_topk_noalloc", "moe_permute",
                  "moe_gemm_workspace_bytes", "moe_grouped_gemm_fwd", "moe_grouped_gemm_bwd",
                  "moe_grouped_gemm_op", "moe_unpermute_combine", "moe_quantize_mxfp8",
-                 "moe_route_add_shared", "moe_router_logits", "moe_gate_grad", "moe_status_string",
-                 "moe_version")
+                 "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_route_add_shared", "moe_router_logits",
+                 "moe_gate_grad", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_bwd",
+                 "moe_status_string", "moe_version")
 
 GEMM_TENSOR_FIELDS = ("x_perm", "x_perm_scales", "w13", "w13_scales", "w2", "w2_scales", "gu",
                       "h", "y_perm", "dy_perm", "dgu", "dx_perm", "dw13", "dw2", "ws")
@@ -91,6 +92,17 @@ def load():
     lib.moe_router_logits.argtypes = [P, P, I, I, I, P, P]
     lib.moe_gate_grad.restype = I
     lib.moe_gate_grad.argtypes = [P, P, P, P, P, I, I, I, I, I64, P, P, P, P, P]
+    F = ctypes.c_float
+    lib.moe_quantize_mxfp4.restype = I
+    lib.moe_quantize_mxfp4.argtypes = [P, I64, I, P, P, P]
+    lib.moe_dequantize_mxfp4.restype = I
+    lib.moe_dequantize_mxfp4.argtypes = [P, P, I64, I, P, P]
+    lib.moe_balance_workspace_bytes.restype = SZ
+    lib.moe_balance_workspace_bytes.argtypes = [I, I, I]
+    lib.moe_balance_loss.restype = I
+    lib.moe_balance_loss.argtypes = [P, P, P, P, I, I, I, I, F, F, P, P, P, P, P, P, SZ, P, P]
+    lib.moe_balance_loss_bwd.restype = I
+    lib.moe_balance_loss_bwd.argtypes = [P, P, P, I, I, I, P, P, F, F, P, P, P, P]
     _lib = lib
     return lib
 
@@ -120,6 +132,27 @@ def _check(rc, name):
 
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _dense(name, t, dtype, *shape):
+    """The data pointer of t (None: NULL) after checking that it is a dense `dtype` tensor
+    of `shape` on a GPU (a -1 in `shape` leaves that size open)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor on the GPU, got {t.dtype} "
+                         f"{tuple(t.shape)} strides {t.stride()} on {t.device}")
+    if len(t.shape) != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on(first, *others):
+    """A guard that makes `first`'s device current, after checking that the other tensors are there too."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return torch.cuda.device(first.device)
 
 
 # ------------------------------------------------------------------ ABI calls
@@ -163,9 +196,14 @@ def moe_route_topk_noalloc(logits, k, capacity, topk_idx, topk_w, counts, offset
 
 def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_perm_scales=None,
                 dev_err=None, stream=None):
-    """x [T, d] -> x_perm [n_rows, d] (MXFP8: codes + x_perm_scales [n_rows, d/32])."""
+    """x [T, d] -> x_perm [n_rows, d] (MXFP8: codes + x_perm_scales [n_rows, d/32]; MXFP4:
+    codes [n_rows, d/2] + x_perm_scales [n_rows, d/32])."""
     T, d = x.shape
     n_rows = x_perm.shape[0]
+    if dtype == MOE_MXFP4:
+        _dense("x", x, torch.bfloat16, T, d)
+        _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2)
+        _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32)
     rc = load().moe_permute(dtype, _p(x), T, d, k, _p(dst_row), _p(src_slot), _p(row_scale),
                             n_rows, _p(x_perm), _p(x_perm_scales), _p(dev_err), _s(stream))
     _check(rc, "moe_permute")
@@ -180,10 +218,24 @@ def moe_grouped_gemm_fwd(dtype, x_perm, w13, w2, group_off, capacity, gu, h, y_p
                          stream=None):
     """x_perm [n_rows, d], w13 [E, 2f, d], w2 [E, d, f] -> gu [n_rows, 2f], h [n_rows, f],
     y_perm [n_rows, d].  group_off [E+1] device int32 (ignored when capacity > 0, but its
-    length still gives E)."""
+    length still gives E).  MXFP4: x_perm, w13 and w2 are codes, two elements per byte, and
+    gu and h may be None (then not written)."""
     E = group_off.numel() - 1
     n_rows, d = x_perm.shape
-    f = h.shape[1]
+    if dtype == MOE_MXFP4:
+        d, f = 2 * d, 2 * w2.shape[-1]
+        _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2)
+        _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32)
+        _dense("w13", w13, torch.uint8, E, 2 * f, d // 2)
+        _dense("w13_scales", w13_scales, torch.uint8, E, 2 * f, d // 32)
+        _dense("w2", w2, torch.uint8, E, d, f // 2)
+        _dense("w2_scales", w2_scales, torch.uint8, E, d, f // 32)
+        _dense("group_off", group_off, torch.int32, E + 1)
+        _dense("gu", gu, torch.bfloat16, n_rows, 2 * f)
+        _dense("h", h, torch.bfloat16, n_rows, f)
+        _dense("y_perm", y_perm, torch.bfloat16, n_rows, d)
+    else:
+        f = h.shape[1]
     rc = load().moe_grouped_gemm_fwd(dtype, _p(x_perm), _p(x_perm_scales), _p(w13),
                                      _p(w13_scales), _p(w2), _p(w2_scales), _p(group_off),
                                      capacity, E, n_rows, d, f, _p(gu), _p(h), _p(y_perm), _p(ws),
@@ -266,6 +318,67 @@ def moe_gate_grad(dout, y_perm, topk_idx, topk_w, dst_row, dlogits, dw=None, dy_
     rc = load().moe_gate_grad(_p(dout), _p(y_perm), _p(topk_idx), _p(topk_w), _p(dst_row), T, E, k, d,
                               n_rows, _p(dlogits), _p(dw), _p(dy_perm), _p(dev_err), _s(stream))
     _check(rc, "moe_gate_grad")
+
+
+def moe_quantize_mxfp4(src, codes, scales, stream=None):
+    """bf16 src [rows, K] -> E2M1 codes [rows, K/2] (element 2i in the low half of byte i) +
+    E8M0 scales [rows, K/32]."""
+    rows, K = src.shape
+    with _on(src, codes, scales):
+        rc = load().moe_quantize_mxfp4(_dense("src", src, torch.bfloat16, rows, K), rows, K,
+                                       _dense("codes", codes, torch.uint8, rows, K // 2),
+                                       _dense("scales", scales, torch.uint8, rows, K // 32), _s(stream))
+    _check(rc, "moe_quantize_mxfp4")
+
+
+def moe_dequantize_mxfp4(codes, scales, dst, stream=None):
+    """MXFP4 codes [rows, K/2] + scales [rows, K/32] -> their values dst [rows, K] bf16."""
+    rows, K = dst.shape
+    with _on(dst, codes, scales):
+        rc = load().moe_dequantize_mxfp4(_dense("codes", codes, torch.uint8, rows, K // 2),
+                                         _dense("scales", scales, torch.uint8, rows, K // 32), rows, K,
+                                         _dense("dst", dst, torch.bfloat16, rows, K), _s(stream))
+    _check(rc, "moe_dequantize_mxfp4")
+
+
+def moe_balance_workspace_bytes(T, E, n_seg=1):
+    return int(load().moe_balance_workspace_bytes(T, E, n_seg))
+
+
+def moe_balance_loss(logits, topk_idx, balance_coef, z_coef, losses, counts, probs, lse, tokens, ws,
+                     seg_off=None, mask=None, dev_err=None, stream=None):
+    """Balance loss and z loss of router logits [T, E] fp32 and topk_idx [T, k] int32 over n_seg
+    packed sequences (seg_off [n_seg+1] int32; None: one sequence), tokens with mask [T] uint8 = 0
+    left out -> losses [2], counts [n_seg, E] int32, probs [n_seg, E], lse [T] (or None),
+    tokens [n_seg+1] int32."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    n_seg = counts.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    with _on(logits, topk_idx, losses, counts, probs, lse, tokens, ws, seg_off, mask, dev_err):
+        rc = load().moe_balance_loss(
+            _dense("logits", logits, f32, T, E), _dense("topk_idx", topk_idx, i32, T, k),
+            _dense("mask", mask, torch.uint8, T), _dense("seg_off", seg_off, i32, n_seg + 1), n_seg, T, E, k,
+            balance_coef, z_coef, _dense("losses", losses, f32, 2), _dense("counts", counts, i32, n_seg, E),
+            _dense("probs", probs, f32, n_seg, E), _dense("lse", lse, f32, T),
+            _dense("tokens", tokens, i32, n_seg + 1), _p(ws), _nbytes(ws), _p(dev_err), _s(stream))
+    _check(rc, "moe_balance_loss")
+
+
+def moe_balance_loss_bwd(logits, counts, tokens, balance_coef, z_coef, dlogits, dlosses=None, add=None,
+                         seg_off=None, mask=None, stream=None):
+    """dlogits [T, E] = add (or 0) + the gradient of <dlosses, losses> (dlosses [2] on the device,
+    None: ones), from counts and tokens as moe_balance_loss wrote them.  add may be dlogits."""
+    T, E = logits.shape
+    n_seg = counts.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    with _on(logits, counts, tokens, dlogits, dlosses, add, seg_off, mask):
+        rc = load().moe_balance_loss_bwd(
+            _dense("logits", logits, f32, T, E), _dense("mask", mask, torch.uint8, T),
+            _dense("seg_off", seg_off, i32, n_seg + 1), n_seg, T, E, _dense("counts", counts, i32, n_seg, E),
+            _dense("tokens", tokens, i32, n_seg + 1), balance_coef, z_coef, _dense("dlosses", dlosses, f32, 2),
+            _dense("add", add, f32, T, E), _dense("dlogits", dlogits, f32, T, E), _s(stream))
+    _check(rc, "moe_balance_loss_bwd")
 
 
 def moe_quantize_mxfp8(src, colwise, codes, scales, group_off=None, n_groups=0, stream=None):

@@ -18,19 +18,24 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
+constexpr int kMaxMx4Width = 1 << 20;
+constexpr int kMaxSequences = 1 << 20;
 
 // common validation of a grouped GEMM shape; returns MOE_OK or an error
 int check_gemm_shape(int dtype, const int32_t* group_off, int capacity, int E, int64_t n_rows,
                      int d, int f)
 {
-    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_MXFP8) return MOE_EUNSUPPORTED;
+    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_MXFP8 && dtype != MOE_MXFP4) return MOE_EUNSUPPORTED;
     if (E < 1 || E > kMaxExperts || n_rows < 0 || n_rows >= kMaxRows || d < 1 || f < 1 ||
         capacity < 0)
         return MOE_EINVAL;
     if (capacity > 0 && (int64_t)E * capacity != n_rows) return MOE_EINVAL;
     if (capacity == 0 && !group_off) return MOE_EINVAL;
-    // MXFP8 GEMMs step K by 128 fp8 (whole 4-byte scale words per row)
-    const int unit = dtype == MOE_MXFP8 ? 128 : (dtype == MOE_F32 ? 4 : 8);
+    // MXFP8 and MXFP4 GEMMs step K by 128 codes (whole 4-byte scale words per row)
+    const bool mx = dtype == MOE_MXFP8 || dtype == MOE_MXFP4;
+    const int unit = mx ? 128 : (dtype == MOE_F32 ? 4 : 8);
+    // (a 128-row tile half's byte offsets stay within 32 bits)
+    if (dtype == MOE_MXFP4 && (d > kMaxMx4Width || f > kMaxMx4Width)) return MOE_EINVAL;
     if (d % unit || f % unit) return MOE_EALIGN;
     if (n_rows * (int64_t)(d > 2 * f ? d : 2 * f) >= ((int64_t)1 << 40)) return MOE_EINVAL;
     return MOE_OK;
@@ -43,6 +48,7 @@ int run_gemm_op(int op, int dtype, const moe_gemm_tensors& t, const GroupSpec& g
     hipError_t e;
     if (dtype == MOE_F32) e = gemm_op_f32(op, t, g, d, f, s);
     else if (dtype == MOE_BF16) e = gemm_op_bf16(op, t, g, d, f, s);
+    else if (dtype == MOE_MXFP4) e = gemm_op_mxfp4(op, t, g, d, f, s);
     else e = gemm_op_mxfp8(op, t, g, d, f, t.ws, s);
     return status_of(e);
 }
@@ -82,7 +88,7 @@ hipError_t scratch_of_current_device(void** out)
 
 extern "C" {
 
-int moe_version(void) { return 100; }
+int moe_version(void) { return 200; }
 
 const char* moe_status_string(int status)
 {
@@ -165,7 +171,7 @@ int moe_permute(int dtype, const void* x, int T, int d, int k, const int32_t* ds
                 const int32_t* src_slot, const float* row_scale, int64_t n_rows, void* x_perm,
                 uint8_t* x_perm_scales, int32_t* dev_err, moe_stream_t stream)
 {
-    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_MXFP8) return MOE_EUNSUPPORTED;
+    if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_MXFP8 && dtype != MOE_MXFP4) return MOE_EUNSUPPORTED;
     if (T < 0 || d < 1 || k < 1 || k > kMaxTopK || n_rows < 0 || n_rows >= kMaxRows)
         return MOE_EINVAL;
     if ((int64_t)T * k >= kMaxRows) return MOE_EINVAL;
@@ -173,10 +179,11 @@ int moe_permute(int dtype, const void* x, int T, int d, int k, const int32_t* ds
     if (T > 0 && (!x || !dst_row)) return MOE_EINVAL;
     if (n_rows > 0 && !x_perm) return MOE_EINVAL;
     if (padded && n_rows > 0 && !src_slot) return MOE_EINVAL;
-    const int unit = dtype == MOE_MXFP8 ? 32 : (dtype == MOE_F32 ? 4 : 8);
+    const bool mx = dtype == MOE_MXFP8 || dtype == MOE_MXFP4;
+    const int unit = mx ? 32 : (dtype == MOE_F32 ? 4 : 8);
     if (d % unit) return MOE_EALIGN;
     if (!aligned16(x) || !aligned16(x_perm)) return MOE_EALIGN;
-    if (dtype == MOE_MXFP8) {
+    if (mx) {
         if (row_scale) return MOE_EUNSUPPORTED;
         if (n_rows > 0 && !x_perm_scales) return MOE_EINVAL;
     }
@@ -203,6 +210,7 @@ size_t moe_gemm_workspace_bytes(int dtype, int E, int64_t n_rows, int d, int f)
 {
     if (E < 1 || n_rows < 0 || d < 1 || f < 1) return 0;
     if (dtype == MOE_BF16) return kGemmCtlBytes;
+    if (dtype == MOE_MXFP4) return gemm_ws_mxfp4(n_rows, f);
     if (dtype != MOE_MXFP8) return 0;
     return gemm_ws_mxfp8(E, n_rows, d, f);
 }
@@ -216,11 +224,15 @@ int moe_grouped_gemm_fwd(int dtype, const void* x_perm, const uint8_t* x_perm_sc
     int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
     if (st != MOE_OK) return st;
     if (!w13 || !w2) return MOE_EINVAL;
-    if (n_rows > 0 && (!x_perm || !gu || !h || !y_perm)) return MOE_EINVAL;
+    const bool need_saved = dtype != MOE_MXFP4;   // MXFP4: gu and h are optional
+    if (n_rows > 0 && (!x_perm || (need_saved && (!gu || !h)) || !y_perm)) return MOE_EINVAL;
     for (const void* p : {x_perm, w13, w2, (const void*)gu, (const void*)h, (const void*)y_perm})
         if (!aligned16(p)) return MOE_EALIGN;
-    if (dtype == MOE_MXFP8) {
-        if (!x_perm_scales || !w13_scales || !w2_scales) return MOE_EINVAL;
+    if (dtype == MOE_MXFP8 || dtype == MOE_MXFP4) {
+        const bool no_rows = dtype == MOE_MXFP4 && n_rows == 0;
+        if ((!x_perm_scales && !no_rows) || !w13_scales || !w2_scales) return MOE_EINVAL;
+        if (dtype == MOE_MXFP4 && (!aligned16(x_perm_scales) || !aligned16(w13_scales) || !aligned16(w2_scales)))
+            return MOE_EALIGN;
         if (!ws || ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(ws))
             return MOE_EWORKSPACE;
     }
@@ -251,6 +263,7 @@ int moe_grouped_gemm_bwd(int dtype, const void* dy_perm, const void* x_perm,
                          int64_t n_rows, int d, int f, void* dgu, void* dx_perm, void* dw13,
                          void* dw2, void* ws, size_t ws_bytes, moe_stream_t stream)
 {
+    if (dtype == MOE_MXFP4) return MOE_EUNSUPPORTED;
     int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
     if (st != MOE_OK) return st;
     if (!w13 || !w2 || !dw13 || !dw2) return MOE_EINVAL;
@@ -292,6 +305,7 @@ int moe_grouped_gemm_op(int op, int dtype, const moe_gemm_tensors* t,
 {
     if (!t) return MOE_EINVAL;
     if (op < MOE_GEMM_GATE_UP || op > MOE_GEMM_WGRAD) return MOE_EINVAL;
+    if (dtype == MOE_MXFP4 && op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return MOE_EUNSUPPORTED;
     int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
     if (st != MOE_OK) return st;
     if (dtype == MOE_MXFP8) {
@@ -300,6 +314,13 @@ int moe_grouped_gemm_op(int op, int dtype, const moe_gemm_tensors* t,
         if ((w13_op && !t->w13_scales) || (w2_op && !t->w2_scales)) return MOE_EINVAL;
         if ((op == MOE_GEMM_GATE_UP || op == MOE_GEMM_WGRAD) && n_rows > 0 && !t->x_perm_scales)
             return MOE_EINVAL;
+        if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
+            return MOE_EWORKSPACE;
+    }
+    if (dtype == MOE_MXFP4) {
+        const uint8_t* ws = op == MOE_GEMM_GATE_UP ? t->w13_scales : t->w2_scales;
+        if (!ws || (op == MOE_GEMM_GATE_UP && n_rows > 0 && !t->x_perm_scales)) return MOE_EINVAL;
+        if (!aligned16(ws) || !aligned16(t->x_perm_scales)) return MOE_EALIGN;
         if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
             return MOE_EWORKSPACE;
     }
@@ -312,6 +333,17 @@ int moe_grouped_gemm_op(int op, int dtype, const moe_gemm_tensors* t,
     case MOE_GEMM_DGRAD_DOWN: need[0] = t->dy_perm; need[1] = t->w2; need[2] = t->gu; need[3] = t->dgu; n = 4; break;
     case MOE_GEMM_DGRAD_GATE_UP: need[0] = t->dgu; need[1] = t->w13; need[2] = t->dx_perm; n = 3; break;
     default: break;
+    }
+    if (dtype == MOE_MXFP4) {
+        // gu and h are optional outputs, and DOWN reads the workspace's h
+        const void* opt[2] = {t->gu, t->h};
+        for (const void* p : opt)
+            if (op == MOE_GEMM_GATE_UP && !aligned16(p)) return MOE_EALIGN;
+        n = 2;
+        if (op == MOE_GEMM_DOWN) {
+            need[0] = t->y_perm;
+            need[1] = t->w2;
+        }
     }
     const bool acc_f32 = t->dw13_f32 || t->dw2_f32;
     if (acc_f32) {
@@ -387,6 +419,55 @@ int moe_quantize_mxfp8(const void* src, int64_t rows, int K, int colwise, const 
     if (K % 8 || (reinterpret_cast<uintptr_t>(scales) & 3u)) return MOE_EALIGN;
     return status_of(launch_quantize_cols((const uint16_t*)src, rows, K, group_off, 0,
                                           group_off ? n_groups : 1, codes, scales, s));
+}
+
+int moe_quantize_mxfp4(const void* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales, moe_stream_t stream)
+{
+    if (rows < 0 || rows >= kMaxRows || K < 1 || rows * (int64_t)K >= ((int64_t)1 << 40)) return MOE_EINVAL;
+    if (rows > 0 && (!src || !codes || !scales)) return MOE_EINVAL;
+    if (K % 32 || !aligned16(src) || !aligned16(codes)) return MOE_EALIGN;
+    return status_of(launch_quantize_rows4((const uint16_t*)src, rows, K, codes, scales, as_stream(stream)));
+}
+
+int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, void* dst,
+                         moe_stream_t stream)
+{
+    if (rows < 0 || rows >= kMaxRows || K < 1 || rows * (int64_t)K >= ((int64_t)1 << 40)) return MOE_EINVAL;
+    if (rows > 0 && (!dst || !codes || !scales)) return MOE_EINVAL;
+    if (K % 32 || !aligned16(dst) || !aligned16(codes)) return MOE_EALIGN;
+    return status_of(launch_dequantize_rows4(codes, scales, rows, K, (uint16_t*)dst, as_stream(stream)));
+}
+
+size_t moe_balance_workspace_bytes(int T, int E, int n_seg)
+{
+    if (T < 0 || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return 0;
+    return balance_ws_bytes(T, E, n_seg);
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask, const int32_t* seg_off,
+                     int n_seg, int T, int E, int k, float balance_coef, float z_coef, float* losses,
+                     int32_t* counts, float* probs, float* lse, int32_t* tokens, void* ws, size_t ws_bytes,
+                     int32_t* dev_err, moe_stream_t stream)
+{
+    if (T < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK || k > E || n_seg < 1 || n_seg > kMaxSequences)
+        return MOE_EINVAL;
+    if ((int64_t)T * k >= kMaxRows || (!seg_off && n_seg != 1)) return MOE_EINVAL;
+    if (T > 0 && (!logits || !topk_idx)) return MOE_EINVAL;
+    if (!losses || !counts || !probs || !tokens) return MOE_EINVAL;
+    if (!ws || ws_bytes < moe_balance_workspace_bytes(T, E, n_seg) || !aligned16(ws)) return MOE_EWORKSPACE;
+    return status_of(launch_balance(logits, topk_idx, mask, seg_off, n_seg, T, E, k, balance_coef, z_coef, losses,
+                                    counts, probs, lse, tokens, ws, dev_err, as_stream(stream)));
+}
+
+int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, const int32_t* seg_off, int n_seg, int T, int E,
+                         const int32_t* counts, const int32_t* tokens, float balance_coef, float z_coef,
+                         const float* dlosses, const float* add, float* dlogits, moe_stream_t stream)
+{
+    if (T < 0 || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return MOE_EINVAL;
+    if (!seg_off && n_seg != 1) return MOE_EINVAL;
+    if (T > 0 && (!logits || !dlogits || !counts || !tokens)) return MOE_EINVAL;
+    return status_of(launch_balance_bwd(logits, mask, seg_off, n_seg, T, E, counts, tokens, balance_coef, z_coef,
+                                        dlosses, add, dlogits, as_stream(stream)));
 }
 
 }  // extern "C"

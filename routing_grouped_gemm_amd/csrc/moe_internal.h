@@ -183,6 +183,23 @@ hipError_t launch_dequant_requant_cols(const uint8_t* codes_row, const uint8_t* 
                                        int capacity, int n_groups, uint8_t* codes,
                                        uint8_t* scales, hipStream_t stream);
 
+// MXFP4
+hipError_t launch_quantize_rows4(const uint16_t* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                                 hipStream_t s);
+hipError_t launch_dequantize_rows4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, uint16_t* dst,
+                                   hipStream_t s);
+hipError_t launch_permute_mx4(const void* x, int T, int d, int k, const int32_t* dst_row, int64_t n_rows,
+                              void* codes, uint8_t* scales, int32_t* dev_err, hipStream_t s);
+
+// balance loss (S sequences)
+size_t balance_ws_bytes(int T, int E, int S);
+hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, const int32_t* seg_off,
+                          int S, int T, int E, int k, float cb, float cz, float* losses, int32_t* counts,
+                          float* probs, float* lse, int32_t* tokens, void* ws, int32_t* dev_err, hipStream_t s);
+hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const int32_t* seg_off, int S, int T, int E,
+                              const int32_t* counts, const int32_t* tokens, float cb, float cz, const float* dlosses,
+                              const float* add, float* dlogits, hipStream_t s);
+
 // router scores and the gradient through the gate weights
 hipError_t launch_router_logits(const uint16_t* x, const uint16_t* w, int T, int E, int d, float* logits,
                                 hipStream_t s);
@@ -191,7 +208,7 @@ hipError_t launch_gate_grad(const void* dout, const void* y_perm, const int32_t*
                             int64_t n_rows, float* dlogits, float* dw, void* dy_perm, int32_t* dev_err,
                             hipStream_t stream);
 
-// grouped GEMMs (bf16 MFMA, fp32 SIMT, MXFP8 MFMA)
+// grouped GEMMs (bf16 MFMA, fp32 SIMT, MXFP8 and MXFP4 MFMA)
 struct GroupSpec {
     const int32_t* group_off;  // [E+1] device, or nullptr with capacity > 0
     int capacity;
@@ -205,5 +222,7 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, in
 size_t gemm_ws_mxfp8(int E, int64_t n_rows, int d, int f);
 hipError_t gemm_op_mxfp8(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f, void* ws,
                          hipStream_t s);
+size_t gemm_ws_mxfp4(int64_t n_rows, int f);
+hipError_t gemm_op_mxfp4(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f, hipStream_t s);
 
 }  // namespace moe

@@ -553,6 +553,14 @@ hipError_t launch_permute(int dtype, const void* x, int T, int d, int k, const i
                           void* x_perm, uint8_t* x_scales, int32_t* dev_err, hipStream_t s)
 {
     const bool padded = n_rows != (int64_t)T * k;
+    if (dtype == MOE_MXFP4) {
+        const hipError_t e = launch_permute_mx4(x, T, d, k, dst_row, n_rows, x_perm, x_scales, dev_err, s);
+        if (e != hipSuccess) return e;
+        if (padded && n_rows > 0)
+            hipLaunchKernelGGL(zero_rows_kernel, dim3((unsigned)((n_rows + 15) / 16)), dim3(256), 0,
+                               s, src_slot, n_rows, d / 32, (uint4*)x_perm, x_scales, d / 32);
+        return hipGetLastError();
+    }
     if (dtype == MOE_MXFP8) {
         const int nb32 = d / 32;
         const int64_t n = (int64_t)T * nb32;

@@ -10,26 +10,35 @@ The backward of the layer with the routing held fixed:
     dy_perm = permute(dout, row_scale = topk_w)     (combine backward)
     dgu, dx_perm, dw13, dw2 = grouped_gemm_bwd(...)
     dx = unpermute_combine(dx_perm, weights = None) (permute backward)
+
+With MXFP4 the forward runs in 4 bits and the backward is the bf16 one on the
+decoded operands (the gradient with every quantiser taken as the identity).
 """
 import torch
 
 from . import (MOE_BF16, MOE_F32, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD,
-               MOE_MXFP8,
-               gemm_tensors, moe_gemm_workspace_bytes, moe_grouped_gemm_bwd, moe_grouped_gemm_fwd,
-               moe_gate_grad, moe_grouped_gemm_op, moe_permute, moe_quantize_mxfp8,
+               MOE_MXFP4, MOE_MXFP8,
+               gemm_tensors, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes,
+               moe_dequantize_mxfp4, moe_gemm_workspace_bytes, moe_grouped_gemm_bwd, moe_grouped_gemm_fwd,
+               moe_gate_grad, moe_grouped_gemm_op, moe_permute, moe_quantize_mxfp4, moe_quantize_mxfp8,
                moe_route_add_shared, moe_route_topk, moe_route_workspace_bytes, moe_router_logits,
                moe_unpermute_combine)
 
-_ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_MXFP8: torch.bfloat16}
+_ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_MXFP8: torch.bfloat16,
+        MOE_MXFP4: torch.bfloat16}
 
 
 class MoELayer:
     """n_shared > 0 adds that many shared experts (ungated, every token, weight
     1) as extra groups E .. E+n_shared-1 of the same grouped GEMM: weights are
     then [E + n_shared, ...] with the shared experts last, and the buffers hold
-    the routed rows followed by n_shared * T shared rows."""
+    the routed rows followed by n_shared * T shared rows.  save=False (MXFP4
+    only) keeps no activations for a backward, as serving wants it."""
 
-    def __init__(self, T, d, E, f, k, dtype=MOE_BF16, capacity=0, device="cuda", n_shared=0):
+    def __init__(self, T, d, E, f, k, dtype=MOE_BF16, capacity=0, device="cuda", n_shared=0, save=True):
+        if not save and dtype != MOE_MXFP4:
+            raise ValueError("save=False: only the MXFP4 forward runs without its saved activations")
+        self.save = save
         self.T, self.d, self.E, self.f, self.k = T, d, E, f, k
         self.dtype, self.capacity, self.device = dtype, capacity, device
         self.S = n_shared
@@ -65,11 +74,14 @@ class MoELayer:
         if dtype == MOE_MXFP8:
             self.x_perm = torch.empty(R, d, dtype=torch.uint8, device=device)
             self.x_perm_scales = torch.empty(R, d // 32, dtype=torch.uint8, device=device)
+        elif dtype == MOE_MXFP4:
+            self.x_perm = torch.empty(R, d // 2, dtype=torch.uint8, device=device)
+            self.x_perm_scales = torch.empty(R, d // 32, dtype=torch.uint8, device=device)
         else:
             self.x_perm = torch.empty(R, d, dtype=act, device=device)
             self.x_perm_scales = None
-        self.gu = torch.empty(R, 2 * f, dtype=act, device=device)
-        self.h = torch.empty(R, f, dtype=act, device=device)
+        self.gu = torch.empty(R, 2 * f, dtype=act, device=device) if save else None
+        self.h = torch.empty(R, f, dtype=act, device=device) if save else None
         self.y_perm = torch.empty(R, d, dtype=act, device=device)
         self.out = torch.empty(T, d, dtype=act, device=device)
         self.gemm_ws = None
@@ -81,6 +93,8 @@ class MoELayer:
     def _alloc_bwd(self):
         if self._bwd_alloc:
             return
+        if not self.save:
+            raise RuntimeError("a layer made with save=False has no backward")
         R, d, f, E = self.n_rows, self.d, self.f, self.G
         act = _ACT[self.dtype]
         dev = self.device
@@ -90,14 +104,36 @@ class MoELayer:
         self.dx = torch.empty(self.T, d, dtype=act, device=dev)
         self.dw13 = torch.empty(E, 2 * f, d, dtype=act, device=dev)
         self.dw2 = torch.empty(E, d, f, dtype=act, device=dev)
+        if self.dtype == MOE_MXFP4:   # the decoded operands of the bf16 backward, and its workspace
+            self.x_perm_d = torch.empty(R, d, dtype=act, device=dev)
+            self.w13_d = torch.empty(E, 2 * f, d, dtype=act, device=dev)
+            self.w2_d = torch.empty(E, d, f, dtype=act, device=dev)
+            self._decode_weights()
+            self.bwd_ws = torch.empty(moe_gemm_workspace_bytes(MOE_BF16, E, R, d, f), dtype=torch.uint8,
+                                      device=dev)
         self._bwd_alloc = True
+
+    def _decode_weights(self):
+        E, f, d = self.G, self.f, self.d
+        moe_dequantize_mxfp4(self.w13_q.view(E * 2 * f, -1), self.w13_s.view(E * 2 * f, -1),
+                             self.w13_d.view(E * 2 * f, d))
+        moe_dequantize_mxfp4(self.w2_q.view(E * d, -1), self.w2_s.view(E * d, -1), self.w2_d.view(E * d, f))
 
     # -------------------------------------------------------------- weights
     def set_weights(self, w13, w2):
         """Weights [E, 2f, d] and [E, d, f] (fp32 or bf16).  For MXFP8 the forward
-        and backward MXFP8 caches are made here (once per optimizer step)."""
+        and backward MXFP8 caches are made here (once per optimizer step), for
+        MXFP4 the codes of both."""
         self.w13, self.w2 = w13, w2
         self._stages = None
+        if self.dtype == MOE_MXFP4:
+            E, f, d = self.G, self.f, self.d
+            u8 = dict(dtype=torch.uint8, device=self.device)
+            self.set_weights_mxfp4(torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
+                                   torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8),
+                                   decode=False)
+            self.requantize_weights()
+            return
         if self.dtype != MOE_MXFP8:
             return
         E, f, d = self.G, self.f, self.d
@@ -120,10 +156,28 @@ class MoELayer:
         self.w2t_s = torch.empty(n2 // 32, **u8)
         self.requantize_weights()
 
+    def set_weights_mxfp4(self, w13_q, w13_s, w2_q, w2_s, decode=True):
+        """MXFP4: weights that are held in 4 bits already, codes [E, 2f, d/2] and [E, d, f/2]
+        with scales [E, 2f, d/32] and [E, d, f/32] (as moe_quantize_mxfp4 makes them)."""
+        if self.dtype != MOE_MXFP4:
+            raise ValueError("set_weights_mxfp4 needs an MXFP4 layer")
+        self.w13_q, self.w13_s, self.w2_q, self.w2_s = w13_q, w13_s, w2_q, w2_s
+        self._stages = None
+        if decode and self._bwd_alloc:
+            self._decode_weights()
+
     def requantize_weights(self):
         """MXFP8: rebuild the four weight caches (forward and backward direction
-        of w13 and w2) from the bf16 weights in place, as an optimizer step does."""
+        of w13 and w2) from the bf16 weights in place, as an optimizer step does.
+        MXFP4: rebuild the codes."""
         E, f, d = self.G, self.f, self.d
+        if self.dtype == MOE_MXFP4:
+            moe_quantize_mxfp4(self.w13.reshape(E * 2 * f, d), self.w13_q.view(E * 2 * f, -1),
+                               self.w13_s.view(E * 2 * f, -1))
+            moe_quantize_mxfp4(self.w2.reshape(E * d, f), self.w2_q.view(E * d, -1), self.w2_s.view(E * d, -1))
+            if self._bwd_alloc:
+                self._decode_weights()
+            return
         moe_quantize_mxfp8(self.w13.reshape(E * 2 * f, d), 0, self.w13_q, self.w13_s)
         moe_quantize_mxfp8(self.w2.reshape(E * d, f), 0, self.w2_q, self.w2_s)
         moe_quantize_mxfp8(self.w13.reshape(E * 2 * f, d), 1, self.w13t_q, self.w13t_s, self._g13, E)
@@ -133,10 +187,17 @@ class MoELayer:
     def _stage_tensors(self):
         """Operands of the five grouped GEMM stages: (forward-direction set,
         backward-direction set); they differ only in the MXFP8 weight caches."""
+        if not self.save:
+            t = dict(x_perm=self.x_perm, x_perm_scales=self.x_perm_scales, y_perm=self.y_perm, ws=self.gemm_ws)
+            return gemm_tensors(w13=self.w13_q, w13_scales=self.w13_s, w2=self.w2_q, w2_scales=self.w2_s, **t), None
         self._alloc_bwd()
         common = dict(x_perm=self.x_perm, x_perm_scales=self.x_perm_scales, gu=self.gu, h=self.h,
                       y_perm=self.y_perm, dy_perm=self.dy_perm, dgu=self.dgu, dx_perm=self.dx_perm,
                       dw13=self.dw13, dw2=self.dw2, ws=self.gemm_ws)
+        if self.dtype == MOE_MXFP4:
+            fwd = gemm_tensors(w13=self.w13_q, w13_scales=self.w13_s, w2=self.w2_q, w2_scales=self.w2_s, **common)
+            common.update(x_perm=self.x_perm_d, x_perm_scales=None, ws=self.bwd_ws)
+            return fwd, gemm_tensors(w13=self.w13_d, w2=self.w2_d, **common)
         if self.dtype != MOE_MXFP8:
             t = gemm_tensors(w13=self.w13, w2=self.w2, **common)
             return t, t
@@ -153,17 +214,27 @@ class MoELayer:
         if getattr(self, "_stages", None) is None:
             self._stages = self._stage_tensors()
         bwd = op in (MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP)
-        moe_grouped_gemm_op(op, self.dtype, self._stages[1 if bwd else 0], self.s_off,
+        dtype = self.dtype
+        if dtype == MOE_MXFP4 and (bwd or op == MOE_GEMM_WGRAD):
+            self._alloc_bwd()
+            bwd, dtype = True, MOE_BF16
+            if op == MOE_GEMM_WGRAD:
+                self._decode_rows()
+        moe_grouped_gemm_op(op, dtype, self._stages[1 if bwd else 0], self.s_off,
                             self.g_cap, self.G, self.n_rows, self.d, self.f)
 
+    def _decode_rows(self):
+        moe_dequantize_mxfp4(self.x_perm, self.x_perm_scales, self.x_perm_d)
+
     def wgrad_accumulate(self, dw13_f32, dw2_f32):
-        """bf16: the weight-gradient stage adding into fp32 accumulators
+        """bf16 and MXFP4: the weight-gradient stage adding into fp32 accumulators
         (dw13_f32 += dgu^T x_perm, dw2_f32 += dy_perm^T h, per expert) instead
         of writing the bf16 dw13 / dw2.  Call after backward (it reads dgu)."""
         self._alloc_bwd()
-        t = gemm_tensors(x_perm=self.x_perm, h=self.h, dy_perm=self.dy_perm, dgu=self.dgu,
-                         dw13_f32=dw13_f32, dw2_f32=dw2_f32, ws=self.gemm_ws)
-        moe_grouped_gemm_op(MOE_GEMM_WGRAD, self.dtype, t, self.s_off, self.g_cap, self.G,
+        mx4 = self.dtype == MOE_MXFP4
+        t = gemm_tensors(x_perm=self.x_perm_d if mx4 else self.x_perm, h=self.h, dy_perm=self.dy_perm,
+                         dgu=self.dgu, dw13_f32=dw13_f32, dw2_f32=dw2_f32, ws=self.bwd_ws if mx4 else self.gemm_ws)
+        moe_grouped_gemm_op(MOE_GEMM_WGRAD, MOE_BF16 if mx4 else self.dtype, t, self.s_off, self.g_cap, self.G,
                             self.n_rows, self.d, self.f)
 
     # -------------------------------------------------------------- steps
@@ -180,7 +251,7 @@ class MoELayer:
                     x_perm_scales=self.x_perm_scales, dev_err=self.dev_err)
 
     def gemm_fwd(self):
-        if self.dtype == MOE_MXFP8:
+        if self.dtype in (MOE_MXFP8, MOE_MXFP4):
             moe_grouped_gemm_fwd(self.dtype, self.x_perm, self.w13_q, self.w2_q, self.s_off,
                                  self.g_cap, self.gu, self.h, self.y_perm,
                                  x_perm_scales=self.x_perm_scales, w13_scales=self.w13_s,
@@ -216,6 +287,36 @@ class MoELayer:
                       dev_err=self.dev_err)
         return self.dlogits
 
+    def balance_loss(self, logits, balance_coef, z_coef=0.0, seg_off=None, mask=None):
+        """losses [2] fp32 on the device: the balance loss and the z loss of the router's
+        logits under the last route, over the packed sequences seg_off [n_seg+1] int32
+        (None: the batch as one), tokens with mask [T] uint8 = 0 left out.  The counts
+        and mean probabilities per sequence stay in balance_counts, balance_probs."""
+        n = 1 if seg_off is None else seg_off.numel() - 1
+        if getattr(self, "balance_counts", None) is None or self.balance_counts.shape[0] != n:
+            dev = self.device
+            self.balance_losses = torch.empty(2, dtype=torch.float32, device=dev)
+            self.balance_counts = torch.empty(n, self.E, dtype=torch.int32, device=dev)
+            self.balance_probs = torch.empty(n, self.E, dtype=torch.float32, device=dev)
+            self.balance_tokens = torch.empty(n + 1, dtype=torch.int32, device=dev)
+            self.balance_ws = torch.empty(moe_balance_workspace_bytes(self.T, self.E, n), dtype=torch.uint8,
+                                          device=dev)
+        moe_balance_loss(logits, self.topk_idx, balance_coef, z_coef, self.balance_losses, self.balance_counts,
+                         self.balance_probs, None, self.balance_tokens, self.balance_ws, seg_off=seg_off, mask=mask,
+                         dev_err=self.dev_err)
+        self._balance = (balance_coef, z_coef, seg_off, mask)
+        return self.balance_losses
+
+    def balance_loss_grad(self, logits, dlosses=None, add_to=None):
+        """dlogits [T, E]: add_to (the layer's dlogits after gate_grad, say; None: zeros) plus
+        the gradient of <dlosses, losses> of the last balance_loss."""
+        cb, cz, seg_off, mask = self._balance
+        if getattr(self, "dlogits", None) is None:
+            self.dlogits = torch.empty(self.T, self.E, dtype=torch.float32, device=logits.device)
+        moe_balance_loss_bwd(logits, self.balance_counts, self.balance_tokens, cb, cz, self.dlogits,
+                             dlosses=dlosses, add=add_to, seg_off=seg_off, mask=mask)
+        return self.dlogits
+
     def forward(self, logits, x, weights=None):
         self.route(logits)
         self.permute(x)
@@ -234,6 +335,11 @@ class MoELayer:
                                  self.dx_perm, self.dw13, self.dw2,
                                  x_perm_scales=self.x_perm_scales, w13_scales=self.w13t_s,
                                  w2_scales=self.w2t_s, ws=self.gemm_ws)
+        elif self.dtype == MOE_MXFP4:
+            self._decode_rows()
+            moe_grouped_gemm_bwd(MOE_BF16, self.dy_perm, self.x_perm_d, self.gu, self.h, self.w13_d, self.w2_d,
+                                 self.s_off, self.g_cap, self.dgu, self.dx_perm, self.dw13, self.dw2,
+                                 ws=self.bwd_ws)
         else:
             moe_grouped_gemm_bwd(self.dtype, self.dy_perm, self.x_perm, self.gu, self.h,
                                  self.w13, self.w2, self.s_off, self.g_cap, self.dgu,

@@ -204,7 +204,7 @@ def _run_own(s):
                        s["tokens"], s["ws"], seg_off=seg, mask=s["mask"])
     out = [s["losses"], s["counts"], s["probs"], s["lse"], s["tokens"]]
     if c["grad"]:
-        m.moe_balance_loss_bwd(s["logits"], s["lse"], s["counts"], s["tokens"], BALANCE, Z, s["dlogits"],
+        m.moe_balance_loss_bwd(s["logits"], s["counts"], s["tokens"], BALANCE, Z, s["dlogits"],
                                dlosses=s["dlosses"], add=s["before"], seg_off=seg, mask=s["mask"])
         out.append(s["dlogits"])
     return out

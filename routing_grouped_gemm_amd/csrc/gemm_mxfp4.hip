@@ -61,12 +61,67 @@ __device__ __forceinline__ f32x16 mfma4(i32x8 b, i32x8 a, f32x16 acc, uint32_t s
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc, 4, 4, SEL, (int)sb, SEL, (int)sa);
 }
 
-// BM x 256 tile, two LDS stages of codes, scales read from memory
+// LDS: stages of codes, then two stages of scales.  A scale stage holds 16
+// bytes of every operand row (512 codes, two K-steps), A rows first: read a
+// K-step at a time, 4 bytes per 128 codes, every row would cost a cache line
+// per K-step, as much traffic as the codes.  The loads of a row's last 16
+// bytes may run into the next row (never multiplied) or past the descriptor's
+// range, where each 4-byte word by itself reads zero (checked on the hardware).
+constexpr int SROWS = 512;
+constexpr int SSTAGE = SROWS * 16;
+
+// this wave's 64 rows of a scale stage: rows 64 w .. 64 w + 63 of A's BM rows
+// followed by B's 256
+template <int BM>
+struct ScaleLoader4 {
+    desc_t d;
+    uint32_t off;
+    uint32_t lds;     // LDS byte address of the wave's rows in stage 0
+    __device__ __forceinline__ void init(const Src4& a, const Src4& b, uint32_t lds_scales)
+    {
+        const int lane = threadIdx.x & 63;
+        const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int row = w * 64;
+        const int ld = a.K / 32;
+        const bool isb = row >= BM;
+        const int r = isb ? row - BM : row;
+        // a 64-row A tile keeps its two 32-row halves in one wave's rows: they are consecutive in memory
+        const int half = BM == 64 && !isb ? 64 : (isb ? 128 : BM / 2);
+        const bool hi = r >= half;
+        const uint8_t* base = isb ? (hi ? b.s1 : b.s0) : (hi ? a.s1 : a.s0);
+        const int rows = isb ? (hi ? b.rows1 : b.rows0) : (BM == 64 ? a.rows0 + a.rows1 : (hi ? a.rows1 : a.rows0));
+        const bool none = row >= BM + BN;
+        d = wave_uniform(make_desc(base, none ? 0 : (int64_t)rows * ld));
+        off = none ? kOOB : (uint32_t)((r - (hi ? half : 0) + lane) * ld);
+        lds = lds_scales + (uint32_t)row * 16u;
+    }
+    // chunk c (two K-steps) into its stage; outside: zeros
+    __device__ __forceinline__ void issue(int c, bool inside = true)
+    {
+        dma16_to_lds_at(d, lds + (uint32_t)(c & 1) * SSTAGE, off, inside ? (uint32_t)c * 16u : d[2]);
+    }
+};
+
+// the scale word of half K-step hs (128 k) of scale-stage row `row`, shifted
+// so that bytes 0 and 2 are this lane's k-blocks of its two k-slices
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* scales, int row, int hs, int lane)
+{
+    return *reinterpret_cast<const uint32_t*>(scales + ((hs >> 2) & 1) * SSTAGE + (row + (lane & 31)) * 16 + (hs & 3) * 4);
+}
+
+// BM x 256 tile (BM = 64, 128: the tail tiles) through a ring of three LDS
+// stages: the loads of K-step kt + 2 go out while K-step kt's MFMAs run, also
+// past the end of K, where they write zeros to a stage nobody reads, so that
+// the wait at each K-step counts a known number of younger operations.
 template <int BM>
 __device__ __forceinline__ void mainloop4(const Src4& sa, const Src4& sb, f32x16 (&acc)[BM / 64][2], uint8_t* smem)
 {
-    constexpr int MI = BM / 64, NJ = 2;
+    constexpr int MI = BM / 64, NJ = 2, NS = 3;
     constexpr int STAGE = (BM + BN) * 128;
+    using LA = DirectLoader<BM, 64, false, NW4>;
+    using LB = DirectLoader<BN, 64, false, NW4>;
+    constexpr int NQ = LA::PER_WAVE + LB::PER_WAVE;
+    uint8_t* scales = smem + NS * STAGE;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int wm = WL<NW4>::wm(wave), wn = WL<NW4>::wn(wave);
 #pragma unroll
@@ -76,54 +131,314 @@ __device__ __forceinline__ void mainloop4(const Src4& sa, const Src4& sb, f32x16
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     const int nk = (sa.K + KB - 1) / KB;
-    if (nk == 0) return;
-    DirectLoader<BM, 64, false, NW4> la;
-    DirectLoader<BN, 64, false, NW4> lb;
-    la.init(codes_as_tile(sa));
-    lb.init(codes_as_tile(sb));
-    auto issue = [&](int kt, int stage) {
-        la.issue(reinterpret_cast<uint16_t*>(smem + stage * STAGE), kt);
-        lb.issue(reinterpret_cast<uint16_t*>(smem + stage * STAGE + BM * 128), kt);
+    LA la;
+    LB lb;
+    ScaleLoader4<BM> sc;
+    la.init(codes_as_tile(sa), lds_addr(smem));
+    lb.init(codes_as_tile(sb), lds_addr(smem + BM * 128));
+    sc.init(sa, sb, lds_addr(scales));
+    auto issue = [&](int kt) __attribute__((always_inline)) {
+        const bool inside = kt < nk;
+        const uint32_t so = (uint32_t)(kt % NS) * STAGE;
+        if ((kt & 1) == 0) sc.issue(kt >> 1, inside);
+#pragma unroll
+        for (int q = 0; q < LA::PER_WAVE; ++q) la.issue_ring(so, kt, q, inside);
+#pragma unroll
+        for (int q = 0; q < LB::PER_WAVE; ++q) lb.issue_ring(so, kt, q, inside);
     };
-    // a row's scale word (128 k), 0 outside the operand
-    auto scale_word = [&](const Src4& s, int row, int half, int w) {
-        const bool hi = row >= half;
-        const int r = hi ? row - half : row;
-        return r < (hi ? s.rows1 : s.rows0) && w * 128 < s.K
-                   ? *reinterpret_cast<const uint32_t*>((hi ? s.s1 : s.s0) + (int64_t)r * (s.K / 32) + w * 4) : 0u;
-    };
-    issue(0, 0);
+#pragma unroll
+    for (int j = 0; j < NS - 1; ++j) issue(j);
     for (int kt = 0; kt < nk; ++kt) {
-        wait_vmcnt<0>();
+        // younger operations: K-step kt + 1's, with a scale load when it is even
+        if (kt & 1) wait_vmcnt<NQ + 1>();
+        else wait_vmcnt<NQ>();
         __syncthreads();
-        if (kt + 1 < nk) issue(kt + 1, (kt + 1) & 1);
-        const uint8_t* a_s = smem + (kt & 1) * STAGE;
+        issue(kt + NS - 1);
+        const uint8_t* a_s = smem + (kt % NS) * STAGE;
         const uint8_t* b_s = a_s + BM * 128;
-        for (int hs = 0; hs < 2 && kt * KB + hs * 128 < sa.K; ++hs) {
+        auto half = [&](int h) __attribute__((always_inline)) {
+            const int hs = kt * 2 + h;
             uint32_t wa[MI], wb[NJ];
 #pragma unroll
             for (int i = 0; i < MI; ++i)
-                wa[i] = scale_word(sa, wm * (BM / 2) + i * 32 + (lane & 31), BM / 2, kt * 2 + hs) >> (8 * (lane >> 5));
+                wa[i] = scale_word(scales, wm * (BM / 2) + i * 32, hs, lane) >> (8 * (lane >> 5));
 #pragma unroll
             for (int j = 0; j < NJ; ++j)
-                wb[j] = scale_word(sb, WL<NW4>::sub_col(wn, j) + (lane & 31), 128, kt * 2 + hs) >> (8 * (lane >> 5));
+                wb[j] = scale_word(scales, BM + WL<NW4>::sub_col(wn, j), hs, lane) >> (8 * (lane >> 5));
+            i32x8 af[2][MI], bf[2][NJ];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                i32x8 af[MI], bf[NJ];
 #pragma unroll
-                for (int i = 0; i < MI; ++i) af[i] = read_frag4(a_s, wm * (BM / 2) + i * 32, hs * 2 + q, lane);
+                for (int i = 0; i < MI; ++i) af[q][i] = read_frag4(a_s, wm * (BM / 2) + i * 32, h * 2 + q, lane);
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) bf[j] = read_frag4(b_s, WL<NW4>::sub_col(wn, j), hs * 2 + q, lane);
-#pragma unroll
-                for (int i = 0; i < MI; ++i)
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j)
-                        acc[i][j] = q ? mfma4<2>(bf[j], af[i], acc[i][j], wb[j], wa[i])
-                                      : mfma4<0>(bf[j], af[i], acc[i][j], wb[j], wa[i]);
+                for (int j = 0; j < NJ; ++j) bf[q][j] = read_frag4(b_s, WL<NW4>::sub_col(wn, j), h * 2 + q, lane);
             }
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = mfma4<0>(bf[0][j], af[0][i], acc[i][j], wb[j], wa[i]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = mfma4<2>(bf[1][j], af[1][i], acc[i][j], wb[j], wa[i]);
+        };
+        half(0);
+        if (kt * KB + 128 < sa.K) half(1);
+    }
+    wait_vmcnt<0>();   // the zero loads past K have landed too
+    __syncthreads();
+}
+
+// this wave's direct loads of half of a 256-row operand tile: 1 KB chunks
+// half*16 + 4i + w4, i = 0..3, of the 32 of a K-step
+struct HalfLoader4 {
+    desc_t d;
+    uint32_t off[4];
+    uint32_t m0w;
+    __device__ __forceinline__ void init(const Src4& s, uint32_t lds_tile, int half, int w4)
+    {
+        const int lane = threadIdx.x & 63;
+        m0w = lds_tile + (uint32_t)(half * 16 + w4) * 1024u;
+        d = wave_uniform(half ? make_desc(s.c1, (int64_t)s.rows1 * (s.K / 2)) : make_desc(s.c0, (int64_t)s.rows0 * (s.K / 2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = (half * 16 + i * 4 + w4) * 8 + lane / 8;
+            off[i] = (uint32_t)((row - half * 128) * (s.K / 2)) + lds_chunk<false, 64>(row, lane % 8) * 16u;
         }
     }
+    __device__ __forceinline__ void issue(uint32_t stage_off, int kt)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dma16_to_lds_at(d, m0w + stage_off + (uint32_t)i * 4096u, off[i], (uint32_t)kt * 128u);
+    }
+};
+
+// Ping-pong main loop of a 256 x 256 tile: the two waves of a SIMD belong to
+// different groups (waves 0..3: tile rows 0..127, waves 4..7: rows 128..255)
+// that alternate, tick by tick, between a compute tick (the 16 MFMAs of a half
+// K-step from registers, with the next half's 12 fragments and 6 scale words
+// read from LDS in their shadow) and a memory tick (this wave's 4 direct loads
+// of a quarter of a K-step); group 1 runs one tick behind group 0 and a
+// barrier ends every tick, so on every SIMD one wave feeds the matrix unit
+// while the other issues loads.  An MXFP4 fragment is 16 bytes per lane, as a
+// bf16 one is, and its MFMA as long, so the schedule is the bf16 kernels':
+// the quarters of K-step j (two LDS stages) go out at ticks 4j-7 (A rows
+// 0..127, group 0), 4j-6 (B half 0, group 1), 4j-5 (B half 1, group 0) and
+// 4j-4 (A rows 128..255, group 1); group 0 reads K-step j at ticks 4j-2 and
+// 4j, group 1 at 4j-1 and 4j+1.  The scales of K-steps 2c, 2c+1 go out ahead
+// of the first quarter a group loads of K-step 2c (A's at tick 8c-7 by group
+// 0, B's at 8c-6 by group 1), after the last read of their stage (8c-11).
+// When K is an odd multiple of 128, the last half K-step is loaded and read
+// like any other and its MFMAs are left out.
+__device__ __forceinline__ void mainloop4_pp(const Src4& sa, const Src4& sb, f32x16 (&acc)[4][2], uint8_t* smem)
+{
+    constexpr int BM = 256, MI = 4, NJ = 2;
+    constexpr int STAGE = (BM + BN) * 128;
+    uint8_t* scales = smem + 2 * STAGE;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = wave >> 2;    // group
+    const int w4 = wave & 3;    // wave column (and SIMD)
+    const int sh = 8 * (lane >> 5);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    const int nk = (sa.K + KB - 1) / KB;
+    const int H = 2 * nk;       // half K-steps
+    const bool whole = sa.K % KB == 0;
+    HalfLoader4 ha, hb;
+    ScaleLoader4<BM> sc;
+    ha.init(sa, lds_addr(smem), g, w4);
+    hb.init(sb, lds_addr(smem + BM * 128), 1 - g, w4);
+    sc.init(sa, sb, lds_addr(scales));
+    sc.issue(0);
+    ha.issue(0, 0);
+    hb.issue(0, 0);
+    if (nk > 1) {
+        ha.issue(STAGE, 1);
+        hb.issue(STAGE, 1);
+        wait_vmcnt<8>();
+    } else {
+        wait_vmcnt<0>();
+    }
     __syncthreads();
+
+    // fragments of one 64-deep k-slice: 4 A sub-tiles, 2 B sub-tiles
+    struct Slot {
+        i32x8 a[MI], b[NJ];
+    };
+    struct Words {
+        uint32_t a[MI], b[NJ];
+    };
+    // fragment m (A 0..3, B 4..5) of k-slice s2 of half K-step hs
+    auto read_one = [&](int hs, int s2, int m, Slot& dst) __attribute__((always_inline)) {
+        const uint8_t* a_s = smem + ((hs >> 1) & 1) * STAGE;
+        const int ks = (hs & 1) * 2 + s2;
+        if (m < MI) dst.a[m] = read_frag4(a_s, g * 128 + m * 32, ks, lane);
+        else dst.b[m - MI] = read_frag4(a_s + BM * 128, WL<8>::sub_col(w4, m - MI), ks, lane);
+    };
+    auto read_word = [&](int hs, int m, Words& w) __attribute__((always_inline)) {
+        if (m < MI) w.a[m] = scale_word(scales, g * 128 + m * 32, hs, lane);
+        else w.b[m - MI] = scale_word(scales, BM + WL<8>::sub_col(w4, m - MI), hs, lane);
+    };
+    // the 16 MFMAs of k-slices p (first) and c1 (second) under the scale words
+    // w; with RD, what half K-step hs needs: its second k-slice into n1 and
+    // its scale words into wn during the first 8 MFMAs, its first k-slice into
+    // p (free by then) during the last 8
+    auto compute = [&](auto RD, int hs, Slot& p, Slot& c1, Slot& n1, Words& w, Words& wn) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < MI; ++m) w.a[m] >>= sh;
+#pragma unroll
+        for (int m = 0; m < NJ; ++m) w.b[m] >>= sh;
+        __builtin_amdgcn_s_setprio(1);   // ahead of the memory-phase wave of this SIMD
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+            const int i = (n >> 1) & 3, j = n & 1;
+            if (n < 8) acc[i][j] = mfma4<0>(p.b[j], p.a[i], acc[i][j], w.b[j], w.a[i]);
+            else acc[i][j] = mfma4<2>(c1.b[j], c1.a[i], acc[i][j], w.b[j], w.a[i]);
+            if constexpr (decltype(RD)::value) {
+                if (n < 6) read_one(hs, 1, n, n1);
+                else if (n < 8) {
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) read_word(hs, (n - 6) * 3 + m, wn);
+                } else if (n < 14) read_one(hs, 0, n - 8, p);
+            }
+        }
+        if constexpr (decltype(RD)::value) {
+#pragma unroll
+            for (int n = 0; n < 6; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+            }
+#pragma unroll
+            for (int n = 0; n < 6; ++n) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        }
+        // the MFMAs belong to this tick: the compiler would sink some of them
+        // past the barrier into the next one (with 190 spilled registers)
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
+        __builtin_amdgcn_s_setprio(0);
+    };
+    // this wave's direct loads of memory tick t
+    auto loads = [&](int t) __attribute__((always_inline)) {
+        int j;
+        if (g == 0) {
+            if ((t & 3) == 1) {          // A half 0 of K-step j, the A scales of K-steps j, j + 1
+                j = (t + 7) >> 2;
+                if (j >= 2 && j < nk) {
+                    if ((j & 1) == 0) sc.issue(j >> 1);
+                    ha.issue((uint32_t)(j & 1) * STAGE, j);
+                }
+            } else {                     // t % 4 == 3: B half 1
+                j = (t + 5) >> 2;
+                if (j >= 2 && j < nk) hb.issue((uint32_t)(j & 1) * STAGE, j);
+            }
+        } else {
+            if ((t & 3) == 2) {          // B half 0 of K-step j, the B scales of K-steps j, j + 1
+                j = (t + 6) >> 2;
+                if (j >= 2 && j < nk) {
+                    if ((j & 1) == 0) sc.issue(j >> 1);
+                    hb.issue((uint32_t)(j & 1) * STAGE, j);
+                }
+            } else {                     // t % 4 == 0: A half 1
+                j = (t + 4) >> 2;
+                if (j >= 2 && j < nk) ha.issue((uint32_t)(j & 1) * STAGE, j);
+            }
+        }
+    };
+    // end of tick t: what the next tick reads has landed, then the barrier.
+    // What was issued this tick (or, for group 1 at t % 4 == 1, the tick
+    // before) may stay in flight: 4 loads, and the scales ahead of them when
+    // they went out this tick
+    auto end_tick = [&](int t) __attribute__((always_inline)) {
+        if ((t & 3) == 1) {
+            const int j = (t + 3) >> 2;
+            const int jn = g == 0 ? j + 1 : j;
+            if (jn < 2 || jn >= nk) wait_vmcnt<0>();
+            else if (g == 0 && (jn & 1) == 0) wait_vmcnt<5>();
+            else wait_vmcnt<4>();
+        } else if ((t & 3) == 2 && g == 1) {
+            const int jn = ((t + 2) >> 2) + 1;
+            if (jn < 2 || jn >= nk) wait_vmcnt<0>();
+            else if ((jn & 1) == 0) wait_vmcnt<5>();
+            else wait_vmcnt<4>();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const std::integral_constant<bool, true> rd;
+    const std::integral_constant<bool, false> no_rd;
+    Slot sp, sq, sr;   // first k-slice; second k-slice, alternating between sq and sr
+    Words wq, wr;
+    auto read_all = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < 6; ++m) read_one(0, 0, m, sp);
+#pragma unroll
+        for (int m = 0; m < 6; ++m) read_one(0, 1, m, sq);
+#pragma unroll
+        for (int m = 0; m < 6; ++m) read_word(0, m, wq);
+    };
+
+    if (g == 0) {
+        read_all();
+        int u = 0;
+        for (; u + 2 < H; u += 2) {
+            compute(rd, u + 1, sp, sq, sr, wq, wr);              // tick 2u
+            end_tick(2 * u);
+            loads(2 * u + 1);                                    // tick 2u+1
+            end_tick(2 * u + 1);
+            compute(rd, u + 2, sp, sr, sq, wr, wq);              // tick 2u+2
+            end_tick(2 * u + 2);
+            loads(2 * u + 3);                                    // tick 2u+3
+            end_tick(2 * u + 3);
+        }
+        compute(rd, u + 1, sp, sq, sr, wq, wr);                  // tick 2H-4
+        end_tick(2 * u);
+        loads(2 * u + 1);
+        end_tick(2 * u + 1);
+        if (whole) compute(no_rd, 0, sp, sr, sq, wr, wq);        // tick 2H-2
+        end_tick(2 * u + 2);
+        loads(2 * u + 3);
+        end_tick(2 * u + 3);
+    } else {
+        loads(0);                                                // tick 0
+        read_all();
+        end_tick(0);
+        int u = 0;
+        for (; u + 2 < H; u += 2) {
+            compute(rd, u + 1, sp, sq, sr, wq, wr);              // tick 2u+1
+            end_tick(2 * u + 1);
+            loads(2 * u + 2);                                    // tick 2u+2
+            end_tick(2 * u + 2);
+            compute(rd, u + 2, sp, sr, sq, wr, wq);              // tick 2u+3
+            end_tick(2 * u + 3);
+            loads(2 * u + 4);                                    // tick 2u+4
+            end_tick(2 * u + 4);
+        }
+        compute(rd, u + 1, sp, sq, sr, wq, wr);                  // tick 2H-3
+        end_tick(2 * u + 1);
+        loads(2 * u + 2);
+        end_tick(2 * u + 2);
+        if (whole) compute(no_rd, 0, sp, sr, sq, wr, wq);        // tick 2H-1
+        end_tick(2 * u + 3);
+    }
 }
 
 struct Mx4Params {
@@ -180,7 +495,9 @@ template <int EPI>
 __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
 {
     constexpr int BM = 256;
-    __shared__ __align__(16) uint8_t smem[2 * (BM + BN) * 128];
+    // all of the LDS: the 128-row ring with its scales
+    __shared__ __align__(16) uint8_t smem[3 * (128 + BN) * 128 + 2 * SSTAGE];
+    static_assert(sizeof(smem) >= 2 * (BM + BN) * 128 + 2 * SSTAGE && sizeof(smem) <= 160 * 1024, "LDS");
     const MParams& p = mp.p;
     MTile tile;
     if (!schedule_m<BM>(p.group_off, p.capacity, p.E, p.n_rows, p.ntn, tile)) return;
@@ -219,7 +536,8 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
         sa.rows0 = min(tile.rows_valid, BMS / 2);
         sa.rows1 = max(tile.rows_valid - BMS / 2, 0);
         f32x16 acc[BMS / 64][2];
-        mainloop4<BMS>(sa, sb, acc, smem);
+        if constexpr (BMS == 256) mainloop4_pp(sa, sb, acc, smem);
+        else mainloop4<BMS>(sa, sb, acc, smem);
         if constexpr (EPI == EPI_SWIGLU_FWD)
             epilogue_swiglu4<BMS>(acc, p, tile.row0, tile.rows_valid, nt, smem);
         else

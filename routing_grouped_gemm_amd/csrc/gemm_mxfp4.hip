@@ -275,65 +275,99 @@ __device__ __forceinline__ void mainloop4_pp(const Src4& sa, const Src4& sb, f32
     struct Words {
         uint32_t a[MI], b[NJ];
     };
+    // LDS offsets of this lane's part of a fragment, per k-slice of a K-step:
+    // the chunk swizzle depends on the lane alone, so sub-tiles are constant
+    // offsets from one address
+    uint32_t vo[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks)
+        vo[ks] = (uint32_t)((lane & 31) * 128) + lds_chunk<false, 64>(lane & 31, ks * 2 + (lane >> 5)) * 16u;
+    const uint32_t vs = (uint32_t)(2 * STAGE + (lane & 31) * 16);
+    // where half K-step hs is read: scalars, opaque so that the per-lane
+    // addresses are made where they are used and not kept for every stage
+    struct At {
+        uint32_t a, b, s;
+    };
+    auto at = [&](int hs) __attribute__((always_inline)) {
+        const uint32_t st = (uint32_t)((hs >> 1) & 1) * STAGE;
+        At r{st + (uint32_t)g * (128 * 128), st + BM * 128 + (uint32_t)w4 * (32 * 128),
+             (uint32_t)((hs >> 2) & 1) * SSTAGE + (uint32_t)(hs & 3) * 4u};
+        asm volatile("" : "+s"(r.a), "+s"(r.b), "+s"(r.s));
+        return r;
+    };
     // fragment m (A 0..3, B 4..5) of k-slice s2 of half K-step hs
-    auto read_one = [&](int hs, int s2, int m, Slot& dst) __attribute__((always_inline)) {
-        const uint8_t* a_s = smem + ((hs >> 1) & 1) * STAGE;
-        const int ks = (hs & 1) * 2 + s2;
-        if (m < MI) dst.a[m] = read_frag4(a_s, g * 128 + m * 32, ks, lane);
-        else dst.b[m - MI] = read_frag4(a_s + BM * 128, WL<8>::sub_col(w4, m - MI), ks, lane);
+    auto read_one = [&](const At& p, int odd, int s2, int m, Slot& dst) __attribute__((always_inline)) {
+        const uint32_t v = vo[odd * 2 + s2];
+        const uint4 x = m < MI ? *reinterpret_cast<const uint4*>(smem + (v + p.a) + m * (32 * 128))
+                               : *reinterpret_cast<const uint4*>(smem + (v + p.b) + (m - MI) * (128 * 128));
+        const i32x8 f = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+        if (m < MI) dst.a[m] = f;
+        else dst.b[m - MI] = f;
     };
-    auto read_word = [&](int hs, int m, Words& w) __attribute__((always_inline)) {
-        if (m < MI) w.a[m] = scale_word(scales, g * 128 + m * 32, hs, lane);
-        else w.b[m - MI] = scale_word(scales, BM + WL<8>::sub_col(w4, m - MI), hs, lane);
+    auto read_word = [&](const At& p, int m, Words& w) __attribute__((always_inline)) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(
+            smem + (vs + p.s) + (m < MI ? (uint32_t)g * 2048u : 4096u + (uint32_t)w4 * 512u) +
+            (m < MI ? m * 512 : (m - MI) * 2048));
+        if (m < MI) w.a[m] = x;
+        else w.b[m - MI] = x;
     };
-    // the 16 MFMAs of k-slices p (first) and c1 (second) under the scale words
-    // w; with RD, what half K-step hs needs: its second k-slice into n1 and
-    // its scale words into wn during the first 8 MFMAs, its first k-slice into
-    // p (free by then) during the last 8
-    auto compute = [&](auto RD, int hs, Slot& p, Slot& c1, Slot& n1, Words& w, Words& wn) __attribute__((always_inline)) {
-#pragma unroll
-        for (int m = 0; m < MI; ++m) w.a[m] >>= sh;
-#pragma unroll
-        for (int m = 0; m < NJ; ++m) w.b[m] >>= sh;
+    auto barrier = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // A compute tick: the 16 MFMAs of k-slices p (first) and c1 (second) under
+    // the scale words w; with RD, what half K-step hs needs is read in their
+    // shadow: its second k-slice into n1, its scale words into wn, its first
+    // k-slice into p, each register once the MFMAs that use it have issued.
+    // The tick's barrier (after `waits`) comes kAfter MFMAs before the end, so
+    // that the other group's first ones queue up behind this one's last: with
+    // the barrier after all 16 the matrix unit idled a quarter of the time.
+    constexpr int kAfter = 3;
+    auto compute = [&](auto RD, auto ODD, int hs, Slot& p, Slot& c1, Slot& n1, Words& w, Words& wn,
+                       auto&& waits) __attribute__((always_inline)) {
+        constexpr int odd = decltype(ODD)::value;
+        At pt{};
+        if constexpr (decltype(RD)::value) pt = at(hs);
         __builtin_amdgcn_s_setprio(1);   // ahead of the memory-phase wave of this SIMD
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
             const int i = (n >> 1) & 3, j = n & 1;
+            if (n == 16 - kAfter) {
+                waits();
+                barrier();
+            }
             if (n < 8) acc[i][j] = mfma4<0>(p.b[j], p.a[i], acc[i][j], w.b[j], w.a[i]);
             else acc[i][j] = mfma4<2>(c1.b[j], c1.a[i], acc[i][j], w.b[j], w.a[i]);
             if constexpr (decltype(RD)::value) {
-                if (n < 6) read_one(hs, 1, n, n1);
-                else if (n < 8) {
+                if (n < 3) {
+                    read_one(pt, odd, 1, 2 * n, n1);
+                    read_one(pt, odd, 1, 2 * n + 1, n1);
+                }
+                if (n == 3 || n == 5) {
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) read_word(hs, (n - 6) * 3 + m, wn);
-                } else if (n < 14) read_one(hs, 0, n - 8, p);
+                    for (int m = 0; m < 3; ++m) read_word(pt, (n - 3) / 2 * 3 + m, wn);
+                }
+                if (n == 2 || n == 4 || n == 6 || n == 8) read_one(pt, odd, 0, n / 2 - 1, p);
+                if (n == 8 || n == 9) read_one(pt, odd, 0, n - 4, p);
             }
-        }
-        if constexpr (decltype(RD)::value) {
-#pragma unroll
-            for (int n = 0; n < 6; ++n) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-            }
-#pragma unroll
-            for (int n = 0; n < 6; ++n) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+            __builtin_amdgcn_sched_barrier(0);
         }
         // the MFMAs belong to this tick: the compiler would sink some of them
-        // past the barrier into the next one (with 190 spilled registers)
+        // past the branches that follow (with 190 spilled registers)
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) asm volatile("" : "+v"(acc[i][j]));
         __builtin_amdgcn_s_setprio(0);
+    };
+    // the scale words read in the last compute tick, shifted for this lane's
+    // k-blocks (in memory ticks: not between the barrier and the MFMAs)
+    auto shift = [&](Words& w) __attribute__((always_inline)) {
+#pragma unroll
+        for (int m = 0; m < MI; ++m) w.a[m] >>= sh;
+#pragma unroll
+        for (int m = 0; m < NJ; ++m) w.b[m] >>= sh;
     };
     // this wave's direct loads of memory tick t
     auto loads = [&](int t) __attribute__((always_inline)) {
@@ -366,7 +400,7 @@ __device__ __forceinline__ void mainloop4_pp(const Src4& sa, const Src4& sb, f32
     // What was issued this tick (or, for group 1 at t % 4 == 1, the tick
     // before) may stay in flight: 4 loads, and the scales ahead of them when
     // they went out this tick
-    auto end_tick = [&](int t) __attribute__((always_inline)) {
+    auto waits = [&](int t) __attribute__((always_inline)) {
         if ((t & 3) == 1) {
             const int j = (t + 3) >> 2;
             const int jn = g == 0 ? j + 1 : j;
@@ -379,65 +413,129 @@ __device__ __forceinline__ void mainloop4_pp(const Src4& sa, const Src4& sb, f32
             else if ((jn & 1) == 0) wait_vmcnt<5>();
             else wait_vmcnt<4>();
         }
-        __builtin_amdgcn_sched_barrier(0);
-        __syncthreads();
-        __builtin_amdgcn_sched_barrier(0);
     };
+    auto end_tick = [&](int t) __attribute__((always_inline)) {
+        waits(t);
+        barrier();
+    };
+    auto none = []() __attribute__((always_inline)) {};
+    auto wait4 = []() __attribute__((always_inline)) { wait_vmcnt<4>(); };
     const std::integral_constant<bool, true> rd;
     const std::integral_constant<bool, false> no_rd;
+    const std::integral_constant<int, 1> odd;    // of the half K-step that is read
+    const std::integral_constant<int, 0> even;
     Slot sp, sq, sr;   // first k-slice; second k-slice, alternating between sq and sr
     Words wq, wr;
     auto read_all = [&]() __attribute__((always_inline)) {
+        const At p0 = at(0);
 #pragma unroll
-        for (int m = 0; m < 6; ++m) read_one(0, 0, m, sp);
+        for (int m = 0; m < 6; ++m) read_one(p0, 0, 0, m, sp);
 #pragma unroll
-        for (int m = 0; m < 6; ++m) read_one(0, 1, m, sq);
+        for (int m = 0; m < 6; ++m) read_one(p0, 0, 1, m, sq);
 #pragma unroll
-        for (int m = 0; m < 6; ++m) read_word(0, m, wq);
+        for (int m = 0; m < 6; ++m) read_word(p0, m, wq);
     };
 
+    // the last half K-step, in tick t
+    auto last = [&](int t) __attribute__((always_inline)) {
+        if (whole) compute(no_rd, even, 0, sp, sr, sq, wr, wq, [&] { waits(t); });
+        else end_tick(t);
+    };
+    // Two K-steps (2c, 2c + 1; their loads are of 2c + 2, 2c + 3) are eight
+    // ticks whose loads and waits are known when all of those K-steps exist
+    // (and, for group 1, c > 0): no branches there.  With the conditions
+    // tested in every tick, and the barrier after the last MFMA, a tick took 800
+    // cycles; so it takes 625 (16 MFMAs are 512).
     if (g == 0) {
         read_all();
+        shift(wq);
         int u = 0;
+        for (int c = 0; 2 * c + 3 < nk; ++c, u += 4) {
+            compute(rd, odd, u + 1, sp, sq, sr, wq, wr, none);                       // tick 8c
+            sc.issue(c + 1);
+            ha.issue(0, 2 * c + 2);
+            shift(wr);
+            wait_vmcnt<5>();
+            barrier();
+            compute(rd, even, u + 2, sp, sr, sq, wr, wq, none);                      // tick 8c+2
+            hb.issue(0, 2 * c + 2);
+            shift(wq);
+            barrier();
+            compute(rd, odd, u + 3, sp, sq, sr, wq, wr, none);                       // tick 8c+4
+            ha.issue(STAGE, 2 * c + 3);
+            shift(wr);
+            wait_vmcnt<4>();
+            barrier();
+            compute(rd, even, u + 4, sp, sr, sq, wr, wq, none);                      // tick 8c+6
+            hb.issue(STAGE, 2 * c + 3);
+            shift(wq);
+            barrier();
+        }
         for (; u + 2 < H; u += 2) {
-            compute(rd, u + 1, sp, sq, sr, wq, wr);              // tick 2u
-            end_tick(2 * u);
+            compute(rd, odd, u + 1, sp, sq, sr, wq, wr, [&] { waits(2 * u); });      // tick 2u
             loads(2 * u + 1);                                    // tick 2u+1
+            shift(wr);
             end_tick(2 * u + 1);
-            compute(rd, u + 2, sp, sr, sq, wr, wq);              // tick 2u+2
-            end_tick(2 * u + 2);
+            compute(rd, even, u + 2, sp, sr, sq, wr, wq, [&] { waits(2 * u + 2); }); // tick 2u+2
             loads(2 * u + 3);                                    // tick 2u+3
+            shift(wq);
             end_tick(2 * u + 3);
         }
-        compute(rd, u + 1, sp, sq, sr, wq, wr);                  // tick 2H-4
-        end_tick(2 * u);
+        compute(rd, odd, u + 1, sp, sq, sr, wq, wr, [&] { waits(2 * u); });      // tick 2H-4
         loads(2 * u + 1);
+        shift(wr);
         end_tick(2 * u + 1);
-        if (whole) compute(no_rd, 0, sp, sr, sq, wr, wq);        // tick 2H-2
-        end_tick(2 * u + 2);
+        last(2 * u + 2);                                         // tick 2H-2
         loads(2 * u + 3);
         end_tick(2 * u + 3);
     } else {
         loads(0);                                                // tick 0
         read_all();
+        shift(wq);
         end_tick(0);
         int u = 0;
-        for (; u + 2 < H; u += 2) {
-            compute(rd, u + 1, sp, sq, sr, wq, wr);              // tick 2u+1
-            end_tick(2 * u + 1);
-            loads(2 * u + 2);                                    // tick 2u+2
-            end_tick(2 * u + 2);
-            compute(rd, u + 2, sp, sr, sq, wr, wq);              // tick 2u+3
-            end_tick(2 * u + 3);
-            loads(2 * u + 4);                                    // tick 2u+4
-            end_tick(2 * u + 4);
+        auto generic = [&](int end) __attribute__((always_inline)) {
+            for (; u + 2 < end; u += 2) {
+                compute(rd, odd, u + 1, sp, sq, sr, wq, wr, [&] { waits(2 * u + 1); });  // tick 2u+1
+                loads(2 * u + 2);                                // tick 2u+2
+                shift(wr);
+                end_tick(2 * u + 2);
+                compute(rd, even, u + 2, sp, sr, sq, wr, wq, [&] { waits(2 * u + 3); }); // tick 2u+3
+                loads(2 * u + 4);                                // tick 2u+4
+                shift(wq);
+                end_tick(2 * u + 4);
+            }
+        };
+        if (nk > 5) {
+            generic(5);
+            for (int c = 1; 2 * c + 3 < nk; ++c, u += 4) {
+                compute(rd, odd, u + 1, sp, sq, sr, wq, wr, wait4);                      // tick 8c+1
+                sc.issue(c + 1);
+                hb.issue(0, 2 * c + 2);
+                shift(wr);
+                wait_vmcnt<5>();
+                barrier();
+                compute(rd, even, u + 2, sp, sr, sq, wr, wq, none);                      // tick 8c+3
+                ha.issue(0, 2 * c + 2);
+                shift(wq);
+                barrier();
+                compute(rd, odd, u + 3, sp, sq, sr, wq, wr, wait4);                      // tick 8c+5
+                hb.issue(STAGE, 2 * c + 3);
+                shift(wr);
+                wait_vmcnt<4>();
+                barrier();
+                compute(rd, even, u + 4, sp, sr, sq, wr, wq, none);                      // tick 8c+7
+                ha.issue(STAGE, 2 * c + 3);
+                shift(wq);
+                barrier();
+            }
         }
-        compute(rd, u + 1, sp, sq, sr, wq, wr);                  // tick 2H-3
-        end_tick(2 * u + 1);
+        generic(H);
+        compute(rd, odd, u + 1, sp, sq, sr, wq, wr, [&] { waits(2 * u + 1); });  // tick 2H-3
         loads(2 * u + 2);
+        shift(wr);
         end_tick(2 * u + 2);
-        if (whole) compute(no_rd, 0, sp, sr, sq, wr, wq);        // tick 2H-1
-        end_tick(2 * u + 3);
+        last(2 * u + 3);                                         // tick 2H-1
     }
 }
 

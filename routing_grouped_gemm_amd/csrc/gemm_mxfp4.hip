@@ -10,6 +10,8 @@
 // row (i & 31)'s 32 codes of k-block (i >> 5), and its scale operand that
 // block's scale (checked on the hardware against a host product with random
 // codes and scales, in all four byte positions of the scale operand).
+#include <algorithm>
+
 #include "gemm_common.h"
 #include "mx4.h"
 
@@ -19,6 +21,7 @@ namespace {
 using namespace gemm;
 
 typedef __attribute__((ext_vector_type(8))) int i32x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 
 constexpr int KB = 256;          // codes per K-step (128 bytes per row)
 constexpr int NW4 = 8;           // waves per workgroup
@@ -646,6 +649,316 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
     else run(std::integral_constant<int, 256>{});
 }
 
+// ---------------------------------------------------------------- few rows
+// The form for few rows per expert (single tokens, small batches): the
+// weights are read once and that bounds it, so a workgroup takes 32 output
+// columns (32 gate and 32 up rows of W13) of one expert against up to 64 of
+// its rows, and its 8 waves split K in units of 256 k, 128 bytes of a row: a
+// panel is U units of every wave.  A wave's weights of a panel come into its
+// own part of the LDS by direct loads, all in flight together and whole
+// 128-byte lines at a time (read straight into the registers of a fragment, 64
+// bytes of each of 16 rows, the same bytes took 1.25 times as long from HBM,
+// twice as long from the L2); the panel's scales, which are consecutive in
+// every row, are loaded once for all waves (each wave fetching its own 16
+// bytes of 64 rows made the kernel half as fast).  They are multiplied with 16
+// rows at a time (v_mfma_scale_f32_16x16x128: lane i holds weight row, or
+// token, i & 15 and k-block i >> 4 of 128 k).  The waves' sums meet in LDS, in
+// wave order.
+constexpr int FROWS = 64, FCOLS = 32;
+
+struct Few4Params {
+    const uint8_t *Aq, *As;    // rows: codes, scales
+    const uint8_t *Bq, *Bs;    // weights of expert 0; sBq bytes between experts' codes
+    int64_t sBq;
+    int K;
+    int f;                     // gate/up: W13's up rows start here
+    int ntn;                   // column tiles: f / 32 or d / 32
+    const int32_t* group_off;
+    int capacity, E;
+    int64_t n_rows;
+    uint16_t* C;               // gate/up: gu [n_rows, 2f] or null; down: y [n_rows, ldc]
+    int64_t ldc;
+    uint16_t* H;               // gate/up: h [n_rows, f] or null
+    uint8_t *Mq, *Ms;          // gate/up: MXFP4 h
+};
+
+// The tile of this workgroup: schedule_m's order (expert-major; a contiguous
+// range of tiles per XCD), with every lane's group bounds loaded at once and
+// the chosen expert's taken from the lane that holds them: one round trip to
+// memory ahead of the weights instead of three.
+template <int PER>   // experts per lane, E <= 64 PER
+__device__ __forceinline__ bool schedule_few(const Few4Params& p, MTile& t)
+{
+    const int lane = threadIdx.x & 63;
+    const int gb = lane * PER;
+    const int n_rows = (int)p.n_rows;   // below 2^31
+    int bnd[PER + 1];
+    if (p.capacity > 0) {
+#pragma unroll
+        for (int k = 0; k <= PER; ++k) bnd[k] = (int)min((int64_t)min(gb + k, p.E) * p.capacity, p.n_rows);
+    } else {
+#pragma unroll
+        for (int k = 0; k <= PER; ++k) bnd[k] = p.group_off[min(gb + k, p.E)];
+    }
+    int cnt = 0, c[PER];
+#pragma unroll
+    for (int k = 0; k <= PER; ++k) bnd[k] = min(max(bnd[k], 0), n_rows);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        c[k] = (int)((uint32_t)(max(bnd[k + 1] - bnd[k], 0) + FROWS - 1) / FROWS) * p.ntn;
+        cnt += c[k];
+    }
+    // inclusive scan by lane permutations: within rows of 16 (row_shr 1, 2, 4,
+    // 8), then each row's last lane into the rows behind it (row_bcast 15, 31)
+    int incl = cnt;
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, true);
+    const int total = __builtin_amdgcn_readlane(incl, 63);
+    const int per_xcd = (total + 7) / 8;
+    const int slot = blockIdx.x / 8;
+    const int L = (int)(blockIdx.x % 8) * per_xcd + slot;
+    if (slot >= per_xcd || L >= total) return false;
+    int run = incl - cnt;
+    const int src = __ffsll((unsigned long long)__ballot(run <= L && L < incl)) - 1;
+    int e = gb, first = run, b0 = 0, rows = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (L >= run && L < run + c[k]) {
+            e = gb + k;
+            first = run;
+            b0 = bnd[k];
+            rows = bnd[k + 1] - bnd[k];
+        }
+        run += c[k];
+    }
+    t.e = __builtin_amdgcn_readlane(e, src);
+    const int local = L - __builtin_amdgcn_readlane(first, src);
+    const int m_e = __builtin_amdgcn_readlane(rows, src);
+    // column tiles across a 64-row group before the next group: a group's
+    // workgroups run together and share its rows
+    t.mt = local / p.ntn;
+    t.nt = local - t.mt * p.ntn;
+    t.row0 = (int64_t)__builtin_amdgcn_readlane(b0, src) + (int64_t)t.mt * FROWS;
+    t.rows_valid = min(FROWS, m_e - t.mt * FROWS);
+    return true;
+}
+
+template <int EPI, int U>   // U: units a wave has in flight
+__global__ __launch_bounds__(64 * NW4) void mx4_few_rows_kernel(Few4Params p)
+{
+    constexpr int NTILE = EPI == EPI_SWIGLU_FWD ? 4 : 2;   // 16-row weight tiles: gate, gate, up, up
+    constexpr int NCH = FROWS / 16;                        // 16-row chunks of the rows
+    constexpr int WROWS = 16 * NTILE;                      // weight rows of the workgroup
+    constexpr int WBYTES = U * WROWS * 128;                // a wave's weights
+    constexpr int RBYTES = NTILE * 64 * 16;                // a wave's sums, in the same place afterwards
+    constexpr int SB = 64 * U;                             // scale bytes of a row and panel
+    constexpr int SPIECE = SB / 16;                        // ... in 16-byte pieces
+    constexpr int NOUT = EPI == EPI_SWIGLU_FWD ? 3 : 1;
+    __shared__ __align__(16) uint8_t lds[NW4 * (WBYTES > RBYTES ? WBYTES : RBYTES)];
+    __shared__ __align__(16) uint8_t lsc[WROWS * SB];
+    __shared__ __align__(16) uint16_t out[NOUT][16 * FCOLS];
+    auto red = reinterpret_cast<f32x4_t(*)[NTILE][64]>(lds);
+    MTile t;
+    if (p.E <= 128 ? !schedule_few<2>(p, t) : !schedule_few<16>(p, t)) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r16 = lane & 15, kb = lane >> 4;
+    const int64_t cb = p.K / 2, sbk = p.K / 32;
+    const int n0 = t.nt * FCOLS;
+    const int nch = (t.rows_valid + 15) / 16;
+
+    // this wave's units; steps of 128 k
+    const int n128 = p.K / 128, n256 = (n128 + 1) / 2;
+    // 32 consecutive rows of W13's gate half and of its up half (of W2)
+    const uint8_t* Bq = p.Bq + (int64_t)t.e * p.sBq + n0 * cb;
+    const uint8_t* Bs = p.Bs + (int64_t)t.e * (p.sBq / 16) + n0 * sbk;
+    desc_t d[NTILE / 2];
+#pragma unroll
+    for (int h = 0; h < NTILE / 2; ++h) d[h] = wave_uniform(make_desc(Bq + h * (p.f * cb), FCOLS * cb));
+    // direct loads of scales: 64 / SPIECE rows each, this wave's is number `wave`;
+    // piece c of row r at piece c ^ (r & (SPIECE - 1))
+    constexpr int SINSTR = WROWS * SPIECE / 64;
+    const int srow = wave * (64 / SPIECE) + lane / SPIECE;   // of WROWS
+    const int shalf = __builtin_amdgcn_readfirstlane(srow) / FCOLS;
+    const desc_t ds = wave_uniform(make_desc(Bs + shalf * (p.f * sbk), wave < SINSTR ? FCOLS * sbk : 0));
+    const uint32_t soff = (uint32_t)((srow % FCOLS) * sbk) + (((uint32_t)lane % SPIECE) ^ ((uint32_t)srow & (SPIECE - 1))) * 16u;
+    const uint32_t sm0 = lds_addr(lsc) + (uint32_t)wave * 1024u;
+    // direct load q of a unit: rows 8q .. 8q+7 of WROWS, 16-byte chunk c of row
+    // r at chunk c ^ ((r >> 1) & 7), so that a fragment's 16 rows of one chunk
+    // lie in 16 different bank groups
+    uint32_t voff[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int row = 8 * q + (lane >> 3);               // of a half's 32
+        voff[q] = (uint32_t)(row * cb) + (((uint32_t)lane & 7u) ^ ((row >> 1) & 7u)) * 16u;
+    }
+    uint8_t* mine = lds + wave * WBYTES;
+    const uint32_t m0 = lds_addr(mine);
+    // the scale words of a unit's two steps of 128 k
+    struct __attribute__((packed, aligned(4))) Words2 { uint32_t v[2]; };
+    auto scales = [&](const uint8_t* row, int u) __attribute__((always_inline)) {
+        Words2 x;
+        if (2 * u + 1 < n128) {
+            x = *reinterpret_cast<const Words2*>(row + u * 8);
+        } else {
+            x.v[0] = *reinterpret_cast<const uint32_t*>(row + u * 8);
+            x.v[1] = 0;
+        }
+        return x;
+    };
+    f32x4_t acc[NCH][NTILE];
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+        for (int i = 0; i < NTILE; ++i) acc[c][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p0 = 0; p0 < n256; p0 += NW4 * U) {
+        const int u0 = p0 + wave * U, u_end = n256;        // this wave's units of the panel
+        if (wave < SINSTR) dma16_to_lds_at(ds, sm0, soff, (uint32_t)p0 * 8u);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u0 + u >= u_end) break;
+#pragma unroll
+            for (int q = 0; q < 2 * NTILE; ++q)
+                dma16_to_lds_at(d[q >> 2], m0 + (uint32_t)(u * WROWS * 128 + q * 1024), voff[q & 3], (uint32_t)(u0 + u) * 128u);
+        }
+        Words2 sw[U][NTILE];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            if (c >= nch) break;
+            // rows past the last valid one repeat it (their sums are not stored)
+            const int64_t row = t.row0 + min(c * 16 + r16, t.rows_valid - 1);
+            const uint8_t* xr = p.Aq + row * cb + kb * 16;
+            uint4 x[U][2];
+            Words2 sx[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u0 + u >= u_end) break;
+                sx[u] = scales(p.As + row * sbk, u0 + u);
+                x[u][0] = *reinterpret_cast<const uint4*>(xr + (int64_t)(u0 + u) * 128);
+                x[u][1] = 2 * (u0 + u) + 1 < n128 ? *reinterpret_cast<const uint4*>(xr + (int64_t)(u0 + u) * 128 + 64)
+                                                  : make_uint4(0, 0, 0, 0);
+            }
+            if (c == 0) {
+                // all waves' direct loads have landed
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                __syncthreads();
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int i = 0; i < NTILE; ++i) {
+                        const int row = i * 16 + r16, at = (wave * U + u) * 8;
+                        const uint2 x2 = *reinterpret_cast<const uint2*>(
+                            lsc + row * SB + (((at >> 4) ^ (row & (SPIECE - 1))) << 4) + (at & 8));
+                        sw[u][i].v[0] = x2.x;
+                        sw[u][i].v[1] = x2.y;
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u0 + u >= u_end) break;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (2 * (u0 + u) + s >= n128) break;
+                    const i32x8 b = {(int)x[u][s].x, (int)x[u][s].y, (int)x[u][s].z, (int)x[u][s].w, 0, 0, 0, 0};
+                    const int sb = (int)(sx[u].v[s] >> (8 * kb));
+#pragma unroll
+                    for (int i = 0; i < NTILE; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(
+                            mine + (u * WROWS + i * 16 + r16) * 128 + ((s * 4 + kb) ^ ((r16 >> 1) & 7)) * 16);
+                        const i32x8 a = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+                        acc[c][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[c][i], 4, 4, 0,
+                                                                                     (int)(sw[u][i].v[s] >> (8 * kb)), 0, sb);
+                    }
+                }
+            }
+        }
+        // the next panel, or the sums, take the weights' and scales' place
+        __syncthreads();
+    }
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+        if (c >= nch) break;
+#pragma unroll
+        for (int i = 0; i < NTILE; ++i) red[wave][i][lane] = acc[c][i];
+        __syncthreads();
+        // 16 rows x 32 columns; lane (col / 4 % 4) * 16 + row holds columns 4g .. 4g+3 of a tile
+        for (int o = tid; o < 16 * FCOLS; o += 64 * NW4) {
+            const int r = o & 15, col = o >> 4;
+            const int l = ((col & 15) >> 2) * 16 + r, q = col & 3, tl = col >> 4;
+            float v = red[0][tl][l][q], u = 0.0f;
+#pragma unroll
+            for (int w = 1; w < NW4; ++w) v += red[w][tl][l][q];
+            if constexpr (EPI == EPI_SWIGLU_FWD) {
+                u = red[0][2 + tl][l][q];
+#pragma unroll
+                for (int w = 1; w < NW4; ++w) u += red[w][2 + tl][l][q];
+                out[1][r * FCOLS + col] = (uint16_t)f32_to_bf16_bits(v);
+                out[2][r * FCOLS + col] = (uint16_t)f32_to_bf16_bits(u);
+                v = silu_f(v) * u;
+            }
+            out[0][r * FCOLS + col] = (uint16_t)f32_to_bf16_bits(v);
+        }
+        __syncthreads();
+        // a wave stores one 16 x 32 tile, 16 bytes per lane: h (or y), g, u
+        const int r = lane >> 2, col = 8 * (lane & 3);
+        const int64_t row = t.row0 + c * 16 + r;
+        const bool valid = c * 16 + r < t.rows_valid;
+        if (wave < NOUT) {
+            const uint4 v = *reinterpret_cast<const uint4*>(&out[wave][r * FCOLS + col]);
+            if constexpr (EPI == EPI_SWIGLU_FWD) {
+                if (wave == 0) {
+                    uint32_t q;
+                    const uint32_t s = mx4::quant8_quad(v, q);
+                    if (valid) {
+                        if (p.H) *reinterpret_cast<uint4*>(p.H + row * p.f + n0 + col) = v;
+                        *reinterpret_cast<uint32_t*>(p.Mq + row * (p.f / 2) + (n0 + col) / 2) = q;
+                        if ((lane & 3) == 0) p.Ms[row * (p.f / 32) + n0 / 32] = (uint8_t)s;
+                    }
+                } else if (valid && p.C) {
+                    *reinterpret_cast<uint4*>(p.C + row * p.ldc + (wave == 2 ? p.f : 0) + n0 + col) = v;
+                }
+            } else {
+                if (valid) *reinterpret_cast<uint4*>(p.C + row * p.ldc + n0 + col) = v;
+            }
+        }
+        // (the next chunk's sums go to red, which nobody reads any more; out is
+        // written again after the barrier that follows them)
+    }
+}
+
+// Whether the few-row form runs: when its workgroups (their host-known bound,
+// sum ceil(m_e / 64) <= experts with rows + n_rows / 64, times the column
+// tiles) run in one round on the chip's 256 CUs, one per CU with two units a
+// wave (139 KB of LDS) and two with one.  Measured against the tile form
+// (gate/up, down, us; d = 4096, f = 1536 unless given): 1 row of 1 expert
+// 5.7 4.3 against 18.0 10.0; 256 rows of 1 expert 15.2 9.6 against 25.8 14.1; 4
+// experts of 32 rows 9.9 6.7 against 17.9 10.1; 8 of 1 row, d = 2048, f =
+// 1152: 6.5 5.0 against 11.9 9.2.  Past one round: 8 experts of 8 rows (384
+// workgroups for gate/up) 16.4 against 18.2, 16 of 1 row (768) 25.6 against
+// 20.3, 128 of 2 rows 198 132 against 160 105: there the tile form streams the
+// weights faster.
+inline bool few_rows(const GroupSpec& g, int K, int ntn)
+{
+    const int64_t groups = std::min<int64_t>(g.E, g.n_rows) + g.n_rows / FROWS;
+    return groups * ntn <= 256 * (K <= NW4 * 256 ? 2 : 1);
+}
+
+template <int EPI>
+hipError_t launch_few4(const Few4Params& p, hipStream_t s)
+{
+    const int64_t groups = std::min<int64_t>(p.E, p.n_rows) + p.n_rows / FROWS;
+    const int64_t grid = (groups * p.ntn + 7) / 8 * 8;
+    if (p.K <= NW4 * 256)   // one unit per wave
+        hipLaunchKernelGGL((mx4_few_rows_kernel<EPI, 1>), dim3((unsigned)grid), dim3(64 * NW4), 0, s, p);
+    else
+        hipLaunchKernelGGL((mx4_few_rows_kernel<EPI, 2>), dim3((unsigned)grid), dim3(64 * NW4), 0, s, p);
+    return hipGetLastError();
+}
+
 template <int EPI>
 hipError_t launch_mx4_m(const Mx4Params& mp, hipStream_t s)
 {
@@ -676,7 +989,31 @@ hipError_t gemm_op_mxfp4(int op, const moe_gemm_tensors& t, GroupSpec g, int d, 
     a.p.E = g.E;
     a.p.n_rows = g.n_rows;
     a.p.f = f;
-    if (op == MOE_GEMM_GATE_UP) {
+    if (op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return hipErrorInvalidValue;
+    if (g.n_rows == 0) return hipSuccess;
+    const bool up = op == MOE_GEMM_GATE_UP;
+    if (few_rows(g, up ? d : f, (up ? f : d) / FCOLS)) {
+        Few4Params p{};
+        p.group_off = g.group_off;
+        p.capacity = g.capacity;
+        p.E = g.E;
+        p.n_rows = g.n_rows;
+        p.f = f;
+        p.K = up ? d : f;
+        p.ntn = (up ? f : d) / FCOLS;
+        p.Aq = up ? static_cast<const uint8_t*>(t.x_perm) : hq;
+        p.As = up ? t.x_perm_scales : hs;
+        p.Bq = static_cast<const uint8_t*>(up ? t.w13 : t.w2);
+        p.Bs = up ? t.w13_scales : t.w2_scales;
+        p.sBq = (int64_t)d * f * (up ? 2 : 1) / 2;
+        p.C = static_cast<uint16_t*>(up ? t.gu : t.y_perm);
+        p.ldc = up ? 2 * f : d;
+        p.H = static_cast<uint16_t*>(t.h);
+        p.Mq = hq;
+        p.Ms = hs;
+        return up ? launch_few4<EPI_SWIGLU_FWD>(p, s) : launch_few4<EPI_STORE>(p, s);
+    }
+    if (up) {
         a.p.N = f;
         a.p.K = d;
         a.p.ntn = (f + 127) / 128;
@@ -694,20 +1031,17 @@ hipError_t gemm_op_mxfp4(int op, const moe_gemm_tensors& t, GroupSpec g, int d, 
         a.sBq = (int64_t)2 * f * (d / 2);
         return launch_mx4_m<EPI_SWIGLU_FWD>(a, s);
     }
-    if (op == MOE_GEMM_DOWN) {
-        a.p.N = d;
-        a.p.K = f;
-        a.p.ntn = (d + BN - 1) / BN;
-        a.p.C = static_cast<uint16_t*>(t.y_perm);
-        a.p.ldc = d;
-        a.Aq = hq;
-        a.As = hs;
-        a.Bq = static_cast<const uint8_t*>(t.w2);
-        a.Bs = t.w2_scales;
-        a.sBq = (int64_t)d * (f / 2);
-        return launch_mx4_m<EPI_STORE>(a, s);
-    }
-    return hipErrorInvalidValue;
+    a.p.N = d;
+    a.p.K = f;
+    a.p.ntn = (d + BN - 1) / BN;
+    a.p.C = static_cast<uint16_t*>(t.y_perm);
+    a.p.ldc = d;
+    a.Aq = hq;
+    a.As = hs;
+    a.Bq = static_cast<const uint8_t*>(t.w2);
+    a.Bs = t.w2_scales;
+    a.sBq = (int64_t)d * (f / 2);
+    return launch_mx4_m<EPI_STORE>(a, s);
 }
 
 }  // namespace moe

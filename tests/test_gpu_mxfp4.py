@@ -223,6 +223,9 @@ SIZES = [
     ([1], 128, 128), ([1, 0, 1], 256, 128), ([0, 0, 5], 128, 384), ([3, 1, 2, 1], 640, 256),
     ([16, 17, 15], 512, 256), ([33, 0, 64, 65], 256, 384), ([129, 128, 127], 384, 128), ([257, 1, 300], 256, 256),
     ([200, 511], 1152, 640), ([70, 0, 260, 90], 128, 128), ([1, 2], 4096, 1536), ([40, 10], 2176, 1280),
+    # few rows over many experts: skewed (several 16- and 64-row groups of one expert), and K of several panels
+    ([0] * 20 + [63] + [0] * 20, 256, 128), ([1] * 3 + [0] * 60 + [130, 1], 640, 256), ([2, 1], 8448, 2176),
+    ([0, 17, 0, 0, 0, 0, 1, 0], 384, 4224), ([1, 0] * 70, 128, 128),
 ]
 
 

@@ -199,5 +199,7 @@ def test_python_calls_refuse_what_is_not_dense(m):
         m.moe_dequantize_mxfp4(u8(4, 32), u8(4, 2), x)
     with pytest.raises(ValueError):
         m._dense("x", x[:, ::2], torch.bfloat16, 4, 32)
+    with pytest.raises(ValueError):                       # another shape, another type
+        m._dense("x", x, torch.bfloat16, 4, 32)
     with pytest.raises(ValueError):
-        m._on(x, torch.empty(1, device="meta"))
+        m._dense("x", x, torch.float32, 4, 64)

@@ -13,8 +13,8 @@
 //      A run is cut where a sequence ends; the piece of run b in sequence s
 //      leaves its sums in row b + s of the workspace (run and sequence never
 //      decrease from piece to piece and one of them grows, so rows are distinct).
-//   2. balance_reduce_kernel: per sequence and group of experts, the sums of
-//      its pieces' rows in order; the last workgroup to finish adds up the losses.
+//   2. balance_reduce_kernel: per sequence, the sums of its pieces' rows in a
+//      fixed order; the last workgroup to finish adds up the losses.
 // Backward, one kernel: the softmax again from the logits (p from a rounded lse
 // would lose |lse| * 2^-24 of relative accuracy).  No floating-point atomics:
 // results are the same bits on every run.
@@ -25,7 +25,7 @@
 namespace moe {
 namespace {
 
-constexpr int NT = 256;
+constexpr int NT = 512;
 
 struct Tokens {
     const float* logits;
@@ -137,24 +137,38 @@ struct Row {
     // set); a row with no finite logit has p = 0 and lse = 0.
     __device__ __forceinline__ float softmax(int E, int l, bool& bad)
     {
-        float top = -INFINITY;
+        // x * 0 is NaN for an x that is not finite: one operation per logit
+        // tells whether any needs to be replaced
+        float odd = 0.0f, top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 4 * NCH; ++i) {
-            const bool fin = fabsf(v[i]) <= 3.402823466e38f;
-            bad |= !fin && col(l, i) < E;
-            v[i] = fin ? v[i] : -INFINITY;
+            odd = fmaf(v[i], 0.0f, odd);
             top = fmaxf(top, v[i]);
         }
-        top = segment_max<LPT>(top);
-        const bool none = top == -INFINITY;
+        bool none = false;
+        if (__builtin_expect(__any(odd != 0.0f), 0)) {   // (also where a lane's chunk lies past E)
+            top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4 * NCH; ++i) {
+                const bool fin = fabsf(v[i]) <= 3.402823466e38f;
+                bad |= !fin && col(l, i) < E;
+                v[i] = fin ? v[i] : -INFINITY;
+                top = fmaxf(top, v[i]);
+            }
+            top = segment_max<LPT>(top);
+            none = top == -INFINITY;
+            top = none ? 0.0f : top;                     // exp(-infinity - 0) = 0
+        } else {
+            top = segment_max<LPT>(top);
+        }
         float den = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * NCH; ++i) {
-            v[i] = none ? 0.0f : __expf(v[i] - top);
+            v[i] = __expf(v[i] - top);
             den += v[i];
         }
         den = segment_sum<LPT>(den);
-        const float r = none ? 0.0f : 1.0f / den;
+        const float r = none ? 0.0f : __builtin_amdgcn_rcpf(den);   // (one unit in the last place)
 #pragma unroll
         for (int i = 0; i < 4 * NCH; ++i) v[i] *= r;
         return none ? 0.0f : top + __logf(den);
@@ -163,12 +177,13 @@ struct Row {
 
 // workspace: the ticket (first 256 bytes), then per piece a row of floats (the
 // sums of p, then the sum of lse^2) and a row of counts (pairs per expert,
-// then tokens, then pairs)
+// then tokens)
 constexpr size_t kTicketBytes = 256;
-__host__ __device__ inline int row_stride(int E) { return (E + 5) & ~3; }
+__host__ __device__ inline int row_stride(int E) { return (E + 4) & ~3; }
 
 template <int LPT, int NCH, bool VEC>
 __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int32_t* __restrict__ topk_idx, int k,
+                                                            uint32_t over_k,   // ceil(2^32 / k), k > 1
                                                             float* __restrict__ lse_out, float* __restrict__ fpart,
                                                             int32_t* __restrict__ ipart, int* __restrict__ ticket,
                                                             int32_t* __restrict__ dev_err)
@@ -177,7 +192,8 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
     constexpr int U = NCH == 1 ? 4 : 2;           // tokens in flight per group
     __shared__ float s_p[NT / 64][kMaxExperts];
     __shared__ float s_z[NT / 64];
-    __shared__ int s_cnt[kMaxExperts + 2];
+    __shared__ int s_n[NT / 64];
+    __shared__ int s_cnt[kMaxExperts];
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT, wave = tid >> 6;
     const int E = a.E, stride = row_stride(E);
     if (blockIdx.x == 0 && tid == 0) *ticket = 0;
@@ -189,7 +205,24 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
                 for (int t = begin + tid; t < end; t += NT) lse_out[t] = 0.0f;
             return;
         }
-        for (int e = tid; e < E + 2; e += NT) s_cnt[e] = 0;
+        for (int e = tid; e < E; e += NT) s_cnt[e] = 0;
+        // The piece's routed pairs, PQ per thread and pass; the first pass is
+        // loaded ahead of the logits.  A pair's token is its number within the
+        // piece over k, by multiplication (numbers below 2^24: exact).
+        constexpr int PQ = 4;
+        const int32_t* idx = topk_idx + (int64_t)begin * k;
+        const int pairs = (end - begin) * k;
+        auto load_pairs = [&](int i0, int (&e)[PQ]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int q = 0; q < PQ; ++q) {
+                const int i = i0 + q * NT;
+                e[q] = i < pairs ? idx[i] : -1;
+                if (a.mask && i < pairs && !a.mask[begin + (k == 1 ? i : (int)__umulhi((uint32_t)i, over_k))]) e[q] = -1;
+            }
+        };
+        int ev[PQ];
+        load_pairs(tid, ev);
+        int n = 0;
         float sum[4 * NCH], z = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4 * NCH; ++i) sum[i] = 0.0f;
@@ -209,6 +242,7 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
                 const float lse = r[u].softmax(E, l, b);
                 bad |= b && on[u];
                 if (on[u]) {
+                    ++n;
 #pragma unroll
                     for (int i = 0; i < 4 * NCH; ++i) sum[i] += r[u].v[i];
                     z = fmaf(lse, lse, z);
@@ -222,146 +256,174 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
 #pragma unroll
             for (int i = 0; i < 4 * NCH; ++i) sum[i] += __shfl_xor(sum[i], off, 64);
             z += __shfl_xor(z, off, 64);
+            n += __shfl_xor(n, off, 64);
         }
         if (grp % GW == 0) {
 #pragma unroll
             for (int i = 0; i < 4 * NCH; ++i)
                 if (Row<LPT, NCH, VEC>::col(l, i) < E) s_p[wave][Row<LPT, NCH, VEC>::col(l, i)] = sum[i];
-            if (l == 0) s_z[wave] = z;
-        }
-        __syncthreads();   // s_cnt is clear, too
-        int n = 0, m = 0;
-        for (int64_t i = (int64_t)begin * k + tid; i < (int64_t)end * k; i += NT) {
-            const int t = (int)(i / k);
-            if (a.mask && !a.mask[t]) continue;
-            const int e = topk_idx[i];
-            n += i == (int64_t)t * k ? 1 : 0;
-            if (e >= 0 && e < E) {
-                atomicAdd(&s_cnt[e], 1);   // integer: the order does not matter
-                ++m;
+            if (l == 0) {
+                s_z[wave] = z;
+                s_n[wave] = n;
             }
         }
-        if (n) atomicAdd(&s_cnt[E], n);
-        if (m) atomicAdd(&s_cnt[E + 1], m);
+        __syncthreads();   // s_cnt is clear, too
+        for (int i0 = tid; i0 < pairs; i0 += NT * PQ) {
+            if (i0 != tid) load_pairs(i0, ev);
+#pragma unroll
+            for (int q = 0; q < PQ; ++q)
+                if (ev[q] >= 0 && ev[q] < E) atomicAdd(&s_cnt[ev[q]], 1);   // integer: the order does not matter
+        }
         __syncthreads();
         float* fo = fpart + (int64_t)(blockIdx.x + s) * stride;
         int32_t* io = ipart + (int64_t)(blockIdx.x + s) * stride;
-        for (int e = tid; e < E + 2; e += NT) {
-            io[e] = s_cnt[e];
-            if (e < E) {
-                float v = s_p[0][e];
+        for (int e = tid; e <= E; e += NT) {
+            float v = e < E ? s_p[0][e] : s_z[0];
+            int c = e < E ? s_cnt[e] : s_n[0];
 #pragma unroll
-                for (int w = 1; w < NT / 64; ++w) v += s_p[w][e];
-                fo[e] = v;
-            } else if (e == E) {
-                float v = s_z[0];
-#pragma unroll
-                for (int w = 1; w < NT / 64; ++w) v += s_z[w];
-                fo[e] = v;
+            for (int w = 1; w < NT / 64; ++w) {
+                v += e < E ? s_p[w][e] : s_z[w];
+                c += e < E ? 0 : s_n[w];
             }
+            fo[e] = v;
+            io[e] = c;
         }
         __syncthreads();   // the next piece clears the counts
     });
     if (bad && dev_err) atomicOr(dev_err, (int)MOE_ERR_NONFINITE_LOGIT);
 }
 
-// Workgroup (s, g): columns of sequence s: experts EG*g .. EG*g + EG-1, then
-// its tokens, its pairs and its sum of lse^2.  32 columns x 32 rows at a time.
-constexpr int RT = 1024, EG = 29;
+// One workgroup per sequence: the sums of its pieces' rows, R rows at a time
+// (a thread takes 4 columns of every R-th row), then R to 1 through LDS.  With
+// one sequence it also makes the losses; else the last workgroup to finish does.
+constexpr int RT = 1024;
 
 __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, float cz,
-                                                            const float* __restrict__ fpart,
-                                                            const int32_t* __restrict__ ipart,
+                                                            const float4* __restrict__ fpart,
+                                                            const int4* __restrict__ ipart,
                                                             int* __restrict__ ticket, float* __restrict__ partial,
                                                             float* __restrict__ losses, int32_t* __restrict__ counts,
                                                             float* __restrict__ probs, int32_t* __restrict__ tokens)
 {
-    __shared__ float s_f[32][33];
-    __shared__ int s_i[32][33];
+    __shared__ float4 s_f[RT];
+    __shared__ int4 s_i[RT];
     __shared__ double s_b[RT / 64], s_zz[RT / 64];
     __shared__ int s_n[RT / 64];
     __shared__ int s_last;
-    const int s = blockIdx.x, g = blockIdx.y, ng = gridDim.y;
-    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-    const int E = a.E, stride = row_stride(E);
+    const int s = blockIdx.x, tid = threadIdx.x;
+    const int E = a.E, nv = row_stride(E) / 4;
     const int begin = seg_at(a, s), end = seg_at(a, s + 1);
     const int b0 = begin / a.TB, b1 = end > begin ? (end - 1) / a.TB + 1 : b0;
-    // column of the float row and of the integer row this thread sums
-    const int e = g * EG + c;
-    const int fc = c < EG ? (e < E ? e : -1) : (c == EG + 2 ? E : -1);
-    const int ic = c < EG ? (e < E ? e : -1) : (c < EG + 2 ? E + (c - EG) : -1);
-    float fv = 0.0f;
-    int iv = 0;
-#pragma unroll 8
-    for (int b = b0 + r; b < b1; b += 32) {
-        const int64_t row = (int64_t)(b + s) * stride;
-        if (fc >= 0) fv += fpart[row + fc];
-        if (ic >= 0) iv += ipart[row + ic];
+    int R = 1;   // a power of two, for the steps below
+    while (2 * R * nv <= RT && R < b1 - b0) R *= 2;
+    const int c = tid % nv, r = tid / nv;
+    float4 fv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int4 iv = make_int4(0, 0, 0, 0);
+    if (r < R) {
+#pragma unroll 4
+        for (int b = b0 + r; b < b1; b += R) {
+            const int64_t at = (int64_t)(b + s) * nv + c;
+            const float4 f = fpart[at];
+            const int4 i = ipart[at];
+            fv.x += f.x;
+            fv.y += f.y;
+            fv.z += f.z;
+            fv.w += f.w;
+            iv.x += i.x;
+            iv.y += i.y;
+            iv.z += i.z;
+            iv.w += i.w;
+        }
+        s_f[tid] = fv;
+        s_i[tid] = iv;
     }
-    s_f[r][c] = fv;
-    s_i[r][c] = iv;
     __syncthreads();
-#pragma unroll
-    for (int h = 16; h >= 1; h >>= 1) {
+    for (int h = R / 2; h >= 1; h /= 2) {
         if (r < h) {
-            s_f[r][c] += s_f[r + h][c];
-            s_i[r][c] += s_i[r + h][c];
+            const float4 f = s_f[tid + h * nv];
+            const int4 i = s_i[tid + h * nv];
+            fv.x += f.x;
+            fv.y += f.y;
+            fv.z += f.z;
+            fv.w += f.w;
+            iv.x += i.x;
+            iv.y += i.y;
+            iv.z += i.z;
+            iv.w += i.w;
+            s_f[tid] = fv;
+            s_i[tid] = iv;
         }
         __syncthreads();
     }
-    if (threadIdx.x < 64) {
-        const int n = s_i[0][EG], m = s_i[0][EG + 1];
-        float part = 0.0f;
-        if (threadIdx.x < EG && e < E) {
-            const int cnt = s_i[0][c];
-            counts[(int64_t)s * E + e] = cnt;
-            probs[(int64_t)s * E + e] = n ? s_f[0][c] / (float)n : 0.0f;
-            part = m ? (float)cnt / (float)m * s_f[0][c] : 0.0f;   // n_s f_se P_se
-        }
-        part = segment_sum<32>(part);
-        if (threadIdx.x == 0) {
-            float* o = partial + ((int64_t)s * ng + g) * 2;
-            o[0] = part;
-            o[1] = g == 0 ? s_f[0][EG + 2] : 0.0f;
-            if (g == 0) tokens[s] = n;
-            __threadfence();
-            s_last = atomicAdd(ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
-        }
+    // row 0: the sums of p and the pairs per expert, then sum lse^2; tokens and pairs
+    const float* sum = reinterpret_cast<const float*>(s_f);
+    const int* cnt = reinterpret_cast<const int*>(s_i);
+    const int n = cnt[E];
+    const float rn = n ? 1.0f / (float)n : 0.0f;
+    double vb = 0.0;
+    int m = 0;
+    for (int e = tid; e < E; e += RT) {
+        counts[(int64_t)s * E + e] = cnt[e];
+        probs[(int64_t)s * E + e] = sum[e] * rn;
+        vb += (double)cnt[e] * sum[e];                        // m n_s f_se P_se, m the pairs
+        m += cnt[e];
     }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    // the last workgroup: all partial losses, in an order of their own
-    double vb = 0.0, vz = 0.0;
-    int n = 0;
-    for (int64_t i = threadIdx.x; i < (int64_t)a.S * ng; i += RT) {
-        vb += __hip_atomic_load(partial + 2 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        vz += __hip_atomic_load(partial + 2 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    for (int i = threadIdx.x; i < a.S; i += RT) n += __hip_atomic_load(tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // sums over the workgroup, in a fixed order
+    auto block_sum = [&](double& b, double& z, int& k) __attribute__((always_inline)) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-        vb += __shfl_xor(vb, off, 64);
-        vz += __shfl_xor(vz, off, 64);
-        n += __shfl_xor(n, off, 64);
-    }
-    if ((threadIdx.x & 63) == 0) {
-        s_b[threadIdx.x >> 6] = vb;
-        s_zz[threadIdx.x >> 6] = vz;
-        s_n[threadIdx.x >> 6] = n;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < RT / 64; ++w) {
-            s_b[0] += s_b[w];
-            s_zz[0] += s_zz[w];
-            s_n[0] += s_n[w];
+        for (int off = 32; off >= 1; off >>= 1) {
+            b += __shfl_xor(b, off, 64);
+            z += __shfl_xor(z, off, 64);
+            k += __shfl_xor(k, off, 64);
         }
-        const double inv = s_n[0] ? 1.0 / s_n[0] : 0.0;
-        losses[0] = (float)((double)cb * E * inv * s_b[0]);
+        if ((tid & 63) == 0) {
+            s_b[tid >> 6] = b;
+            s_zz[tid >> 6] = z;
+            s_n[tid >> 6] = k;
+        }
+        __syncthreads();
+        b = z = 0.0;
+        k = 0;
+        for (int w = 0; w < RT / 64; ++w) {
+            b += s_b[w];
+            z += s_zz[w];
+            k += s_n[w];
+        }
+        __syncthreads();
+    };
+    double vz = tid == 0 ? (double)sum[E] : 0.0;
+    int vn = n;
+    block_sum(vb, vz, m);
+    vb = m ? vb / m : 0.0;
+    if (a.S > 1) {
+        if (tid == 0) {
+            partial[2 * s] = (float)vb;
+            partial[2 * s + 1] = (float)vz;
+            tokens[s] = n;
+            __threadfence();
+            s_last = atomicAdd(ticket, 1) == a.S - 1;
+        }
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        vb = vz = 0.0;
+        vn = 0;
+        // (each sequence's sums were rounded to 32 bits once)
+        for (int i = tid; i < a.S; i += RT) {
+            vb += __hip_atomic_load(partial + 2 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            vz += __hip_atomic_load(partial + 2 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            vn += __hip_atomic_load(tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        block_sum(vb, vz, vn);
+    } else if (tid == 0) {
+        tokens[0] = n;
+    }
+    if (tid == 0) {
+        const double inv = vn ? 1.0 / vn : 0.0;
+        losses[0] = (float)((double)cb * E * inv * vb);
         // (a row of the type's lowest value has an lse^2 past fp32: no 0 * infinity)
-        losses[1] = cz == 0.0f ? 0.0f : (float)((double)cz * inv * s_zz[0]);
-        tokens[a.S] = s_n[0];
+        losses[1] = cz == 0.0f ? 0.0f : (float)((double)cz * inv * vz);
+        tokens[a.S] = vn;
     }
 }
 
@@ -455,8 +517,7 @@ inline bool vec_ok(int E, const void* p) { return E % 4 == 0 && (reinterpret_cas
 
 size_t balance_ws_bytes(int T, int E, int S)
 {
-    const int64_t ng = (E + EG - 1) / EG;
-    return kTicketBytes + (size_t)(S * ng * 2 * 4 + 255) / 256 * 256 + (size_t)piece_rows(T, S) * row_stride(E) * 8;
+    return kTicketBytes + ((size_t)S * 2 * 4 + 255) / 256 * 256 + (size_t)piece_rows(T, S) * row_stride(E) * 8;
 }
 
 hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, const int32_t* seg_off,
@@ -464,19 +525,19 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
                           float* probs, float* lse, int32_t* tokens, void* ws, int32_t* dev_err, hipStream_t s)
 {
     const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T)};
-    const int ng = (E + EG - 1) / EG;
     uint8_t* w = static_cast<uint8_t*>(ws);
     int* ticket = reinterpret_cast<int*>(w);
     float* partial = reinterpret_cast<float*>(w + kTicketBytes);
-    float* fpart = reinterpret_cast<float*>(w + kTicketBytes + (size_t)((int64_t)S * ng * 2 * 4 + 255) / 256 * 256);
+    float* fpart = reinterpret_cast<float*>(w + kTicketBytes + ((size_t)S * 2 * 4 + 255) / 256 * 256);
     int32_t* ipart = reinterpret_cast<int32_t*>(fpart + piece_rows(T, S) * row_stride(E));
     const int nblk = T > 0 ? (T + a.TB - 1) / a.TB : 1;
     with_shape(E, vec_ok(E, logits), [&](auto L, auto N, auto V) {
         hipLaunchKernelGGL((balance_tokens_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value>),
-                           dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k, lse, fpart, ipart, ticket, dev_err);
+                           dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k,
+                           (uint32_t)(((1ull << 32) + k - 1) / k), lse, fpart, ipart, ticket, dev_err);
     });
-    hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S, (unsigned)ng), dim3(RT), 0, s, a, cb, cz, fpart,
-                       ipart, ticket, partial, losses, counts, probs, tokens);
+    hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S), dim3(RT), 0, s, a, cb, cz,
+                       reinterpret_cast<const float4*>(fpart), reinterpret_cast<const int4*>(ipart), ticket, partial, losses, counts, probs, tokens);
     return hipGetLastError();
 }
 

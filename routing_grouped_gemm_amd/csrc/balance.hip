@@ -13,8 +13,9 @@
 //      A run is cut where a sequence ends; the piece of run b in sequence s
 //      leaves its sums in row b + s of the workspace (run and sequence never
 //      decrease from piece to piece and one of them grows, so rows are distinct).
-//   2. balance_reduce_kernel: per sequence, the sums of its pieces' rows in a
-//      fixed order; the last workgroup to finish adds up the losses.
+//   2. balance_reduce_kernel: per sequence and group of experts, the sums of
+//      its pieces' rows in a fixed order; the last workgroup to finish adds up
+//      the losses.
 // Backward, one kernel: the softmax again from the logits (p from a rounded lse
 // would lose |lse| * 2^-24 of relative accuracy).  No floating-point atomics:
 // results are the same bits on every run.
@@ -97,7 +98,13 @@ __device__ __forceinline__ float segment_max(float x)
 // Lane l of a token's LPT holds NCH chunks of 4 experts, chunk q at expert
 // 4 * (q * LPT + l): consecutive lanes on consecutive 16 bytes of the row.
 // VEC: E is a multiple of 4 and rows are 16-byte aligned.
-template <int LPT, int NCH, bool VEC>
+// STREAM: loads and stores that do not displace what the caches hold, for
+// logits that do not fit there (the 256 MB last-level cache) between the
+// forward and the backward anyway.  At 2^20 x 128: forward 113 -> 98 us,
+// backward with an addend 317 -> 303 us; at 2^16 x 128 the backward goes 19.5
+// -> 21.1 us with them.
+typedef __attribute__((ext_vector_type(4))) float vf4;
+template <int LPT, int NCH, bool VEC, bool STREAM>
 struct Row {
     float v[4 * NCH];
     __device__ __forceinline__ static int col(int l, int i) { return 4 * ((i >> 2) * LPT + l) + (i & 3); }
@@ -107,11 +114,11 @@ struct Row {
         for (int q = 0; q < NCH; ++q) {
             const int c = col(l, 4 * q);
             if constexpr (VEC) {
-                const float4 x = c < E ? *reinterpret_cast<const float4*>(row + c) : make_float4(pad, pad, pad, pad);
-                v[4 * q] = x.x;
-                v[4 * q + 1] = x.y;
-                v[4 * q + 2] = x.z;
-                v[4 * q + 3] = x.w;
+                const vf4* at = reinterpret_cast<const vf4*>(row + c);
+                vf4 x = {pad, pad, pad, pad};
+                if (c < E) x = STREAM ? __builtin_nontemporal_load(at) : *at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = x[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[4 * q + i] = c + i < E ? row[c + i] : pad;
@@ -124,7 +131,12 @@ struct Row {
         for (int q = 0; q < NCH; ++q) {
             const int c = col(l, 4 * q);
             if constexpr (VEC) {
-                if (c < E) *reinterpret_cast<float4*>(row + c) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                const vf4 x = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                vf4* at = reinterpret_cast<vf4*>(row + c);
+                if (c < E) {
+                    if constexpr (STREAM) __builtin_nontemporal_store(x, at);
+                    else *at = x;
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -175,27 +187,30 @@ struct Row {
     }
 };
 
-// workspace: the ticket (first 256 bytes), then per piece a row of floats (the
-// sums of p, then the sum of lse^2) and a row of counts (pairs per expert,
-// then tokens)
+// workspace: the ticket (first 256 bytes), the reduction's partial losses, then
+// per piece the sums of p and, apart, the pairs per expert, in vectors of 4
+// experts with one more vector at the end: the sum of lse^2; the tokens and the
+// pairs.  Vector v of all pieces is contiguous, so that the reduction reads
+// whole lines.
 constexpr size_t kTicketBytes = 256;
-__host__ __device__ inline int row_stride(int E) { return (E + 4) & ~3; }
+__host__ __device__ inline int last_vector(int E) { return (E + 3) / 4; }
 
-template <int LPT, int NCH, bool VEC>
+template <int LPT, int NCH, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int32_t* __restrict__ topk_idx, int k,
                                                             uint32_t over_k,   // ceil(2^32 / k), k > 1
-                                                            float* __restrict__ lse_out, float* __restrict__ fpart,
-                                                            int32_t* __restrict__ ipart, int* __restrict__ ticket,
+                                                            float* __restrict__ lse_out, float4* __restrict__ fpart,
+                                                            int4* __restrict__ ipart, int rows,
+                                                            int* __restrict__ ticket,
                                                             int32_t* __restrict__ dev_err)
 {
     constexpr int NG = NT / LPT, GW = 64 / LPT;   // lane groups per workgroup, per wave
     constexpr int U = NCH == 1 ? 4 : 2;           // tokens in flight per group
     __shared__ float s_p[NT / 64][kMaxExperts];
     __shared__ float s_z[NT / 64];
-    __shared__ int s_n[NT / 64];
+    __shared__ int s_n[NT / 64], s_m[NT / 64];
     __shared__ int s_cnt[kMaxExperts];
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT, wave = tid >> 6;
-    const int E = a.E, stride = row_stride(E);
+    const int E = a.E, vl = last_vector(E);
     if (blockIdx.x == 0 && tid == 0) *ticket = 0;
     const int t0 = blockIdx.x * a.TB, t1 = min(t0 + a.TB, a.T);
     bool bad = false;
@@ -227,7 +242,7 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
 #pragma unroll
         for (int i = 0; i < 4 * NCH; ++i) sum[i] = 0.0f;
         for (int t = begin + grp; t < end; t += NG * U) {
-            Row<LPT, NCH, VEC> r[U];
+            Row<LPT, NCH, VEC, STREAM> r[U];
             bool on[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -261,173 +276,179 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
         if (grp % GW == 0) {
 #pragma unroll
             for (int i = 0; i < 4 * NCH; ++i)
-                if (Row<LPT, NCH, VEC>::col(l, i) < E) s_p[wave][Row<LPT, NCH, VEC>::col(l, i)] = sum[i];
+                if (Row<LPT, NCH, VEC, STREAM>::col(l, i) < E) s_p[wave][Row<LPT, NCH, VEC, STREAM>::col(l, i)] = sum[i];
             if (l == 0) {
                 s_z[wave] = z;
                 s_n[wave] = n;
             }
         }
         __syncthreads();   // s_cnt is clear, too
-        for (int i0 = tid; i0 < pairs; i0 += NT * PQ) {
+        int m = 0;   // the wave's pairs
+        for (int i0 = tid; i0 - tid < pairs; i0 += NT * PQ) {
             if (i0 != tid) load_pairs(i0, ev);
 #pragma unroll
-            for (int q = 0; q < PQ; ++q)
-                if (ev[q] >= 0 && ev[q] < E) atomicAdd(&s_cnt[ev[q]], 1);   // integer: the order does not matter
+            for (int q = 0; q < PQ; ++q) {
+                const bool valid = ev[q] >= 0 && ev[q] < E;
+                if (valid) atomicAdd(&s_cnt[ev[q]], 1);   // integer: the order does not matter
+                m += __popcll(__ballot(valid));
+            }
         }
+        if ((tid & 63) == 0) s_m[wave] = m;
         __syncthreads();
-        float* fo = fpart + (int64_t)(blockIdx.x + s) * stride;
-        int32_t* io = ipart + (int64_t)(blockIdx.x + s) * stride;
-        for (int e = tid; e <= E; e += NT) {
-            float v = e < E ? s_p[0][e] : s_z[0];
-            int c = e < E ? s_cnt[e] : s_n[0];
+        const int64_t piece = (int64_t)blockIdx.x + s;
+        for (int v = tid; v < vl; v += NT) {
+            float f[4];
+            int c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = min(4 * v + i, E - 1);   // (past E: nobody looks)
+                f[i] = s_p[0][e];
+#pragma unroll
+                for (int w = 1; w < NT / 64; ++w) f[i] += s_p[w][e];
+                c[i] = s_cnt[e];
+            }
+            fpart[v * (int64_t)rows + piece] = make_float4(f[0], f[1], f[2], f[3]);
+            ipart[v * (int64_t)rows + piece] = make_int4(c[0], c[1], c[2], c[3]);
+        }
+        if (tid == NT - 1) {
+            float v = s_z[0];
+            int nn = s_n[0], mm = s_m[0];
 #pragma unroll
             for (int w = 1; w < NT / 64; ++w) {
-                v += e < E ? s_p[w][e] : s_z[w];
-                c += e < E ? 0 : s_n[w];
+                v += s_z[w];
+                nn += s_n[w];
+                mm += s_m[w];
             }
-            fo[e] = v;
-            io[e] = c;
+            fpart[vl * (int64_t)rows + piece] = make_float4(v, 0.0f, 0.0f, 0.0f);
+            ipart[vl * (int64_t)rows + piece] = make_int4(nn, mm, 0, 0);
         }
         __syncthreads();   // the next piece clears the counts
     });
     if (bad && dev_err) atomicOr(dev_err, (int)MOE_ERR_NONFINITE_LOGIT);
 }
 
-// One workgroup per sequence: the sums of its pieces' rows, R rows at a time
-// (a thread takes 4 columns of every R-th row), then R to 1 through LDS.  With
-// one sequence it also makes the losses; else the last workgroup to finish does.
-constexpr int RT = 1024;
+// Workgroup (s, g): the sums of sequence s's pieces' rows over RW - 1 4-column
+// vectors (group g of them) and the rows' last vector: a wave per vector, a lane per row (every 64th), then the lanes.  The
+// last workgroup to finish makes the losses from what each left in `partial`.
+constexpr int RW = 8, RT = 64 * RW;
+
+struct Partial {
+    float b, z;      // its experts' n f P; sum of lse^2 (group 0, else 0)
+};
+
+template <int L>
+__device__ __forceinline__ int segment_sum(int x)
+{
+#pragma unroll
+    for (int off = 1; off < L; off <<= 1) x += __shfl_xor(x, off, 64);
+    return x;
+}
 
 __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, float cz,
                                                             const float4* __restrict__ fpart,
-                                                            const int4* __restrict__ ipart,
-                                                            int* __restrict__ ticket, float* __restrict__ partial,
+                                                            const int4* __restrict__ ipart, int rows,
+                                                            int* __restrict__ ticket, Partial* __restrict__ partial,
                                                             float* __restrict__ losses, int32_t* __restrict__ counts,
                                                             float* __restrict__ probs, int32_t* __restrict__ tokens)
 {
-    __shared__ float4 s_f[RT];
-    __shared__ int4 s_i[RT];
-    __shared__ double s_b[RT / 64], s_zz[RT / 64];
-    __shared__ int s_n[RT / 64];
+    __shared__ float s_f[RW][4];
+    __shared__ int s_i[RW][4];
+    __shared__ float s_b[RW], s_z[RW];
+    __shared__ int s_n[RW];
     __shared__ int s_last;
-    const int s = blockIdx.x, tid = threadIdx.x;
-    const int E = a.E, nv = row_stride(E) / 4;
+    const int s = blockIdx.x, g = blockIdx.y, ng = gridDim.y, tid = threadIdx.x;
+    const int lane = tid & 63, wave = tid >> 6;
+    const int E = a.E, vl = last_vector(E);
     const int begin = seg_at(a, s), end = seg_at(a, s + 1);
     const int b0 = begin / a.TB, b1 = end > begin ? (end - 1) / a.TB + 1 : b0;
-    int R = 1;   // a power of two, for the steps below
-    while (2 * R * nv <= RT && R < b1 - b0) R *= 2;
-    const int c = tid % nv, r = tid / nv;
-    float4 fv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    int4 iv = make_int4(0, 0, 0, 0);
-    if (r < R) {
+    const int v = wave < RW - 1 ? g * (RW - 1) + wave : vl;
+    if (wave == RW - 1 || v < vl) {
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        int c[4] = {0, 0, 0, 0};
 #pragma unroll 4
-        for (int b = b0 + r; b < b1; b += R) {
-            const int64_t at = (int64_t)(b + s) * nv + c;
-            const float4 f = fpart[at];
+        for (int b = b0 + lane; b < b1; b += 64) {
+            const int64_t at = v * (int64_t)rows + b + s;
+            const float4 x = fpart[at];
             const int4 i = ipart[at];
-            fv.x += f.x;
-            fv.y += f.y;
-            fv.z += f.z;
-            fv.w += f.w;
-            iv.x += i.x;
-            iv.y += i.y;
-            iv.z += i.z;
-            iv.w += i.w;
+            f[0] += x.x;
+            f[1] += x.y;
+            f[2] += x.z;
+            f[3] += x.w;
+            c[0] += i.x;
+            c[1] += i.y;
+            c[2] += i.z;
+            c[3] += i.w;
         }
-        s_f[tid] = fv;
-        s_i[tid] = iv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = segment_sum<64>(f[i]);
+            c[i] = segment_sum<64>(c[i]);
+            if (lane == 0) {
+                s_f[wave][i] = f[i];
+                s_i[wave][i] = c[i];
+            }
+        }
     }
     __syncthreads();
-    for (int h = R / 2; h >= 1; h /= 2) {
-        if (r < h) {
-            const float4 f = s_f[tid + h * nv];
-            const int4 i = s_i[tid + h * nv];
-            fv.x += f.x;
-            fv.y += f.y;
-            fv.z += f.z;
-            fv.w += f.w;
-            iv.x += i.x;
-            iv.y += i.y;
-            iv.z += i.z;
-            iv.w += i.w;
-            s_f[tid] = fv;
-            s_i[tid] = iv;
+    const int n = s_i[RW - 1][0], m = s_i[RW - 1][1];
+    if (wave == 0) {
+        const int w = lane >> 2, e = 4 * (g * (RW - 1) + w) + (lane & 3);
+        float vb = 0.0f;
+        if (w < RW - 1 && e < E) {
+            const float p = s_f[w][lane & 3];
+            const int c = s_i[w][lane & 3];
+            counts[(int64_t)s * E + e] = c;
+            probs[(int64_t)s * E + e] = n ? p / (float)n : 0.0f;
+            vb = m ? (float)c / (float)m * p : 0.0f;          // n f P
         }
-        __syncthreads();
+        vb = segment_sum<32>(vb);
+        // What passes between workgroups does so through device-scope atomics
+        // alone, which are performed where all XCDs see them: each exchange has
+        // been when its old value is back, and the ticket is taken after that.
+        // (With plain stores between fences the kernel took 4 us longer: a
+        // release writes back the XCD's whole L2.)
+        if (lane == 0) {
+            Partial* q = partial + s * ng + g;
+            const int o0 = atomicExch(reinterpret_cast<int*>(&q->b), __float_as_int(vb));
+            const int o1 = atomicExch(reinterpret_cast<int*>(&q->z), __float_as_int(g == 0 ? s_f[RW - 1][0] : 0.0f));
+            const int o2 = g == 0 ? atomicExch(tokens + s, n) : 0;
+            asm volatile("" :: "v"(o0), "v"(o1), "v"(o2) : "memory");
+            s_last = atomicAdd(ticket, 1) == a.S * ng - 1;
+        }
     }
-    // row 0: the sums of p and the pairs per expert, then sum lse^2; tokens and pairs
-    const float* sum = reinterpret_cast<const float*>(s_f);
-    const int* cnt = reinterpret_cast<const int*>(s_i);
-    const int n = cnt[E];
-    const float rn = n ? 1.0f / (float)n : 0.0f;
-    double vb = 0.0;
-    int m = 0;
-    for (int e = tid; e < E; e += RT) {
-        counts[(int64_t)s * E + e] = cnt[e];
-        probs[(int64_t)s * E + e] = sum[e] * rn;
-        vb += (double)cnt[e] * sum[e];                        // m n_s f_se P_se, m the pairs
-        m += cnt[e];
+    __syncthreads();
+    if (!s_last) return;
+    float vb = 0.0f, vz = 0.0f;
+    int N = 0;
+    for (int i = tid; i < a.S * ng; i += RT) {
+        vb += __hip_atomic_load(&partial[i].b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        vz += __hip_atomic_load(&partial[i].z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (i < a.S) N += __hip_atomic_load(tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    // sums over the workgroup, in a fixed order
-    auto block_sum = [&](double& b, double& z, int& k) __attribute__((always_inline)) {
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            b += __shfl_xor(b, off, 64);
-            z += __shfl_xor(z, off, 64);
-            k += __shfl_xor(k, off, 64);
-        }
-        if ((tid & 63) == 0) {
-            s_b[tid >> 6] = b;
-            s_zz[tid >> 6] = z;
-            s_n[tid >> 6] = k;
-        }
-        __syncthreads();
-        b = z = 0.0;
-        k = 0;
-        for (int w = 0; w < RT / 64; ++w) {
-            b += s_b[w];
-            z += s_zz[w];
-            k += s_n[w];
-        }
-        __syncthreads();
-    };
-    double vz = tid == 0 ? (double)sum[E] : 0.0;
-    int vn = n;
-    block_sum(vb, vz, m);
-    vb = m ? vb / m : 0.0;
-    if (a.S > 1) {
-        if (tid == 0) {
-            partial[2 * s] = (float)vb;
-            partial[2 * s + 1] = (float)vz;
-            tokens[s] = n;
-            __threadfence();
-            s_last = atomicAdd(ticket, 1) == a.S - 1;
-        }
-        __syncthreads();
-        if (!s_last) return;
-        __threadfence();
-        vb = vz = 0.0;
-        vn = 0;
-        // (each sequence's sums were rounded to 32 bits once)
-        for (int i = tid; i < a.S; i += RT) {
-            vb += __hip_atomic_load(partial + 2 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            vz += __hip_atomic_load(partial + 2 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            vn += __hip_atomic_load(tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-        block_sum(vb, vz, vn);
-    } else if (tid == 0) {
-        tokens[0] = n;
+    vb = segment_sum<64>(vb);
+    vz = segment_sum<64>(vz);
+    N = segment_sum<64>(N);
+    if (lane == 0) {
+        s_b[wave] = vb;
+        s_z[wave] = vz;
+        s_n[wave] = N;
     }
+    __syncthreads();
     if (tid == 0) {
-        const double inv = vn ? 1.0 / vn : 0.0;
-        losses[0] = (float)((double)cb * E * inv * vb);
+        for (int w = 1; w < RW; ++w) {
+            vb += s_b[w];
+            vz += s_z[w];
+            N += s_n[w];
+        }
+        const float inv = N ? 1.0f / (float)N : 0.0f;
+        losses[0] = cb * (float)E * inv * vb;
         // (a row of the type's lowest value has an lse^2 past fp32: no 0 * infinity)
-        losses[1] = cz == 0.0f ? 0.0f : (float)((double)cz * inv * vz);
-        tokens[a.S] = vn;
+        losses[1] = cz == 0.0f ? 0.0f : cz * inv * vz;
+        tokens[a.S] = N;
     }
 }
 
-template <int LPT, int NCH, bool VEC>
+template <int LPT, int NCH, bool VEC, bool STREAM>
 __global__ __launch_bounds__(NT) void balance_bwd_kernel(Tokens a, const int32_t* __restrict__ counts,
                                                          const int32_t* __restrict__ tokens, float cb, float cz,
                                                          const float* __restrict__ dlosses, const float* add,
@@ -435,7 +456,7 @@ __global__ __launch_bounds__(NT) void balance_bwd_kernel(Tokens a, const int32_t
 {
     constexpr int NG = NT / LPT;
     constexpr int U = NCH == 1 ? 4 : 2;
-    using R = Row<LPT, NCH, VEC>;
+    using R = Row<LPT, NCH, VEC, STREAM>;
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
     const int E = a.E;
     const int t0 = blockIdx.x * a.TB, t1 = min(t0 + a.TB, a.T);
@@ -483,19 +504,24 @@ __global__ __launch_bounds__(NT) void balance_bwd_kernel(Tokens a, const int32_t
     });
 }
 
-// tokens per workgroup: 64, or as many as leave 1024 workgroups
-int tokens_per_block(int T)
+// tokens per workgroup: 64, or as many as leave `most` workgroups
+int tokens_per_block(int T, int most)
 {
-    const int64_t tb = ((int64_t)T + 1023) / 1024;
-    return (int)((tb + 63) / 64 * 64 > 64 ? (tb + 63) / 64 * 64 : 64);
+    const int64_t tb = (((int64_t)T + most - 1) / most + 15) / 16 * 16;
+    return (int)(tb > 64 ? tb : 64);
 }
+// forward: two workgroups per CU, since each leaves a row of sums to add up
+// (2^16 tokens of 128 experts: 29 us with 1024 workgroups, 17 with 512)
+constexpr int kMostFwd = 512, kMostBwd = 1024;
 
 template <class F>
-void with_shape(int E, bool vec, F&& f)
+void with_shape(int T, int E, bool vec, F&& f)
 {
+    const bool stream = (int64_t)T * E * 4 >= ((int64_t)256 << 20);
     auto go = [&](auto L, auto N) {
-        if (vec) f(L, N, std::true_type{});
-        else f(L, N, std::false_type{});
+        if (vec && stream) f(L, N, std::true_type{}, std::true_type{});
+        else if (vec) f(L, N, std::true_type{}, std::false_type{});
+        else f(L, N, std::false_type{}, std::false_type{});
     };
     using std::integral_constant;
     if (E <= 4) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
@@ -509,7 +535,20 @@ void with_shape(int E, bool vec, F&& f)
     else go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
 
-inline int64_t piece_rows(int T, int S) { return ((int64_t)T + tokens_per_block(T) - 1) / tokens_per_block(T) + S; }
+inline int64_t piece_rows(int T, int S)
+{
+    const int tb = tokens_per_block(T, kMostFwd);
+    return ((int64_t)T + tb - 1) / tb + S;
+}
+
+inline int reduce_groups(int E)
+{
+    return (last_vector(E) + RW - 2) / (RW - 1);
+}
+inline size_t partial_bytes(int E, int S)
+{
+    return ((size_t)S * reduce_groups(E) * sizeof(Partial) + 255) / 256 * 256;
+}
 
 inline bool vec_ok(int E, const void* p) { return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -517,27 +556,30 @@ inline bool vec_ok(int E, const void* p) { return E % 4 == 0 && (reinterpret_cas
 
 size_t balance_ws_bytes(int T, int E, int S)
 {
-    return kTicketBytes + ((size_t)S * 2 * 4 + 255) / 256 * 256 + (size_t)piece_rows(T, S) * row_stride(E) * 8;
+    return kTicketBytes + partial_bytes(E, S) + (size_t)piece_rows(T, S) * (last_vector(E) + 1) * 32;
 }
 
 hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const uint8_t* mask, const int32_t* seg_off,
                           int S, int T, int E, int k, float cb, float cz, float* losses, int32_t* counts,
                           float* probs, float* lse, int32_t* tokens, void* ws, int32_t* dev_err, hipStream_t s)
 {
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kMostFwd)};
     uint8_t* w = static_cast<uint8_t*>(ws);
     int* ticket = reinterpret_cast<int*>(w);
-    float* partial = reinterpret_cast<float*>(w + kTicketBytes);
-    float* fpart = reinterpret_cast<float*>(w + kTicketBytes + ((size_t)S * 2 * 4 + 255) / 256 * 256);
-    int32_t* ipart = reinterpret_cast<int32_t*>(fpart + piece_rows(T, S) * row_stride(E));
+    Partial* partial = reinterpret_cast<Partial*>(w + kTicketBytes);
+    const int rows = (int)piece_rows(T, S);
+    float4* fpart = reinterpret_cast<float4*>(w + kTicketBytes + partial_bytes(E, S));
+    int4* ipart = reinterpret_cast<int4*>(fpart + (int64_t)rows * (last_vector(E) + 1));
     const int nblk = T > 0 ? (T + a.TB - 1) / a.TB : 1;
-    with_shape(E, vec_ok(E, logits), [&](auto L, auto N, auto V) {
-        hipLaunchKernelGGL((balance_tokens_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value>),
+    with_shape(T, E, vec_ok(E, logits), [&](auto L, auto N, auto V, auto ST) {
+        hipLaunchKernelGGL((balance_tokens_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value,
+                            decltype(ST)::value>),
                            dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k,
-                           (uint32_t)(((1ull << 32) + k - 1) / k), lse, fpart, ipart, ticket, dev_err);
+                           (uint32_t)(((1ull << 32) + k - 1) / k), lse, fpart, ipart, rows, ticket, dev_err);
     });
-    hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S), dim3(RT), 0, s, a, cb, cz,
-                       reinterpret_cast<const float4*>(fpart), reinterpret_cast<const int4*>(ipart), ticket, partial, losses, counts, probs, tokens);
+    hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S, (unsigned)reduce_groups(E)), dim3(RT),
+                       0, s, a, cb, cz,
+                       fpart, ipart, rows, ticket, partial, losses, counts, probs, tokens);
     return hipGetLastError();
 }
 
@@ -546,11 +588,12 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
                               const float* add, float* dlogits, hipStream_t s)
 {
     if (T == 0) return hipSuccess;
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kMostBwd)};
     const int nblk = (T + a.TB - 1) / a.TB;
     const bool vec = vec_ok(E, logits) && vec_ok(E, dlogits) && vec_ok(E, add);
-    with_shape(E, vec, [&](auto L, auto N, auto V) {
-        hipLaunchKernelGGL((balance_bwd_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value>),
+    with_shape(T, E, vec, [&](auto L, auto N, auto V, auto ST) {
+        hipLaunchKernelGGL((balance_bwd_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value,
+                            decltype(ST)::value>),
                            dim3((unsigned)nblk), dim3(NT), 0, s, a, counts, tokens, cb, cz, dlosses, add, dlogits);
     });
     return hipGetLastError();

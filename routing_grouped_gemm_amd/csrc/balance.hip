@@ -19,6 +19,7 @@
 // Backward, one kernel: the softmax again from the logits (p from a rounded lse
 // would lose |lse| * 2^-24 of relative accuracy).  No floating-point atomics:
 // results are the same bits on every run.
+#include <algorithm>
 #include <type_traits>
 
 #include "moe_internal.h"
@@ -26,7 +27,7 @@
 namespace moe {
 namespace {
 
-constexpr int NT = 512;
+constexpr int NT = 512, NTB = 256;   // threads of the forward's and the backward's workgroups
 
 struct Tokens {
     const float* logits;
@@ -449,12 +450,12 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, 
 }
 
 template <int LPT, int NCH, bool VEC, bool STREAM>
-__global__ __launch_bounds__(NT) void balance_bwd_kernel(Tokens a, const int32_t* __restrict__ counts,
+__global__ __launch_bounds__(NTB) void balance_bwd_kernel(Tokens a, const int32_t* __restrict__ counts,
                                                          const int32_t* __restrict__ tokens, float cb, float cz,
                                                          const float* __restrict__ dlosses, const float* add,
                                                          float* dlogits)
 {
-    constexpr int NG = NT / LPT;
+    constexpr int NG = NTB / LPT;
     constexpr int U = NCH == 1 ? 4 : 2;
     using R = Row<LPT, NCH, VEC, STREAM>;
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT;
@@ -504,15 +505,26 @@ __global__ __launch_bounds__(NT) void balance_bwd_kernel(Tokens a, const int32_t
     });
 }
 
-// tokens per workgroup: 64, or as many as leave `most` workgroups
-int tokens_per_block(int T, int most)
+// tokens per workgroup: `least`, or as many as leave `most` workgroups
+int tokens_per_block(int T, int least, int most)
 {
     const int64_t tb = (((int64_t)T + most - 1) / most + 15) / 16 * 16;
-    return (int)(tb > 64 ? tb : 64);
+    return (int)(tb > least ? tb : least);
 }
 // forward: two workgroups per CU, since each leaves a row of sums to add up
 // (2^16 tokens of 128 experts: 29 us with 1024 workgroups, 17 with 512)
-constexpr int kMostFwd = 512, kMostBwd = 1024;
+constexpr int kLeastFwd = 64, kMostFwd = 512;
+// backward: 32 KB of logits a workgroup, nothing to add up after it (2^20
+// tokens of 128 experts, with the gradient added on: 263 us; 64 KB 283, 128 KB
+// 303; of 16: 32.5, 33.0, 33.9), at least 32 tokens, and 512 workgroups before
+// they grow past that
+constexpr int kLeastBwd = 32, kElemsBwd = 8192, kFillBwd = 512;
+int tokens_per_block_bwd(int T, int E)
+{
+    int64_t tb = kElemsBwd / E;
+    tb = std::min<int64_t>(tb, T / kFillBwd) / 16 * 16;
+    return (int)(tb > kLeastBwd ? tb : kLeastBwd);
+}
 
 template <class F>
 void with_shape(int T, int E, bool vec, F&& f)
@@ -537,7 +549,7 @@ void with_shape(int T, int E, bool vec, F&& f)
 
 inline int64_t piece_rows(int T, int S)
 {
-    const int tb = tokens_per_block(T, kMostFwd);
+    const int tb = tokens_per_block(T, kLeastFwd, kMostFwd);
     return ((int64_t)T + tb - 1) / tb + S;
 }
 
@@ -563,7 +575,7 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
                           int S, int T, int E, int k, float cb, float cz, float* losses, int32_t* counts,
                           float* probs, float* lse, int32_t* tokens, void* ws, int32_t* dev_err, hipStream_t s)
 {
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kMostFwd)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kLeastFwd, kMostFwd)};
     uint8_t* w = static_cast<uint8_t*>(ws);
     int* ticket = reinterpret_cast<int*>(w);
     Partial* partial = reinterpret_cast<Partial*>(w + kTicketBytes);
@@ -588,13 +600,13 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
                               const float* add, float* dlogits, hipStream_t s)
 {
     if (T == 0) return hipSuccess;
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kMostBwd)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block_bwd(T, E)};
     const int nblk = (T + a.TB - 1) / a.TB;
     const bool vec = vec_ok(E, logits) && vec_ok(E, dlogits) && vec_ok(E, add);
     with_shape(T, E, vec, [&](auto L, auto N, auto V, auto ST) {
         hipLaunchKernelGGL((balance_bwd_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value,
                             decltype(ST)::value>),
-                           dim3((unsigned)nblk), dim3(NT), 0, s, a, counts, tokens, cb, cz, dlosses, add, dlogits);
+                           dim3((unsigned)nblk), dim3(NTB), 0, s, a, counts, tokens, cb, cz, dlosses, add, dlogits);
     });
     return hipGetLastError();
 }

@@ -154,9 +154,9 @@ def _dense(name, t, dtype, *shape):
 def _call(name, stream, tensors, *args):
     """The C entry point `name` on `stream` (None: the current one of the tensors' device), with that
     device current; `tensors` must be on one device.  The stream is the last argument."""
-    dev = tensors[0].device.index
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     fn = getattr(load(), name)
     if dev == torch.cuda.current_device():

@@ -6,7 +6,8 @@
 //   balance = c_b * E * sum_s (n_s / N) sum_e f_se P_se
 //   z       = c_z / N * sum_t lse_t^2,   lse_t = log sum_e exp(logits[t, e])
 //   dlogits = p_te * (g_b c_b E / N (f_se - sum_j f_sj p_tj) + g_z 2 c_z / N lse_t)
-// (the counts are piecewise constant).  Forward, two kernels:
+// (the counts are piecewise constant).  Forward, two kernels (few tokens: the
+// first alone, in a single workgroup that finishes by itself):
 //   1. balance_tokens_kernel: a workgroup takes a run of TB tokens; LPT lanes
 //      hold one token's logits, so its softmax is a few lane exchanges, and
 //      every lane keeps the running sums of p of its experts in registers.
@@ -196,12 +197,30 @@ struct Row {
 constexpr size_t kTicketBytes = 256;
 __host__ __device__ inline int last_vector(int E) { return (E + 3) / 4; }
 
-template <int LPT, int NCH, bool VEC, bool STREAM>
+struct Results {
+    float cb, cz;
+    float* losses;      // [2]
+    int32_t* counts;    // [S, E]
+    float* probs;       // [S, E]
+    int32_t* tokens;    // [S + 1]
+};
+__device__ __forceinline__ void write_losses(const Results& o, int E, int S, float vb, float vz, int N)
+{
+    const float inv = N ? 1.0f / (float)N : 0.0f;
+    o.losses[0] = o.cb * (float)E * inv * vb;
+    // (a row of the type's lowest value has an lse^2 past fp32: no 0 * infinity)
+    o.losses[1] = o.cz == 0.0f ? 0.0f : o.cz * inv * vz;
+    o.tokens[S] = N;
+}
+
+// ONE: a single workgroup has all tokens, so every piece is a whole sequence
+// and its sums are the results.
+template <int LPT, int NCH, bool VEC, bool STREAM, bool ONE>
 __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int32_t* __restrict__ topk_idx, int k,
                                                             uint32_t over_k,   // ceil(2^32 / k), k > 1
                                                             float* __restrict__ lse_out, float4* __restrict__ fpart,
                                                             int4* __restrict__ ipart, int rows,
-                                                            int* __restrict__ ticket,
+                                                            int* __restrict__ ticket, Results o,
                                                             int32_t* __restrict__ dev_err)
 {
     constexpr int NG = NT / LPT, GW = 64 / LPT;   // lane groups per workgroup, per wave
@@ -212,7 +231,18 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
     __shared__ int s_cnt[kMaxExperts];
     const int tid = threadIdx.x, l = tid % LPT, grp = tid / LPT, wave = tid >> 6;
     const int E = a.E, vl = last_vector(E);
-    if (blockIdx.x == 0 && tid == 0) *ticket = 0;
+    float all_b = 0.0f, all_z = 0.0f;   // ONE, wave 0: over the sequences so far
+    int all_n = 0;
+    if constexpr (ONE) {   // sequences without a token
+        for (int64_t i = tid; i < (int64_t)a.S * E; i += NT) {
+            o.counts[i] = 0;
+            o.probs[i] = 0.0f;
+        }
+        for (int i = tid; i < a.S; i += NT) o.tokens[i] = 0;
+        __syncthreads();
+    } else if (blockIdx.x == 0 && tid == 0) {
+        *ticket = 0;
+    }
     const int t0 = blockIdx.x * a.TB, t1 = min(t0 + a.TB, a.T);
     bool bad = false;
     for_pieces(a, t0, t1, [&](int s, int begin, int end) {
@@ -296,10 +326,7 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
         }
         if ((tid & 63) == 0) s_m[wave] = m;
         __syncthreads();
-        const int64_t piece = (int64_t)blockIdx.x + s;
-        for (int v = tid; v < vl; v += NT) {
-            float f[4];
-            int c[4];
+        auto vector = [&](int v, float (&f)[4], int (&c)[4]) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int e = min(4 * v + i, E - 1);   // (past E: nobody looks)
@@ -308,23 +335,57 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
                 for (int w = 1; w < NT / 64; ++w) f[i] += s_p[w][e];
                 c[i] = s_cnt[e];
             }
-            fpart[v * (int64_t)rows + piece] = make_float4(f[0], f[1], f[2], f[3]);
-            ipart[v * (int64_t)rows + piece] = make_int4(c[0], c[1], c[2], c[3]);
-        }
-        if (tid == NT - 1) {
-            float v = s_z[0];
-            int nn = s_n[0], mm = s_m[0];
+        };
+        float zz = 0.0f;
+        int nn = 0, mm = 0;
+        auto scalars = [&]() __attribute__((always_inline)) {
 #pragma unroll
-            for (int w = 1; w < NT / 64; ++w) {
-                v += s_z[w];
+            for (int w = 0; w < NT / 64; ++w) {
+                zz += s_z[w];
                 nn += s_n[w];
                 mm += s_m[w];
             }
-            fpart[vl * (int64_t)rows + piece] = make_float4(v, 0.0f, 0.0f, 0.0f);
-            ipart[vl * (int64_t)rows + piece] = make_int4(nn, mm, 0, 0);
+        };
+        if constexpr (ONE) {
+            if (wave == 0) {
+                scalars();
+                float vb = 0.0f;
+                for (int v = tid; v < vl; v += 64) {
+                    float f[4];
+                    int c[4];
+                    vector(v, f, c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t at = (int64_t)s * E + 4 * v + i;
+                        if (4 * v + i >= E) break;
+                        o.counts[at] = c[i];
+                        o.probs[at] = nn ? f[i] / (float)nn : 0.0f;
+                        vb += mm ? (float)c[i] / (float)mm * f[i] : 0.0f;   // n f P
+                    }
+                }
+                all_b += segment_sum<64>(vb);
+                all_z += zz;
+                all_n += nn;
+                if (tid == 0) o.tokens[s] = nn;
+            }
+        } else {
+            const int64_t piece = (int64_t)blockIdx.x + s;
+            for (int v = tid; v < vl; v += NT) {
+                float f[4];
+                int c[4];
+                vector(v, f, c);
+                fpart[v * (int64_t)rows + piece] = make_float4(f[0], f[1], f[2], f[3]);
+                ipart[v * (int64_t)rows + piece] = make_int4(c[0], c[1], c[2], c[3]);
+            }
+            if (tid == NT - 1) {
+                scalars();
+                fpart[vl * (int64_t)rows + piece] = make_float4(zz, 0.0f, 0.0f, 0.0f);
+                ipart[vl * (int64_t)rows + piece] = make_int4(nn, mm, 0, 0);
+            }
         }
         __syncthreads();   // the next piece clears the counts
     });
+    if (ONE && tid == 0) write_losses(o, E, a.S, all_b, all_z, all_n);
     if (bad && dev_err) atomicOr(dev_err, (int)MOE_ERR_NONFINITE_LOGIT);
 }
 
@@ -345,12 +406,10 @@ __device__ __forceinline__ int segment_sum(int x)
     return x;
 }
 
-__global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, float cz,
-                                                            const float4* __restrict__ fpart,
+__global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, const float4* __restrict__ fpart,
                                                             const int4* __restrict__ ipart, int rows,
                                                             int* __restrict__ ticket, Partial* __restrict__ partial,
-                                                            float* __restrict__ losses, int32_t* __restrict__ counts,
-                                                            float* __restrict__ probs, int32_t* __restrict__ tokens)
+                                                            Results o)
 {
     __shared__ float s_f[RW][4];
     __shared__ int s_i[RW][4];
@@ -398,8 +457,8 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, 
         if (w < RW - 1 && e < E) {
             const float p = s_f[w][lane & 3];
             const int c = s_i[w][lane & 3];
-            counts[(int64_t)s * E + e] = c;
-            probs[(int64_t)s * E + e] = n ? p / (float)n : 0.0f;
+            o.counts[(int64_t)s * E + e] = c;
+            o.probs[(int64_t)s * E + e] = n ? p / (float)n : 0.0f;
             vb = m ? (float)c / (float)m * p : 0.0f;          // n f P
         }
         vb = segment_sum<32>(vb);
@@ -412,7 +471,7 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, 
             Partial* q = partial + s * ng + g;
             const int o0 = atomicExch(reinterpret_cast<int*>(&q->b), __float_as_int(vb));
             const int o1 = atomicExch(reinterpret_cast<int*>(&q->z), __float_as_int(g == 0 ? s_f[RW - 1][0] : 0.0f));
-            const int o2 = g == 0 ? atomicExch(tokens + s, n) : 0;
+            const int o2 = g == 0 ? atomicExch(o.tokens + s, n) : 0;
             asm volatile("" :: "v"(o0), "v"(o1), "v"(o2) : "memory");
             s_last = atomicAdd(ticket, 1) == a.S * ng - 1;
         }
@@ -424,7 +483,7 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, 
     for (int i = tid; i < a.S * ng; i += RT) {
         vb += __hip_atomic_load(&partial[i].b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         vz += __hip_atomic_load(&partial[i].z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (i < a.S) N += __hip_atomic_load(tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (i < a.S) N += __hip_atomic_load(o.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     vb = segment_sum<64>(vb);
     vz = segment_sum<64>(vz);
@@ -441,11 +500,7 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, float cb, 
             vz += s_z[w];
             N += s_n[w];
         }
-        const float inv = N ? 1.0f / (float)N : 0.0f;
-        losses[0] = cb * (float)E * inv * vb;
-        // (a row of the type's lowest value has an lse^2 past fp32: no 0 * infinity)
-        losses[1] = cz == 0.0f ? 0.0f : cz * inv * vz;
-        tokens[a.S] = N;
+        write_losses(o, E, a.S, vb, vz, N);
     }
 }
 
@@ -547,6 +602,13 @@ void with_shape(int T, int E, bool vec, F&& f)
     else go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
 
+// A single workgroup saves the second kernel while it does not take longer
+// than that: with 128 experts 128 tokens take 6.1 us (two kernels 9.2), 256 7.9
+// (9.0), 512 12.0 (9.3); with 8 experts 2048 take 7.0 (8.8), 4096 10.1 (8.4); it
+// takes sequences one after another (256 tokens of 8 experts in two 9.0 us, two
+// kernels 11.6; in three 12.0 and 11.7).
+inline bool one_workgroup(int T, int E, int S) { return (int64_t)T * E <= 32768 && T <= 2048 && S <= 2; }
+
 inline int64_t piece_rows(int T, int S)
 {
     const int tb = tokens_per_block(T, kLeastFwd, kMostFwd);
@@ -575,6 +637,18 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
                           int S, int T, int E, int k, float cb, float cz, float* losses, int32_t* counts,
                           float* probs, float* lse, int32_t* tokens, void* ws, int32_t* dev_err, hipStream_t s)
 {
+    const Results o{cb, cz, losses, counts, probs, tokens};
+    const uint32_t over_k = (uint32_t)(((1ull << 32) + k - 1) / k);
+    if (one_workgroup(T, E, S)) {
+        const Tokens a{logits, mask, seg_off, T, E, S, T};
+        with_shape(T, E, vec_ok(E, logits), [&](auto L, auto N, auto V, auto) {
+            hipLaunchKernelGGL((balance_tokens_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value, false,
+                                true>),
+                               dim3(1), dim3(NT), 0, s, a, topk_idx, k, over_k, lse, nullptr, nullptr, 0, nullptr, o,
+                               dev_err);
+        });
+        return hipGetLastError();
+    }
     const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kLeastFwd, kMostFwd)};
     uint8_t* w = static_cast<uint8_t*>(ws);
     int* ticket = reinterpret_cast<int*>(w);
@@ -585,13 +659,12 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
     const int nblk = T > 0 ? (T + a.TB - 1) / a.TB : 1;
     with_shape(T, E, vec_ok(E, logits), [&](auto L, auto N, auto V, auto ST) {
         hipLaunchKernelGGL((balance_tokens_kernel<decltype(L)::value, decltype(N)::value, decltype(V)::value,
-                            decltype(ST)::value>),
-                           dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k,
-                           (uint32_t)(((1ull << 32) + k - 1) / k), lse, fpart, ipart, rows, ticket, dev_err);
+                            decltype(ST)::value, false>),
+                           dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k, over_k, lse, fpart, ipart, rows, ticket,
+                           o, dev_err);
     });
     hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S, (unsigned)reduce_groups(E)), dim3(RT),
-                       0, s, a, cb, cz,
-                       fpart, ipart, rows, ticket, partial, losses, counts, probs, tokens);
+                       0, s, a, fpart, ipart, rows, ticket, partial, o);
     return hipGetLastError();
 }
 

@@ -20,6 +20,7 @@ int status_of(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 constexpr int64_t kMaxRows = (int64_t)1 << 31;
 constexpr int kMaxMx4Width = 1 << 20;
 constexpr int kMaxSequences = 1 << 20;
+constexpr int kMaxTokens = 1 << 30;   // of the balance loss (token numbers plus a stride stay in 32 bits)
 
 // common validation of a grouped GEMM shape; returns MOE_OK or an error
 int check_gemm_shape(int dtype, const int32_t* group_off, int capacity, int E, int64_t n_rows,
@@ -440,7 +441,7 @@ int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t ro
 
 size_t moe_balance_workspace_bytes(int T, int E, int n_seg)
 {
-    if (T < 0 || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return 0;
+    if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return 0;
     return balance_ws_bytes(T, E, n_seg);
 }
 
@@ -449,7 +450,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t
                      int32_t* counts, float* probs, float* lse, int32_t* tokens, void* ws, size_t ws_bytes,
                      int32_t* dev_err, moe_stream_t stream)
 {
-    if (T < 0 || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK || k > E || n_seg < 1 || n_seg > kMaxSequences)
+    if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts || k < 1 || k > kMaxTopK || k > E || n_seg < 1 ||
+        n_seg > kMaxSequences)
         return MOE_EINVAL;
     if ((int64_t)T * k >= kMaxRows || (!seg_off && n_seg != 1)) return MOE_EINVAL;
     if (T > 0 && (!logits || !topk_idx)) return MOE_EINVAL;
@@ -463,7 +465,7 @@ int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, const int32_t
                          const int32_t* counts, const int32_t* tokens, float balance_coef, float z_coef,
                          const float* dlosses, const float* add, float* dlogits, moe_stream_t stream)
 {
-    if (T < 0 || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return MOE_EINVAL;
+    if (T < 0 || T > kMaxTokens || E < 1 || E > kMaxExperts || n_seg < 1 || n_seg > kMaxSequences) return MOE_EINVAL;
     if (!seg_off && n_seg != 1) return MOE_EINVAL;
     if (T > 0 && (!logits || !dlogits || !counts || !tokens)) return MOE_EINVAL;
     return status_of(launch_balance_bwd(logits, mask, seg_off, n_seg, T, E, counts, tokens, balance_coef, z_coef,

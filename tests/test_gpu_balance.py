@@ -121,6 +121,25 @@ def test_sequences_and_masks(moe, T, E, k, seg, masked):
         np.testing.assert_array_equal(o2[n], o[n])
 
 
+@pytest.mark.parametrize("T,E,k,seg,masked", [
+    # one workgroup with everything (up to 32768 logits, 2048 tokens, two sequences), and the next size
+    (2048, 16, 2, None, True), (2049, 15, 2, None, True), (256, 128, 8, None, False), (257, 128, 8, None, False),
+    (32, 1024, 4, None, True), (33, 1024, 4, None, True), (31, 1021, 4, None, False),
+    (255, 128, 4, [0, 255], True), (255, 128, 4, [3, 100, 250], True), (255, 128, 4, [3, 100, 250, 255], True),
+    (300, 9, 3, [0, 0, 300], False), (300, 9, 3, [0, 300, 300], False), (300, 9, 3, [300, 300], False),
+    (1, 2, 2, [0, 1, 1], False), (2, 1, 1, [0, 1, 2], True),
+])
+def test_few_tokens(moe, T, E, k, seg, masked):
+    _say("few", T, E, k, seg, masked)
+    x, idx = _inputs(T, E, k, T * 5 + E)
+    x[T // 2, 0] = float("nan")
+    mask = (np.random.default_rng(T).random(T) > 0.3).astype(np.uint8) if masked else None
+    o = _run(moe, x, idx, 0.5, 0.1, seg, mask)
+    _check(o, x, idx, 0.5, 0.1, seg, mask)
+    counted = (mask is None or bool(mask[T // 2])) and (seg is None or seg[0] <= T // 2 < seg[-1])
+    assert o["err"][0] == (moe.MOE_ERR_NONFINITE_LOGIT if counted else 0)
+
+
 def test_nothing_counted(moe):
     _say("nothing")
     x, idx = _inputs(100, 8, 2, 1)

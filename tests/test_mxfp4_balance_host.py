@@ -191,6 +191,15 @@ def test_balance_validation(m):
     assert bwd(T=0, lg=None, dl=None) == m.MOE_OK
 
 
+def test_balance_refuses_token_numbers_that_leave_32_bits(m):
+    lib = m.load()
+    P, T = FAKE, (1 << 30) + 1
+    assert lib.moe_balance_workspace_bytes(T - 1, 1, 1) > 0 and lib.moe_balance_workspace_bytes(T, 1, 1) == 0
+    assert lib.moe_balance_loss(P, P, None, None, 1, T, 1, 1, 0.1, 0.1, P, P, P, None, P, P, 1 << 40, None,
+                                None) == m.MOE_EINVAL
+    assert lib.moe_balance_loss_bwd(P, None, None, 1, T, 1, P, P, 0.1, 0.1, None, None, P, None) == m.MOE_EINVAL
+
+
 def test_python_calls_refuse_what_is_not_dense(m):
     """The Python entry points check types, shapes and strides before anything is passed on."""
     x = torch.zeros(4, 64, dtype=torch.bfloat16)

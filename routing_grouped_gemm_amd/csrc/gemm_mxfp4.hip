@@ -552,7 +552,14 @@ struct Mx4Params {
 };
 
 // SwiGLU forward epilogue: [g | u] (when p.C is given), h in bf16 (when p.H
-// is), and always the MXFP4 copy of the bf16 h, which the down GEMM reads
+// is), and always the MXFP4 copy of the bf16 h, which the down GEMM reads.
+// A wave's 32 x 32 sub-tile has a row in the lanes l and l + 32, four columns
+// in turn: columns 8 q + 4 (lane >> 5) .. + 3 in registers 4 q .. 4 q + 3.  Rounded
+// to bf16 and with its middle quarters exchanged between the lanes' halves,
+// lane l holds columns 0 .. 15 and lane l + 32 columns 16 .. 31: MXFP4 blocks
+// are made there, and only bf16 rows go through the LDS, for stores of whole
+// lines (stored from the registers, 64 bytes of a row by two lanes, the outputs
+// of 65536 rows cost more: gate/up with gu and h 649 -> 665 us, down 406 -> 443).
 template <int BM>
 __device__ __forceinline__ void epilogue_swiglu4(const f32x16 (&acc)[BM / 64][2], const MParams& p, int64_t row0,
                                                  int rows_valid, int nt, uint8_t* lds)
@@ -561,41 +568,55 @@ __device__ __forceinline__ void epilogue_swiglu4(const f32x16 (&acc)[BM / 64][2]
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int wm = WL<NW4>::wm(wave), wn = WL<NW4>::wn(wave);
-    const int n0 = nt * 128;
+    const int n0 = nt * 128;   // (f is a multiple of 128: a tile's columns all exist)
     if (p.C) {
         stage_acc<BM, NW4>(acc, lds);
         stage_flush<BM, 32, NT>(lds, [&](int r, int c, uint4 v) {
             const int n = n0 + 8 * (c & 15);
-            if (r < rows_valid && n < p.f)
-                *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + (c < 16 ? n : p.f + n)) = v;
+            if (r < rows_valid) *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + (c < 16 ? n : p.f + n)) = v;
         });
     }
 #pragma unroll
-    for (int i = 0; i < BM / 64; ++i)
+    for (int i = 0; i < BM / 64; ++i) {
+        uint2 w[4];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int q = 0; q < 4; ++q) {
             float hv[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) hv[q] = silu_f(acc[i][0][4 * g + q]) * acc[i][1][4 * g + q];
-            stage_put(lds, stage_off<16>(wm * (BM / 2) + i * 32 + (lane & 31), acc_col<NW4>(wn, 0, g, lane)),
-                      pack4_bf16(hv[0], hv[1], hv[2], hv[3]));
+            for (int e = 0; e < 4; ++e) hv[e] = silu_f(acc[i][0][4 * q + e]) * acc[i][1][4 * q + e];
+            w[q] = pack4_bf16(hv[0], hv[1], hv[2], hv[3]);
         }
-    stage_flush<BM, 16, NT>(lds, [&](int r, int c, uint4 v) {
-        const int n = n0 + 8 * c;
-        uint32_t q;
-        const uint32_t s = mx4::quant8_quad(v, q);
-        if (r < rows_valid && n < p.f) {
-            if (p.H) *reinterpret_cast<uint4*>(p.H + (row0 + r) * p.ldh + n) = v;
-            *reinterpret_cast<uint32_t*>(p.Mq + (row0 + r) * (p.ldq / 2) + n / 2) = q;
-            if ((c & 3) == 0) p.Ms[(row0 + r) * (p.ldq / 32) + n / 32] = (uint8_t)s;
+        uint4 v[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const auto x = __builtin_amdgcn_permlane32_swap(w[q].x, w[q + 2].x, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(w[q].y, w[q + 2].y, false, false);
+            v[q] = make_uint4(x[0], y[0], x[1], y[1]);
         }
-    });
+        const uint32_t m = max(mx4::amax8(v[0]), mx4::amax8(v[1]));
+        const auto o = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        const uint32_t s = mx4::scale_byte(max(o[0], o[1]));
+        const int r = wm * (BM / 2) + i * 32 + (lane & 31);
+        const int col = wn * 32 + 16 * (lane >> 5);
+        if (r < rows_valid) {
+            const int64_t at = (row0 + r) * p.ldq + n0 + col;
+            *reinterpret_cast<uint2*>(p.Mq + at / 2) = make_uint2(mx4::encode8(v[0], s), mx4::encode8(v[1], s));
+            if (lane < 32) p.Ms[at / 32] = (uint8_t)s;
+        }
+        if (p.H) {
+            *reinterpret_cast<uint4*>(lds + stage_off<16>(r, col)) = v[0];
+            *reinterpret_cast<uint4*>(lds + stage_off<16>(r, col + 8)) = v[1];
+        }
+    }
+    if (p.H)
+        stage_flush<BM, 16, NT>(lds, [&](int r, int c, uint4 v) {
+            if (r < rows_valid) *reinterpret_cast<uint4*>(p.H + (row0 + r) * p.ldh + n0 + 8 * c) = v;
+        });
 }
 
-template <int EPI>
+template <int EPI, int BM>   // M-tiles of BM rows
 __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
 {
-    constexpr int BM = 256;
     // all of the LDS: the 128-row ring with its scales
     __shared__ __align__(16) uint8_t smem[3 * (128 + BN) * 128 + 2 * SSTAGE];
     static_assert(sizeof(smem) >= 2 * (BM + BN) * 128 + 2 * SSTAGE && sizeof(smem) <= 160 * 1024, "LDS");
@@ -644,9 +665,13 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
         else
             epilogue_m<BMS, EPI_STORE, NW4>(acc, p, tile.row0, tile.rows_valid, nt, smem);
     };
-    if (tile.rows_valid <= 64) run(std::integral_constant<int, 64>{});
-    else if (tile.rows_valid <= 128) run(std::integral_constant<int, 128>{});
-    else run(std::integral_constant<int, 256>{});
+    if constexpr (BM == 64) {
+        run(std::integral_constant<int, 64>{});
+    } else {
+        if (tile.rows_valid <= 64) run(std::integral_constant<int, 64>{});
+        else if (BM == 128 || tile.rows_valid <= 128) run(std::integral_constant<int, 128>{});
+        else if constexpr (BM == 256) run(std::integral_constant<int, 256>{});
+    }
 }
 
 // ---------------------------------------------------------------- few rows
@@ -959,13 +984,27 @@ hipError_t launch_few4(const Few4Params& p, hipStream_t s)
     return hipGetLastError();
 }
 
+// Tiles of 64 or 128 rows, the smallest whose number (its host-known bound)
+// runs in one round on the 256 CUs, else of 256 rows, whose loop does the most
+// per byte read.  Measured (64, 128, 256 rows a tile, us): 838 rows of 3
+// experts, d = 2048, f = 1280, gate/up 14.1 16.2 19.6 and down 9.8 11.1 14.5;
+// 2000 rows of 8, f = 1152, 24.3 17.1 20.5 and 18.8 13.1 17.0 (351 and 312
+// tiles of 64 rows); 16576 rows of 43, d = f = 1024, 72.2 53.2 47.3 and 39.7
+// 31.6 29.0.
 template <int EPI>
 hipError_t launch_mx4_m(const Mx4Params& mp, hipStream_t s)
 {
-    const int64_t bound = (mp.p.n_rows / 256 + mp.p.E) * (int64_t)mp.p.ntn;
-    const int64_t grid = (bound + 7) / 8 * 8;
-    if (grid == 0 || mp.p.n_rows == 0) return hipSuccess;
-    hipLaunchKernelGGL((mx4_grouped_m_kernel<EPI>), dim3((unsigned)grid), dim3(64 * NW4), 0, s, mp);
+    const int64_t n = mp.p.n_rows, e = std::min<int64_t>(mp.p.E, n), ntn = mp.p.ntn;
+    auto tiles = [&](int bm) { return (n / bm + e) * ntn; };
+    auto go = [&](auto BM) {
+        const int64_t grid = (tiles(decltype(BM)::value) + 7) / 8 * 8;
+        if (grid > 0)
+            hipLaunchKernelGGL((mx4_grouped_m_kernel<EPI, decltype(BM)::value>), dim3((unsigned)grid), dim3(64 * NW4), 0,
+                               s, mp);
+    };
+    if (tiles(64) <= 256) go(std::integral_constant<int, 64>{});
+    else if (tiles(128) <= 256) go(std::integral_constant<int, 128>{});
+    else go(std::integral_constant<int, 256>{});
     return hipGetLastError();
 }
 

@@ -243,6 +243,23 @@ def test_products(moe, sizes, d, f):
     assert torch.equal(y2, y) and torch.equal(y3, y) and torch.equal(gu3, gu) and torch.equal(h3, h)
 
 
+# enough column tiles that 256-row tiles are taken: every length of that loop
+# (an odd and an even number of 128-k halves up to its steady state and past
+# it) for the gate/up stage (K = d), then for the down stage (K = f)
+@pytest.mark.parametrize("d,f", [(128, 1536), (256, 1536), (384, 1536), (512, 1536), (640, 1536), (768, 1536),
+                                 (1024, 1536), (1152, 1536), (1280, 1536), (1408, 1536), (2176, 1536), (4096, 128),
+                                 (4096, 384), (4096, 640), (3968, 896)])
+def test_products_with_large_tiles(moe, d, f):
+    _say("products-large-tiles", d, f)
+    sizes = [257, 0, 512, 700, 255, 1000]
+    q = _case(moe, sizes, d, f, seed=d + f)
+    gu, h, y = _forward(moe, q, d, f)
+    _, _, y2 = _forward(moe, q, d, f, save=False)
+    torch.cuda.synchronize()
+    _check(q, gu, h, y, sizes, d, f)
+    assert torch.equal(y2, y)
+
+
 def test_products_padded(moe):
     _say("products-padded")
     C, d, f, E = 70, 256, 128, 3

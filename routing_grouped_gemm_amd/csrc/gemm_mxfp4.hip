@@ -955,28 +955,40 @@ __global__ __launch_bounds__(64 * NW4) void mx4_few_rows_kernel(Few4Params p)
     }
 }
 
-// Whether the few-row form runs: when its workgroups (their host-known bound,
-// sum ceil(m_e / 64) <= experts with rows + n_rows / 64, times the column
-// tiles) run in one round on the chip's 256 CUs, one per CU with two units a
-// wave (139 KB of LDS) and two with one.  Measured against the tile form
-// (gate/up, down, us; d = 4096, f = 1536 unless given): 1 row of 1 expert
-// 5.7 4.3 against 18.0 10.0; 256 rows of 1 expert 15.2 9.6 against 25.8 14.1; 4
-// experts of 32 rows 9.9 6.7 against 17.9 10.1; 8 of 1 row, d = 2048, f =
-// 1152: 6.5 5.0 against 11.9 9.2.  Past one round: 8 experts of 8 rows (384
-// workgroups for gate/up) 16.4 against 18.2, 16 of 1 row (768) 25.6 against
-// 20.3, 128 of 2 rows 198 132 against 160 105: there the tile form streams the
-// weights faster.
+// The tiles of bm rows that the groups can have: sum ceil(m_e / bm) over the
+// groups with rows, at most e of them, is sum 1 + floor((m_e - 1) / bm).
+inline int64_t row_tiles(int64_t n_rows, int E, int bm)
+{
+    const int64_t e = std::min<int64_t>(E, n_rows);
+    return e + (n_rows - e) / bm;
+}
+
+// Whether the few-row form runs: when its workgroups (at most) run in one round
+// on the chip's 256 CUs, one per CU with two units a wave (139 KB of LDS) and
+// two with one; in one and a half with at most 48 rows per expert on average;
+// in two with at most 16 and a K that the tile form takes long over.
+// Measured, this form and the tile form (us):
+//   within a round: 1 row of 1 expert, d = 4096, f = 1536, gate/up 5.4 17.2 and
+//     down 4.5 9.6; 256 rows of 1 expert 15.0 17.9 and 9.3 10.1
+//   1.5 rounds: 64 rows of 8 experts, gate/up 15.8 17.7; 256 rows of 32, d =
+//     1024, 5.7 8.2 (with 1024 rows 8.1 8.2); but 64 rows each: 512 rows of 8,
+//     d = 2048, 15.2 11.6
+//   2 rounds: 64 rows of 8, down (K = 1536) 7.9 9.8; of 32, K = 512, 7.2 6.5
+//   more: 16 rows of 16 24.8 19.7 and 16.6 12.8; 256 rows of 128 194 156 and
+//     129 103: there the tile form streams the weights faster.
 inline bool few_rows(const GroupSpec& g, int K, int ntn)
 {
-    const int64_t groups = std::min<int64_t>(g.E, g.n_rows) + g.n_rows / FROWS;
-    return groups * ntn <= 256 * (K <= NW4 * 256 ? 2 : 1);
+    const int64_t n = g.n_rows, e = std::min<int64_t>(g.E, n);
+    const int64_t wgs = row_tiles(n, g.E, FROWS) * ntn, round = 256 * (K <= NW4 * 256 ? 2 : 1);
+    if (n <= 16 * e && K >= 1536) return wgs <= 2 * round;
+    if (n <= 48 * e) return 2 * wgs <= 3 * round;
+    return wgs <= round;
 }
 
 template <int EPI>
 hipError_t launch_few4(const Few4Params& p, hipStream_t s)
 {
-    const int64_t groups = std::min<int64_t>(p.E, p.n_rows) + p.n_rows / FROWS;
-    const int64_t grid = (groups * p.ntn + 7) / 8 * 8;
+    const int64_t grid = (row_tiles(p.n_rows, p.E, FROWS) * p.ntn + 7) / 8 * 8;
     if (p.K <= NW4 * 256)   // one unit per wave
         hipLaunchKernelGGL((mx4_few_rows_kernel<EPI, 1>), dim3((unsigned)grid), dim3(64 * NW4), 0, s, p);
     else
@@ -988,14 +1000,13 @@ hipError_t launch_few4(const Few4Params& p, hipStream_t s)
 // runs in one round on the 256 CUs, else of 256 rows, whose loop does the most
 // per byte read.  Measured (64, 128, 256 rows a tile, us): 838 rows of 3
 // experts, d = 2048, f = 1280, gate/up 14.1 16.2 19.6 and down 9.8 11.1 14.5;
-// 2000 rows of 8, f = 1152, 24.3 17.1 20.5 and 18.8 13.1 17.0 (351 and 312
+// 2000 rows of 8, f = 1152, 24.3 17.1 20.5 and 18.8 13.1 17.0 (342 and 304
 // tiles of 64 rows); 16576 rows of 43, d = f = 1024, 72.2 53.2 47.3 and 39.7
 // 31.6 29.0.
 template <int EPI>
 hipError_t launch_mx4_m(const Mx4Params& mp, hipStream_t s)
 {
-    const int64_t n = mp.p.n_rows, e = std::min<int64_t>(mp.p.E, n), ntn = mp.p.ntn;
-    auto tiles = [&](int bm) { return (n / bm + e) * ntn; };
+    auto tiles = [&](int bm) { return row_tiles(mp.p.n_rows, mp.p.E, bm) * mp.p.ntn; };
     auto go = [&](auto BM) {
         const int64_t grid = (tiles(decltype(BM)::value) + 7) / 8 * 8;
         if (grid > 0)

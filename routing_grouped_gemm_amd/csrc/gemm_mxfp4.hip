@@ -542,6 +542,79 @@ __device__ __forceinline__ void mainloop4_pp(const Src4& sa, const Src4& sb, f32
     }
 }
 
+// The tile of this workgroup in schedule_m's order (expert-major; a contiguous
+// range of tiles per XCD), with every lane's group bounds loaded at once and
+// the chosen expert's taken from the lane that holds them: one round trip to
+// memory ahead of the operands instead of three, which nothing hides with one
+// workgroup per CU (268 rows of 128 experts, d = 4096, f = 1536: gate/up 152 ->
+// 141 us, down 101 -> 86; 65536 rows 656 -> 634 and 418 -> 383).  With 64-row
+// tiles all column tiles of a row tile go before the next: they run together
+// and share its rows.
+template <int PER, int BM>   // experts per lane, E <= 64 PER; M-tiles of BM rows
+__device__ __forceinline__ bool schedule_per(const int32_t* group_off, int capacity, int E, int64_t n_rows64, int ntn,
+                                             MTile& t)
+{
+    const int lane = threadIdx.x & 63;
+    const int gb = lane * PER;
+    const int n_rows = (int)n_rows64;   // below 2^31
+    int bnd[PER + 1];
+    if (capacity > 0) {
+#pragma unroll
+        for (int k = 0; k <= PER; ++k) bnd[k] = (int)min((int64_t)min(gb + k, E) * capacity, n_rows64);
+    } else {
+#pragma unroll
+        for (int k = 0; k <= PER; ++k) bnd[k] = group_off[min(gb + k, E)];
+    }
+    int cnt = 0, c[PER];
+#pragma unroll
+    for (int k = 0; k <= PER; ++k) bnd[k] = min(max(bnd[k], 0), n_rows);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        c[k] = (int)((uint32_t)(max(bnd[k + 1] - bnd[k], 0) + BM - 1) / BM) * ntn;
+        cnt += c[k];
+    }
+    // inclusive scan by lane permutations: within rows of 16 (row_shr 1, 2, 4,
+    // 8), then each row's last lane into the rows behind it (row_bcast 15, 31)
+    int incl = cnt;
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, true);
+    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, true);
+    const int total = __builtin_amdgcn_readlane(incl, 63);
+    const int per_xcd = (total + 7) / 8;
+    const int slot = blockIdx.x / 8;
+    const int L = (int)(blockIdx.x % 8) * per_xcd + slot;
+    if (slot >= per_xcd || L >= total) return false;
+    int run = incl - cnt;
+    const int src = __ffsll((unsigned long long)__ballot(run <= L && L < incl)) - 1;
+    int e = gb, first = run, b0 = 0, rows = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (L >= run && L < run + c[k]) {
+            e = gb + k;
+            first = run;
+            b0 = bnd[k];
+            rows = bnd[k + 1] - bnd[k];
+        }
+        run += c[k];
+    }
+    t.e = __builtin_amdgcn_readlane(e, src);
+    const int local = L - __builtin_amdgcn_readlane(first, src);
+    const int m_e = __builtin_amdgcn_readlane(rows, src);
+    grouped_tile(local, (m_e + BM - 1) / BM, ntn, BM == 64 ? 1 : kMTileGroup, t.mt, t.nt);
+    t.row0 = (int64_t)__builtin_amdgcn_readlane(b0, src) + (int64_t)t.mt * BM;
+    t.rows_valid = min(BM, m_e - t.mt * BM);
+    return true;
+}
+template <int BM>
+__device__ __forceinline__ bool schedule4(const int32_t* group_off, int capacity, int E, int64_t n_rows, int ntn, MTile& t)
+{
+    if (E <= 128) return schedule_per<2, BM>(group_off, capacity, E, n_rows, ntn, t);
+    return schedule_per<16, BM>(group_off, capacity, E, n_rows, ntn, t);
+}
+
 struct Mx4Params {
     MParams p;             // shapes, schedule and outputs (p.A / p.B unused; p.C, p.H may be null)
     const uint8_t* Aq;     // [n_rows, K/2] codes
@@ -622,7 +695,7 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW4) void mx4_grouped_m_kernel(Mx4Params mp)
     static_assert(sizeof(smem) >= 2 * (BM + BN) * 128 + 2 * SSTAGE && sizeof(smem) <= 160 * 1024, "LDS");
     const MParams& p = mp.p;
     MTile tile;
-    if (!schedule_m<BM>(p.group_off, p.capacity, p.E, p.n_rows, p.ntn, tile)) return;
+    if (!schedule4<BM>(p.group_off, p.capacity, p.E, p.n_rows, p.ntn, tile)) return;
     const int nt = tile.nt;
     const int64_t cb = p.K / 2, sbk = p.K / 32;   // bytes per row: codes, scales
 
@@ -707,71 +780,6 @@ struct Few4Params {
     uint8_t *Mq, *Ms;          // gate/up: MXFP4 h
 };
 
-// The tile of this workgroup: schedule_m's order (expert-major; a contiguous
-// range of tiles per XCD), with every lane's group bounds loaded at once and
-// the chosen expert's taken from the lane that holds them: one round trip to
-// memory ahead of the weights instead of three.
-template <int PER>   // experts per lane, E <= 64 PER
-__device__ __forceinline__ bool schedule_few(const Few4Params& p, MTile& t)
-{
-    const int lane = threadIdx.x & 63;
-    const int gb = lane * PER;
-    const int n_rows = (int)p.n_rows;   // below 2^31
-    int bnd[PER + 1];
-    if (p.capacity > 0) {
-#pragma unroll
-        for (int k = 0; k <= PER; ++k) bnd[k] = (int)min((int64_t)min(gb + k, p.E) * p.capacity, p.n_rows);
-    } else {
-#pragma unroll
-        for (int k = 0; k <= PER; ++k) bnd[k] = p.group_off[min(gb + k, p.E)];
-    }
-    int cnt = 0, c[PER];
-#pragma unroll
-    for (int k = 0; k <= PER; ++k) bnd[k] = min(max(bnd[k], 0), n_rows);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        c[k] = (int)((uint32_t)(max(bnd[k + 1] - bnd[k], 0) + FROWS - 1) / FROWS) * p.ntn;
-        cnt += c[k];
-    }
-    // inclusive scan by lane permutations: within rows of 16 (row_shr 1, 2, 4,
-    // 8), then each row's last lane into the rows behind it (row_bcast 15, 31)
-    int incl = cnt;
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x111, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x112, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x114, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x118, 0xF, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x142, 0xA, 0xF, true);
-    incl += __builtin_amdgcn_update_dpp(0, incl, 0x143, 0xC, 0xF, true);
-    const int total = __builtin_amdgcn_readlane(incl, 63);
-    const int per_xcd = (total + 7) / 8;
-    const int slot = blockIdx.x / 8;
-    const int L = (int)(blockIdx.x % 8) * per_xcd + slot;
-    if (slot >= per_xcd || L >= total) return false;
-    int run = incl - cnt;
-    const int src = __ffsll((unsigned long long)__ballot(run <= L && L < incl)) - 1;
-    int e = gb, first = run, b0 = 0, rows = 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        if (L >= run && L < run + c[k]) {
-            e = gb + k;
-            first = run;
-            b0 = bnd[k];
-            rows = bnd[k + 1] - bnd[k];
-        }
-        run += c[k];
-    }
-    t.e = __builtin_amdgcn_readlane(e, src);
-    const int local = L - __builtin_amdgcn_readlane(first, src);
-    const int m_e = __builtin_amdgcn_readlane(rows, src);
-    // column tiles across a 64-row group before the next group: a group's
-    // workgroups run together and share its rows
-    t.mt = local / p.ntn;
-    t.nt = local - t.mt * p.ntn;
-    t.row0 = (int64_t)__builtin_amdgcn_readlane(b0, src) + (int64_t)t.mt * FROWS;
-    t.rows_valid = min(FROWS, m_e - t.mt * FROWS);
-    return true;
-}
-
 template <int EPI, int U>   // U: units a wave has in flight
 __global__ __launch_bounds__(64 * NW4) void mx4_few_rows_kernel(Few4Params p)
 {
@@ -788,7 +796,7 @@ __global__ __launch_bounds__(64 * NW4) void mx4_few_rows_kernel(Few4Params p)
     __shared__ __align__(16) uint16_t out[NOUT][16 * FCOLS];
     auto red = reinterpret_cast<f32x4_t(*)[NTILE][64]>(lds);
     MTile t;
-    if (p.E <= 128 ? !schedule_few<2>(p, t) : !schedule_few<16>(p, t)) return;
+    if (!schedule4<FROWS>(p.group_off, p.capacity, p.E, p.n_rows, p.ntn, t)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, kb = lane >> 4;
@@ -963,26 +971,24 @@ inline int64_t row_tiles(int64_t n_rows, int E, int bm)
     return e + (n_rows - e) / bm;
 }
 
-// Whether the few-row form runs: when its workgroups (at most) run in one round
-// on the chip's 256 CUs, one per CU with two units a wave (139 KB of LDS) and
-// two with one; in one and a half with at most 48 rows per expert on average;
-// in two with at most 16 and a K that the tile form takes long over.
-// Measured, this form and the tile form (us):
-//   within a round: 1 row of 1 expert, d = 4096, f = 1536, gate/up 5.4 17.2 and
-//     down 4.5 9.6; 256 rows of 1 expert 15.0 17.9 and 9.3 10.1
-//   1.5 rounds: 64 rows of 8 experts, gate/up 15.8 17.7; 256 rows of 32, d =
-//     1024, 5.7 8.2 (with 1024 rows 8.1 8.2); but 64 rows each: 512 rows of 8,
-//     d = 2048, 15.2 11.6
-//   2 rounds: 64 rows of 8, down (K = 1536) 7.9 9.8; of 32, K = 512, 7.2 6.5
-//   more: 16 rows of 16 24.8 19.7 and 16.6 12.8; 256 rows of 128 194 156 and
-//     129 103: there the tile form streams the weights faster.
+// Whether the few-row form runs: with more than 32 rows per expert on average
+// when its workgroups (at most) are one per CU, else when they run in one round
+// (one per CU with two units a wave, 139 KB of LDS, two with one), with at most
+// 16 rows in one and a half.  Measured, this form and the tile form (us):
+//   one per CU: 1 row of 1 expert, d = 4096, f = 1536, gate/up 5.5 16.1 and down
+//     3.9 8.3; 256 rows of 1 expert, gate/up 15.0 16.6 (down, two per CU, 9.2 8.7)
+//   one round: 256 rows of 8, d = 2048, f = 1152, 9.7 9.9 (384 rows 12.3 10.2)
+//   1.5 rounds: 64 rows of 8, d = 4096, 15.8 16.6; 256 rows of 32, d = 1024, 5.8
+//     6.9 (but 1024 rows 8.2 7.0)
+//   more: 64 rows of 8, down (2 rounds) 8.2 8.4; 256 of 32, d = 1024, f = 512,
+//     7.5 5.4; 16 rows of 16 25.0 18.5; 256 rows of 128 198 147 and 131 89: there
+//     the tile form streams the weights faster.
 inline bool few_rows(const GroupSpec& g, int K, int ntn)
 {
     const int64_t n = g.n_rows, e = std::min<int64_t>(g.E, n);
     const int64_t wgs = row_tiles(n, g.E, FROWS) * ntn, round = 256 * (K <= NW4 * 256 ? 2 : 1);
-    if (n <= 16 * e && K >= 1536) return wgs <= 2 * round;
-    if (n <= 48 * e) return 2 * wgs <= 3 * round;
-    return wgs <= round;
+    if (n > 32 * e) return wgs <= 256;
+    return n > 16 * e ? wgs <= round : 2 * wgs <= 3 * round;
 }
 
 template <int EPI>

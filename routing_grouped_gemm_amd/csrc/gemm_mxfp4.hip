@@ -1005,10 +1005,10 @@ hipError_t launch_few4(const Few4Params& p, hipStream_t s)
 // Tiles of 64 or 128 rows, the smallest whose number (its host-known bound)
 // runs in one round on the 256 CUs, else of 256 rows, whose loop does the most
 // per byte read.  Measured (64, 128, 256 rows a tile, us): 838 rows of 3
-// experts, d = 2048, f = 1280, gate/up 14.1 16.2 19.6 and down 9.8 11.1 14.5;
-// 2000 rows of 8, f = 1152, 24.3 17.1 20.5 and 18.8 13.1 17.0 (342 and 304
-// tiles of 64 rows); 16576 rows of 43, d = f = 1024, 72.2 53.2 47.3 and 39.7
-// 31.6 29.0.
+// experts, d = 2048, f = 1280, gate/up 12.5 14.6 17.4 and down 9.3 10.0 13.8;
+// 2000 rows of 8, f = 1152, 21.9 15.4 18.4 and 16.2 11.6 15.5 (342 and 304
+// tiles of 64 rows); 16576 rows of 43, d = f = 1024, 62.4 46.1 42.4 and 34.6
+// 28.6 27.0.
 template <int EPI>
 hipError_t launch_mx4_m(const Mx4Params& mp, hipStream_t s)
 {

@@ -142,25 +142,27 @@ def _nbytes(t):
 
 def _dense(name, t, dtype, *shape):
     """The data pointer of t (None: NULL) after checking that it is a dense `dtype` tensor
-    of `shape` on a GPU."""
+    of `shape`."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on the GPU, got {t.dtype} "
-                         f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
 def _call(name, stream, tensors, *args):
     """The C entry point `name` on `stream` (None: the current one of the tensors' device), with that
-    device current; `tensors` must be on one device.  The stream is the last argument."""
+    device current; `tensors` must be on one GPU.  The stream is the last argument."""
     dev = tensors[0].get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected tensors on a GPU, got one on {tensors[0].device}")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     fn = getattr(load(), name)
     if dev == torch.cuda.current_device():
-        rc = fn(*args, _s(stream))
+        rc = fn(*args, _raw_stream(dev) if stream is None and _raw_stream else _s(stream))
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _s(stream))
@@ -214,9 +216,14 @@ def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_p
     T, d = x.shape
     n_rows = x_perm.shape[0]
     if dtype == MOE_MXFP4:
-        _dense("x", x, torch.bfloat16, T, d)
-        _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2)
-        _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32)
+        if dst_row.numel() != T * k:
+            raise ValueError(f"dst_row: expected {T * k} rows for {T} tokens, got {dst_row.numel()}")
+        _call("moe_permute", stream, (x, dst_row, x_perm, src_slot, row_scale, x_perm_scales, dev_err), dtype,
+              _dense("x", x, torch.bfloat16, T, d), T, d, k, _dense("dst_row", dst_row, torch.int32, *dst_row.shape),
+              _dense("src_slot", src_slot, torch.int32, n_rows), _p(row_scale), n_rows,
+              _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2),
+              _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32), _p(dev_err))
+        return
     rc = load().moe_permute(dtype, _p(x), T, d, k, _p(dst_row), _p(src_slot), _p(row_scale),
                             n_rows, _p(x_perm), _p(x_perm_scales), _p(dev_err), _s(stream))
     _check(rc, "moe_permute")
@@ -237,18 +244,16 @@ def moe_grouped_gemm_fwd(dtype, x_perm, w13, w2, group_off, capacity, gu, h, y_p
     n_rows, d = x_perm.shape
     if dtype == MOE_MXFP4:
         d, f = 2 * d, 2 * w2.shape[-1]
-        _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2)
-        _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32)
-        _dense("w13", w13, torch.uint8, E, 2 * f, d // 2)
-        _dense("w13_scales", w13_scales, torch.uint8, E, 2 * f, d // 32)
-        _dense("w2", w2, torch.uint8, E, d, f // 2)
-        _dense("w2_scales", w2_scales, torch.uint8, E, d, f // 32)
-        _dense("group_off", group_off, torch.int32, E + 1)
-        _dense("gu", gu, torch.bfloat16, n_rows, 2 * f)
-        _dense("h", h, torch.bfloat16, n_rows, f)
-        _dense("y_perm", y_perm, torch.bfloat16, n_rows, d)
-    else:
-        f = h.shape[1]
+        u8, bf = torch.uint8, torch.bfloat16
+        _call("moe_grouped_gemm_fwd", stream, (x_perm, x_perm_scales, w13, w13_scales, w2, w2_scales, group_off, gu, h,
+                                               y_perm, ws), dtype, _dense("x_perm", x_perm, u8, n_rows, d // 2),
+              _dense("x_perm_scales", x_perm_scales, u8, n_rows, d // 32), _dense("w13", w13, u8, E, 2 * f, d // 2),
+              _dense("w13_scales", w13_scales, u8, E, 2 * f, d // 32), _dense("w2", w2, u8, E, d, f // 2),
+              _dense("w2_scales", w2_scales, u8, E, d, f // 32), _dense("group_off", group_off, torch.int32, E + 1),
+              capacity, E, n_rows, d, f, _dense("gu", gu, bf, n_rows, 2 * f), _dense("h", h, bf, n_rows, f),
+              _dense("y_perm", y_perm, bf, n_rows, d), _p(ws), _nbytes(ws))
+        return
+    f = h.shape[1]
     rc = load().moe_grouped_gemm_fwd(dtype, _p(x_perm), _p(x_perm_scales), _p(w13),
                                      _p(w13_scales), _p(w2), _p(w2_scales), _p(group_off),
                                      capacity, E, n_rows, d, f, _p(gu), _p(h), _p(y_perm), _p(ws),

@@ -212,3 +212,14 @@ def test_python_calls_refuse_what_is_not_dense(m):
         m._dense("x", x, torch.bfloat16, 4, 32)
     with pytest.raises(ValueError):
         m._dense("x", x, torch.float32, 4, 64)
+    # MXFP4 calls: what lies on the host, a destination per slot
+    dst = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        m.moe_permute(m.MOE_MXFP4, x, 2, dst, u8(8, 32), x_perm_scales=u8(8, 2))
+    with pytest.raises(ValueError):
+        m.moe_permute(m.MOE_MXFP4, x, 2, dst[:7], u8(8, 32), x_perm_scales=u8(8, 2))
+    off = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        m.moe_grouped_gemm_fwd(m.MOE_MXFP4, u8(4, 64), u8(1, 256, 64), u8(1, 128, 64), off, 0, None, None,
+                               torch.zeros(4, 128, dtype=torch.bfloat16), x_perm_scales=u8(4, 4),
+                               w13_scales=u8(1, 256, 4), w2_scales=u8(1, 128, 4), ws=u8(4096))

@@ -307,3 +307,87 @@ def test_router_step(moe):
             torch.cuda.synchronize()
             for n in names:
                 assert torch.equal(getattr(lay, n), ref[n]), (rep, n)
+
+
+def test_two_graphs_share_a_workspace(moe):
+    """Two captured losses (two kernels each, one of them over sequences) with one workspace, replayed in turn."""
+    _say("graphs")
+    E, k = 24, 3
+    ws = torch.empty(moe.moe_balance_workspace_bytes(9000, E, 4), dtype=torch.uint8, device=DEV)
+    sets = []
+    for T, seg in ((9000, None), (5003, [0, 64, 64, 3000, 5003])):
+        S = 1 if seg is None else len(seg) - 1
+        s = dict(x=torch.empty(T, E, device=DEV), idx=torch.empty(T, k, dtype=torch.int32, device=DEV),
+                 losses=torch.empty(2, device=DEV), counts=torch.empty(S, E, dtype=torch.int32, device=DEV),
+                 probs=torch.empty(S, E, device=DEV), lse=torch.empty(T, device=DEV),
+                 tokens=torch.empty(S + 1, dtype=torch.int32, device=DEV), grad=torch.empty(T, E, device=DEV),
+                 seg=None if seg is None else torch.tensor(seg, dtype=torch.int32, device=DEV))
+
+        def step(s=s):
+            moe.moe_balance_loss(s["x"], s["idx"], 0.1, 0.01, s["losses"], s["counts"], s["probs"], s["lse"],
+                                 s["tokens"], ws, seg_off=s["seg"])
+            moe.moe_balance_loss_bwd(s["x"], s["counts"], s["tokens"], 0.1, 0.01, s["grad"], seg_off=s["seg"])
+        s["step"] = step
+        x, idx = _inputs(T, E, k, T)
+        s["x"].copy_(x), s["idx"].copy_(idx.to(torch.int32))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.synchronize()
+        s["graph"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(s["graph"]):
+            step()
+        sets.append(s)
+    names = ("losses", "counts", "probs", "lse", "tokens", "grad")
+    for rep in range(4):
+        refs = []
+        for s in sets:
+            x, idx = _inputs(s["x"].shape[0], E, k, 100 + rep)
+            s["x"].copy_(x), s["idx"].copy_(idx.to(torch.int32))
+            s["step"]()
+            torch.cuda.synchronize()
+            refs.append({n: s[n].clone() for n in names})
+            for n in names:
+                s[n].zero_()
+        ws.fill_(0xFF)
+        for s in sets:
+            s["graph"].replay()
+        torch.cuda.synchronize()
+        for s, r in zip(sets, refs):
+            for n in names:
+                assert torch.equal(s[n], r[n]), (rep, n)
+
+
+def test_more_logits_than_32_bits_count(moe):
+    """A block of tokens over and over: counts are exact multiples, every block's lse and gradient the first's bits,
+    and the gradient the block's own over the repetitions (the counts' shares are the same quotients)."""
+    _say("long")
+    n, reps, E, k = 1000, 2200, 1024, 4
+    x, idx = _inputs(n, E, k, 8)
+    small = _run(moe, x, idx, 0.5, 0.1)
+    xg, ig = x.to(DEV).repeat(reps, 1), idx.to(torch.int32).to(DEV).repeat(reps, 1)
+    T = n * reps
+    assert T * E > 1 << 31
+    losses, counts = torch.empty(2, device=DEV), torch.empty(1, E, dtype=torch.int32, device=DEV)
+    probs, lse = torch.empty(1, E, device=DEV), torch.empty(T, device=DEV)
+    tokens = torch.empty(2, dtype=torch.int32, device=DEV)
+    ws = torch.empty(moe.moe_balance_workspace_bytes(T, E, 1), dtype=torch.uint8, device=DEV)
+    moe.moe_balance_loss(xg, ig, 0.5, 0.1, losses, counts, probs, lse, tokens, ws)
+    grad = torch.full((T, E), 9.0, device=DEV)
+    moe.moe_balance_loss_bwd(xg, counts, tokens, 0.5, 0.1, grad)
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(counts.cpu().numpy(), small["counts"] * reps)
+    assert tokens.tolist() == [T, T]
+    first, last = grad[:n], grad[T - n:]
+    assert torch.equal(first, last) and torch.equal(grad[T // 2:T // 2 + n], first)
+    assert torch.equal(lse.view(reps, n), lse[:n].expand(reps, n))
+    # f is counts / sum of counts, here both `reps` times as large (below 2^24: exact), so it is the same
+    # quotient; k_b, k_z and the three products after them are rounded anew: 2^-21 of each term's size
+    p = torch.softmax(x.double(), 1)
+    f = torch.as_tensor(small["counts"]).double() / (n * k)
+    mag = p * (0.5 * E / n * (f + (p * f).sum(1, keepdim=True)) + 0.2 / n * torch.as_tensor(small["lse"]).double().abs()[:, None])
+    err = (first.cpu().double() * reps - torch.as_tensor(small["grad"]).double()).abs()
+    assert bool((err <= 2.0 ** -21 * mag + 2.0 ** -100).all())
+    # the sums: at most T additions of rounded terms in any order
+    assert float((probs.cpu() - torch.as_tensor(small["probs"])).abs().max()) <= T * 2.0 ** -24 * float(small["probs"].max())

@@ -139,6 +139,12 @@ def test_dispatch_bit_exact(moe, T, d, E, k, C):
     np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
 
 
+@pytest.mark.parametrize("T,d,E,k,C", [(70, 2048, 6, 3, 0), (70, 2080, 9, 8, 0), (120, 4128, 4, 2, 50), (5, 2016, 5, 5, 0)])
+def test_dispatch_of_wide_rows(moe, T, d, E, k, C):
+    """Rows on both sides of a workgroup per token, vectors that end inside its second pass, padding."""
+    test_dispatch_bit_exact(moe, T, d, E, k, C)
+
+
 def test_dispatch_flags_rows_out_of_range(moe):
     _say("dispatch-range")
     x = _bf16((4, 64), 1)
@@ -155,6 +161,68 @@ def test_dispatch_flags_rows_out_of_range(moe):
         np.testing.assert_array_equal(got[row], c[tok])
     for row in (3, 4, 6):
         assert (got[row] == 0xAA).all()
+
+
+def test_quantize_past_the_cache(moe):
+    """From 256 MB of source on the accesses stream: the same codes as of its halves."""
+    _say("quantize-stream")
+    rows, K = 33001, 4128
+    x = torch.randn(rows, K, generator=torch.Generator(DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
+    codes, scales = _quantize(moe, x)
+    back = torch.empty_like(x)
+    moe.moe_dequantize_mxfp4(codes, scales, back)
+    for sl in (slice(0, 15000), slice(15000, 30000), slice(30000, rows)):
+        c, s = _quantize(moe, x[sl].contiguous())
+        b = torch.empty_like(x[sl])
+        moe.moe_dequantize_mxfp4(c, s, b)
+        assert torch.equal(codes[sl], c) and torch.equal(scales[sl], s) and torch.equal(back[sl], b)
+
+
+def test_quantize_and_dispatch_past_32_bits(moe):
+    """More elements than 2^32, more workgroups than a grid has: the last rows are those of small calls."""
+    _say("quantize-dispatch-long")
+    rows, K = (1 << 20) + 1003, 4224
+    x = torch.empty(rows, K, dtype=torch.bfloat16, device=DEV)
+    base = torch.randn(1009, K, generator=torch.Generator(DEV).manual_seed(2), device=DEV).to(torch.bfloat16)
+    for a in range(0, rows, 1009):
+        n = min(1009, rows - a)
+        x[a:a + n] = base[:n]
+    bc, bs = _quantize(moe, base)
+    idx = torch.arange(rows, device=DEV) % 1009
+    ends = torch.cat([torch.arange(0, 5000), torch.arange(rows - 5000, rows)]).to(DEV)
+    mid = torch.randint(0, rows, (5000,), generator=torch.Generator(DEV).manual_seed(3), device=DEV)
+    pick = torch.cat([ends, mid])
+    codes, scales = _quantize(moe, x)
+    assert torch.equal(codes[pick], bc[idx[pick]]) and torch.equal(scales[pick], bs[idx[pick]])
+    back = torch.zeros_like(x)
+    moe.moe_dequantize_mxfp4(codes, scales, back)
+    small = torch.empty_like(base)
+    moe.moe_dequantize_mxfp4(bc, bs, small)
+    assert torch.equal(back[pick], small[idx[pick]])
+    del back
+    for d in (K, 128):                        # a workgroup per token, and by vectors
+        T = rows * K // d
+        dst = torch.arange(T - 1, -1, -1, dtype=torch.int32, device=DEV)
+        codes.fill_(0xAA)
+        moe.moe_permute(moe.MOE_MXFP4, x.view(T, d), 1, dst, codes.view(T, d // 2), x_perm_scales=scales.view(T, d // 32))
+        want_c, want_s = bc.view(-1, d // 2), bs.view(-1, d // 32)
+        tok = torch.cat([torch.arange(0, 9000), torch.arange(T - 9000, T)]).to(DEV)
+        per = want_c.shape[0]
+        assert torch.equal(codes.view(T, d // 2)[T - 1 - tok], want_c[tok % per])
+        assert torch.equal(scales.view(T, d // 32)[T - 1 - tok], want_s[tok % per])
+
+
+def test_tensors_of_the_host_are_refused(moe):
+    q = _case(moe, [4], 256, 128)
+    x = _bf16((4, 256), 1).to(DEV)
+    dst = torch.arange(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        moe.moe_permute(moe.MOE_MXFP4, x, 1, dst, q["x"], x_perm_scales=q["xs"])
+    y = torch.empty(4, 256, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_gemm_fwd(moe.MOE_MXFP4, q["x"], q["w13"], q["w2"], q["off"], 0, None, None, y,
+                                 x_perm_scales=q["xs"], w13_scales=q["w13s"], w2_scales=q["w2s"],
+                                 ws=torch.empty(1 << 16, dtype=torch.uint8))
 
 
 # ------------------------------------------------------------------ products
@@ -258,6 +326,24 @@ def test_products_with_large_tiles(moe, d, f):
     torch.cuda.synchronize()
     _check(q, gu, h, y, sizes, d, f)
     assert torch.equal(y2, y)
+
+
+def test_products_past_32_bits(moe):
+    """More than 2^32 outputs: a block of rows over and over gives the same bits everywhere, up to the last row."""
+    _say("products-long")
+    n, reps, d, f = 512, 4200, 256, 1024
+    q = _case(moe, [n], d, f)
+    q["x"], q["xs"] = q["x"].repeat(reps, 1), q["xs"].repeat(reps, 1)
+    q["off"] = torch.tensor([0, n * reps], dtype=torch.int32, device=DEV)
+    assert n * reps * 2 * f > 1 << 32
+    gu, h, y = _forward(moe, q, d, f)
+    torch.cuda.synchronize()
+    for t in (gu, h, y):
+        b = t.view(reps, n, -1)
+        for i in (1, reps // 2, reps - 2, reps - 1):
+            assert torch.equal(b[i], b[0]), i
+    q["x"], q["xs"] = q["x"][:n].contiguous(), q["xs"][:n].contiguous()
+    _check(q, gu[:n], h[:n], y[:n], [n], d, f)
 
 
 def test_products_padded(moe):

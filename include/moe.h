@@ -472,7 +472,7 @@ MOE_API size_t moe_balance_workspace_bytes(int T, int E, int n_seg);
  * out  tokens     [n_seg + 1] int32: n_s, then N.
  * in   ws         device scratch of moe_balance_workspace_bytes(T, E, n_seg), 16-byte aligned.
  * out  dev_err    optional; MOE_ERR_NONFINITE_LOGIT.
- * T = 0 is allowed.  Two kernels, or one for few tokens.  Errors: MOE_EINVAL
+ * T = 0 is allowed.  One to three kernels.  Errors: MOE_EINVAL
  * (sizes: 0 <= T <= 2^30, T * k < 2^31, 1 <= k <= 8, k <= E <= 1024,
  * 1 <= n_seg <= 2^20, n_seg = 1 without seg_off; null pointers),
  * MOE_EWORKSPACE.

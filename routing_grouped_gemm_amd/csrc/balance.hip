@@ -7,7 +7,8 @@
 //   z       = c_z / N * sum_t lse_t^2,   lse_t = log sum_e exp(logits[t, e])
 //   dlogits = p_te * (g_b c_b E / N (f_se - sum_j f_sj p_tj) + g_z 2 c_z / N lse_t)
 // (the counts are piecewise constant).  Forward, two kernels (few tokens: the
-// first alone, in a single workgroup that finishes by itself):
+// first alone, in a single workgroup that finishes by itself; many sequences: a
+// third for the losses):
 //   1. balance_tokens_kernel: a workgroup takes a run of TB tokens; LPT lanes
 //      hold one token's logits, so its softmax is a few lane exchanges, and
 //      every lane keeps the running sums of p of its experts in registers.
@@ -16,7 +17,7 @@
 //      decrease from piece to piece and one of them grows, so rows are distinct).
 //   2. balance_reduce_kernel: per sequence and group of experts, the sums of
 //      its pieces' rows in a fixed order; the last workgroup to finish adds up
-//      the losses.
+//      the losses (or balance_losses_kernel does).
 // Backward, one kernel: the softmax again from the logits (p from a rounded lse
 // would lose |lse| * 2^-24 of relative accuracy).  No floating-point atomics:
 // results are the same bits on every run.
@@ -45,17 +46,34 @@ __device__ __forceinline__ int seg_at(const Tokens& a, int i)
 
 // Calls f(s, begin, end) for the pieces of [t0, t1) in order; s < 0 for tokens
 // outside every sequence.  Every piece holds a token whatever seg_off holds.
+// The first sequence that ends past t0 is searched by all 64 lanes at once, a
+// round trip to memory per factor of 64 (halving took 5 for 23 sequences: 2 us
+// of each kernel).
 template <class F>
 __device__ __forceinline__ void for_pieces(const Tokens& a, int t0, int t1, F&& f)
 {
-    int lo = 0, hi = a.S;   // first sequence that ends past t0
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (seg_at(a, mid + 1) > t0) hi = mid;
-        else lo = mid + 1;
-    }
-    int s = lo;
     const int first = seg_at(a, 0);
+    int s = 0, end_s = a.T;   // the sequence, and its end
+    if (a.seg_off) {
+        const int lane = threadIdx.x & 63;
+        int lo = 0, hi = a.S;
+        for (;;) {
+            const int step = (hi - lo + 63) >> 6;
+            const int i = min(lo + lane * step + step - 1, hi - 1);
+            const int v = seg_at(a, i + 1);
+            const unsigned long long past = __ballot(v > t0);
+            if (!past) {
+                s = a.S;
+                break;
+            }
+            const int l = __ffsll(past) - 1;
+            s = __builtin_amdgcn_readlane(i, l);
+            end_s = __builtin_amdgcn_readlane(v, l);
+            if (step == 1) break;
+            lo = s - min(step - 1, s - lo);
+            hi = s + 1;
+        }
+    }
     for (int cur = t0; cur < t1;) {
         if (cur < first) {
             const int end = min(t1, first);
@@ -63,8 +81,9 @@ __device__ __forceinline__ void for_pieces(const Tokens& a, int t0, int t1, F&& 
             cur = end;
             continue;
         }
-        while (s < a.S && seg_at(a, s + 1) <= cur) ++s;
-        const int end = s < a.S ? min(t1, seg_at(a, s + 1)) : t1;
+        while (s < a.S && end_s <= cur)
+            if (++s < a.S) end_s = seg_at(a, s + 1);
+        const int end = s < a.S ? min(t1, end_s) : t1;
         f(s < a.S ? s : -1, cur, end);
         cur = end;
     }
@@ -391,7 +410,8 @@ __global__ __launch_bounds__(NT) void balance_tokens_kernel(Tokens a, const int3
 
 // Workgroup (s, g): the sums of sequence s's pieces' rows over RW - 1 4-column
 // vectors (group g of them) and the rows' last vector: a wave per vector, a lane per row (every 64th), then the lanes.  The
-// last workgroup to finish makes the losses from what each left in `partial`.
+// last workgroup to finish (TICKET) or a kernel behind this one makes the losses
+// from what each left in `partial`.
 constexpr int RW = 8, RT = 64 * RW;
 
 struct Partial {
@@ -406,6 +426,53 @@ __device__ __forceinline__ int segment_sum(int x)
     return x;
 }
 
+// The losses from the partial ones of all sequences and groups (one workgroup).
+// ATOMIC: they were left by other workgroups of the same launch.
+template <bool ATOMIC>
+__device__ __forceinline__ void add_losses(const Partial* partial, int n, const Results& o, int S, int E)
+{
+    __shared__ float s_b[RW], s_z[RW];
+    __shared__ int s_n[RW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    float vb = 0.0f, vz = 0.0f;
+    int N = 0;
+    for (int i = tid; i < n; i += RT) {
+        if constexpr (ATOMIC) {
+            vb += __hip_atomic_load(&partial[i].b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            vz += __hip_atomic_load(&partial[i].z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (i < S) N += __hip_atomic_load(o.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        } else {
+            vb += partial[i].b;
+            vz += partial[i].z;
+            if (i < S) N += o.tokens[i];
+        }
+    }
+    vb = segment_sum<64>(vb);
+    vz = segment_sum<64>(vz);
+    N = segment_sum<64>(N);
+    if (lane == 0) {
+        s_b[wave] = vb;
+        s_z[wave] = vz;
+        s_n[wave] = N;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        for (int w = 1; w < RW; ++w) {
+            vb += s_b[w];
+            vz += s_z[w];
+            N += s_n[w];
+        }
+        write_losses(o, E, S, vb, vz, N);
+    }
+}
+
+__global__ __launch_bounds__(RT) void balance_losses_kernel(const Partial* __restrict__ partial, int n, Results o, int S,
+                                                            int E)
+{
+    add_losses<false>(partial, n, o, S, E);
+}
+
+template <bool TICKET>
 __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, const float4* __restrict__ fpart,
                                                             const int4* __restrict__ ipart, int rows,
                                                             int* __restrict__ ticket, Partial* __restrict__ partial,
@@ -413,8 +480,6 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, const floa
 {
     __shared__ float s_f[RW][4];
     __shared__ int s_i[RW][4];
-    __shared__ float s_b[RW], s_z[RW];
-    __shared__ int s_n[RW];
     __shared__ int s_last;
     const int s = blockIdx.x, g = blockIdx.y, ng = gridDim.y, tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
@@ -469,38 +534,23 @@ __global__ __launch_bounds__(RT) void balance_reduce_kernel(Tokens a, const floa
         // release writes back the XCD's whole L2.)
         if (lane == 0) {
             Partial* q = partial + s * ng + g;
-            const int o0 = atomicExch(reinterpret_cast<int*>(&q->b), __float_as_int(vb));
-            const int o1 = atomicExch(reinterpret_cast<int*>(&q->z), __float_as_int(g == 0 ? s_f[RW - 1][0] : 0.0f));
-            const int o2 = g == 0 ? atomicExch(o.tokens + s, n) : 0;
-            asm volatile("" :: "v"(o0), "v"(o1), "v"(o2) : "memory");
-            s_last = atomicAdd(ticket, 1) == a.S * ng - 1;
+            const float vz = g == 0 ? s_f[RW - 1][0] : 0.0f;
+            if constexpr (TICKET) {
+                const int o0 = atomicExch(reinterpret_cast<int*>(&q->b), __float_as_int(vb));
+                const int o1 = atomicExch(reinterpret_cast<int*>(&q->z), __float_as_int(vz));
+                const int o2 = g == 0 ? atomicExch(o.tokens + s, n) : 0;
+                asm volatile("" :: "v"(o0), "v"(o1), "v"(o2) : "memory");
+                s_last = atomicAdd(ticket, 1) == a.S * ng - 1;
+            } else {
+                q->b = vb;
+                q->z = vz;
+                if (g == 0) o.tokens[s] = n;
+            }
         }
     }
-    __syncthreads();
-    if (!s_last) return;
-    float vb = 0.0f, vz = 0.0f;
-    int N = 0;
-    for (int i = tid; i < a.S * ng; i += RT) {
-        vb += __hip_atomic_load(&partial[i].b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        vz += __hip_atomic_load(&partial[i].z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (i < a.S) N += __hip_atomic_load(o.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    vb = segment_sum<64>(vb);
-    vz = segment_sum<64>(vz);
-    N = segment_sum<64>(N);
-    if (lane == 0) {
-        s_b[wave] = vb;
-        s_z[wave] = vz;
-        s_n[wave] = N;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        for (int w = 1; w < RW; ++w) {
-            vb += s_b[w];
-            vz += s_z[w];
-            N += s_n[w];
-        }
-        write_losses(o, E, a.S, vb, vz, N);
+    if constexpr (TICKET) {
+        __syncthreads();
+        if (s_last) add_losses<true>(partial, a.S * ng, o, a.S, E);
     }
 }
 
@@ -569,16 +619,34 @@ int tokens_per_block(int T, int least, int most)
 // forward: two workgroups per CU, since each leaves a row of sums to add up
 // (2^16 tokens of 128 experts: 29 us with 1024 workgroups, 17 with 512)
 constexpr int kLeastFwd = 64, kMostFwd = 512;
+// A workgroup takes the sequences of its run one after another: no longer runs
+// than a sequence is on average, down to kShort tokens (300 tokens in 40
+// sequences: forward 33 -> 19 us, backward 17.5 -> 11.6; 16 tokens 24 and 15.5, 4
+// tokens as 8).
+constexpr int kShort = 8;
+int not_past_sequences(int tb, int T, int S)
+{
+    return std::min(tb, std::max((T / S + 7) / 8 * 8, kShort));
+}
+int tokens_per_block_fwd(int T, int S)
+{
+    return not_past_sequences(tokens_per_block(T, kLeastFwd, kMostFwd), T, S);
+}
+// Up to so many workgroups of the reduction take a ticket; more of them would
+// wait at it, one after another, for longer than another launch takes (64
+// sequences, 64 experts, 192 workgroups: 17.8 -> 16.2 us; 200 of 128, 1000: 30 ->
+// 22; 8 of 64, 24: 12.1 -> 12.4, a call 12.3 -> 14.2).
+constexpr int kTickets = 64;
 // backward: 32 KB of logits a workgroup, nothing to add up after it (2^20
 // tokens of 128 experts, with the gradient added on: 263 us; 64 KB 283, 128 KB
 // 303; of 16: 32.5, 33.0, 33.9), at least 32 tokens, and 512 workgroups before
 // they grow past that
 constexpr int kLeastBwd = 32, kElemsBwd = 8192, kFillBwd = 512;
-int tokens_per_block_bwd(int T, int E)
+int tokens_per_block_bwd(int T, int E, int S)
 {
     int64_t tb = kElemsBwd / E;
     tb = std::min<int64_t>(tb, T / kFillBwd) / 16 * 16;
-    return (int)(tb > kLeastBwd ? tb : kLeastBwd);
+    return not_past_sequences((int)(tb > kLeastBwd ? tb : kLeastBwd), T, S);
 }
 
 template <class F>
@@ -611,7 +679,7 @@ inline bool one_workgroup(int T, int E, int S) { return (int64_t)T * E <= 32768 
 
 inline int64_t piece_rows(int T, int S)
 {
-    const int tb = tokens_per_block(T, kLeastFwd, kMostFwd);
+    const int tb = tokens_per_block_fwd(T, S);
     return ((int64_t)T + tb - 1) / tb + S;
 }
 
@@ -649,7 +717,7 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
         });
         return hipGetLastError();
     }
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block(T, kLeastFwd, kMostFwd)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block_fwd(T, S)};
     uint8_t* w = static_cast<uint8_t*>(ws);
     int* ticket = reinterpret_cast<int*>(w);
     Partial* partial = reinterpret_cast<Partial*>(w + kTicketBytes);
@@ -663,8 +731,14 @@ hipError_t launch_balance(const float* logits, const int32_t* topk_idx, const ui
                            dim3((unsigned)nblk), dim3(NT), 0, s, a, topk_idx, k, over_k, lse, fpart, ipart, rows, ticket,
                            o, dev_err);
     });
-    hipLaunchKernelGGL(balance_reduce_kernel, dim3((unsigned)S, (unsigned)reduce_groups(E)), dim3(RT),
-                       0, s, a, fpart, ipart, rows, ticket, partial, o);
+    const int ng = reduce_groups(E);
+    const dim3 grid((unsigned)S, (unsigned)ng);
+    if ((int64_t)S * ng <= kTickets) {
+        hipLaunchKernelGGL(balance_reduce_kernel<true>, grid, dim3(RT), 0, s, a, fpart, ipart, rows, ticket, partial, o);
+    } else {
+        hipLaunchKernelGGL(balance_reduce_kernel<false>, grid, dim3(RT), 0, s, a, fpart, ipart, rows, ticket, partial, o);
+        hipLaunchKernelGGL(balance_losses_kernel, dim3(1), dim3(RT), 0, s, partial, S * ng, o, S, E);
+    }
     return hipGetLastError();
 }
 
@@ -673,7 +747,7 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
                               const float* add, float* dlogits, hipStream_t s)
 {
     if (T == 0) return hipSuccess;
-    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block_bwd(T, E)};
+    const Tokens a{logits, mask, seg_off, T, E, S, tokens_per_block_bwd(T, E, S)};
     const int nblk = (T + a.TB - 1) / a.TB;
     const bool vec = vec_ok(E, logits) && vec_ok(E, dlogits) && vec_ok(E, add);
     with_shape(T, E, vec, [&](auto L, auto N, auto V, auto ST) {

@@ -140,6 +140,24 @@ def test_few_tokens(moe, T, E, k, seg, masked):
     assert o["err"][0] == (moe.MOE_ERR_NONFINITE_LOGIT if counted else 0)
 
 
+@pytest.mark.parametrize("T,E,k,S", [(300, 16, 2, 40), (1000, 100, 4, 64), (5000, 130, 2, 300), (40000, 32, 2, 5000),
+                                     (700, 7, 3, 699), (64, 8, 2, 4100), (9000, 30, 1, 65)])
+def test_many_sequences(moe, T, E, k, S):
+    """Ragged sequences, some empty, tokens outside all of them; more of them than one search step and one ticket hold."""
+    _say("many", T, E, k, S)
+    g = np.random.default_rng(T + S)
+    seg = np.sort(g.integers(T // 50, T + 1 - T // 60, S + 1)).astype(np.int32)
+    x, idx = _inputs(T, E, k, T + S)
+    mask = (g.random(T) > 0.2).astype(np.uint8)
+    add = g.standard_normal((T, E)).astype(np.float32) * 1e-3
+    dl = (1.5, -0.5)
+    o = _run(moe, x, idx, 0.5, 0.1, list(seg), mask, dl, add)
+    _check(o, x, idx, 0.5, 0.1, list(seg), mask, dl, add)
+    o2 = _run(moe, x, idx, 0.5, 0.1, list(seg), mask, dl, add)
+    for n in ("losses", "counts", "probs", "lse", "tokens", "grad"):
+        np.testing.assert_array_equal(o2[n], o[n])
+
+
 def test_nothing_counted(moe):
     _say("nothing")
     x, idx = _inputs(100, 8, 2, 1)

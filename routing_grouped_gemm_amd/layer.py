@@ -124,16 +124,17 @@ class MoELayer:
         """Weights [E, 2f, d] and [E, d, f] (fp32 or bf16).  For MXFP8 the forward
         and backward MXFP8 caches are made here (once per optimizer step), for
         MXFP4 the codes of both."""
-        self.w13, self.w2 = w13, w2
-        self._stages = None
         if self.dtype == MOE_MXFP4:
             E, f, d = self.G, self.f, self.d
             u8 = dict(dtype=torch.uint8, device=self.device)
             self.set_weights_mxfp4(torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
                                    torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8),
                                    decode=False)
+            self.w13, self.w2 = w13, w2
             self.requantize_weights()
             return
+        self.w13, self.w2 = w13, w2
+        self._stages = None
         if self.dtype != MOE_MXFP8:
             return
         E, f, d = self.G, self.f, self.d
@@ -162,6 +163,7 @@ class MoELayer:
         if self.dtype != MOE_MXFP4:
             raise ValueError("set_weights_mxfp4 needs an MXFP4 layer")
         self.w13_q, self.w13_s, self.w2_q, self.w2_s = w13_q, w13_s, w2_q, w2_s
+        self.w13 = self.w2 = None   # these codes have no bf16 weights behind them
         self._stages = None
         if decode and self._bwd_alloc:
             self._decode_weights()
@@ -172,6 +174,8 @@ class MoELayer:
         MXFP4: rebuild the codes."""
         E, f, d = self.G, self.f, self.d
         if self.dtype == MOE_MXFP4:
+            if self.w13 is None:
+                raise ValueError("requantize_weights: the layer's weights were given in 4 bits")
             moe_quantize_mxfp4(self.w13.reshape(E * 2 * f, d), self.w13_q.view(E * 2 * f, -1),
                                self.w13_s.view(E * 2 * f, -1))
             moe_quantize_mxfp4(self.w2.reshape(E * d, f), self.w2_q.view(E * d, -1), self.w2_s.view(E * d, -1))

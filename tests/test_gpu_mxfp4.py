@@ -515,6 +515,27 @@ def test_layer_forward_backward(moe, T, d, E, f, k, S, C):
         serve.backward(g["dout"])
 
 
+def test_codes_given_to_a_layer_are_not_made_anew(moe):
+    """Weights given in 4 bits after bf16 ones: no call writes the old weights' codes into them."""
+    from routing_grouped_gemm_amd.layer import MoELayer
+    T, d, E, f, k = 20, 128, 4, 128, 2
+    inp = moe_synth.make_inputs(T=T, d=d, E=E, f=f, k=k, seed=3)
+    lay = MoELayer(T, d, E, f, k, moe.MOE_MXFP4)
+    lay.set_weights(inp["w13"].to(DEV), inp["w2"].to(DEV))
+    codes = [t.clone() for t in (lay.w13_q, lay.w13_s, lay.w2_q, lay.w2_s)]
+    codes[0].zero_()
+    lay.set_weights_mxfp4(*codes)
+    with pytest.raises(ValueError):
+        lay.requantize_weights()
+    assert not bool(codes[0].any())
+    out = lay.forward(inp["logits"].to(DEV), inp["x"].to(DEV))
+    torch.cuda.synchronize()
+    assert not bool(out.any())                       # silu(0) * 0
+    lay.set_weights(inp["w13"].to(DEV), inp["w2"].to(DEV))
+    lay.requantize_weights()
+    assert bool(lay.w13_q.any()) and not bool(codes[0].any())
+
+
 def test_two_layers_two_streams_and_graphs(moe):
     """Forwards of two layers captured in two graphs and replayed on two streams at once, with eager
     steps in between, give the eager results."""

@@ -108,7 +108,8 @@ class MoELayer:
             self.x_perm_d = torch.empty(R, d, dtype=act, device=dev)
             self.w13_d = torch.empty(E, 2 * f, d, dtype=act, device=dev)
             self.w2_d = torch.empty(E, d, f, dtype=act, device=dev)
-            self._decode_weights()
+            if self.w13 is not None:
+                self._decode_weights()
             self.bwd_ws = torch.empty(moe_gemm_workspace_bytes(MOE_BF16, E, R, d, f), dtype=torch.uint8,
                                       device=dev)
         self._bwd_alloc = True
@@ -128,8 +129,7 @@ class MoELayer:
             E, f, d = self.G, self.f, self.d
             u8 = dict(dtype=torch.uint8, device=self.device)
             self.set_weights_mxfp4(torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
-                                   torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8),
-                                   decode=False)
+                                   torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8))
             self.w13, self.w2 = w13, w2
             self.requantize_weights()
             return
@@ -157,16 +157,16 @@ class MoELayer:
         self.w2t_s = torch.empty(n2 // 32, **u8)
         self.requantize_weights()
 
-    def set_weights_mxfp4(self, w13_q, w13_s, w2_q, w2_s, decode=True):
+    def set_weights_mxfp4(self, w13_q, w13_s, w2_q, w2_s):
         """MXFP4: weights that are held in 4 bits already, codes [E, 2f, d/2] and [E, d, f/2]
-        with scales [E, 2f, d/32] and [E, d, f/32] (as moe_quantize_mxfp4 makes them)."""
+        with scales [E, 2f, d/32] and [E, d, f/32] (as moe_quantize_mxfp4 makes them).  The
+        layer reads these tensors at each step: they may be quantised anew in place between
+        steps, so the backward decodes them each time it runs."""
         if self.dtype != MOE_MXFP4:
             raise ValueError("set_weights_mxfp4 needs an MXFP4 layer")
         self.w13_q, self.w13_s, self.w2_q, self.w2_s = w13_q, w13_s, w2_q, w2_s
         self.w13 = self.w2 = None   # these codes have no bf16 weights behind them
         self._stages = None
-        if decode and self._bwd_alloc:
-            self._decode_weights()
 
     def requantize_weights(self):
         """MXFP8: rebuild the four weight caches (forward and backward direction
@@ -221,9 +221,11 @@ class MoELayer:
         dtype = self.dtype
         if dtype == MOE_MXFP4 and (bwd or op == MOE_GEMM_WGRAD):
             self._alloc_bwd()
-            bwd, dtype = True, MOE_BF16
             if op == MOE_GEMM_WGRAD:
                 self._decode_rows()
+            elif self.w13 is None:
+                self._decode_weights()
+            bwd, dtype = True, MOE_BF16
         moe_grouped_gemm_op(op, dtype, self._stages[1 if bwd else 0], self.s_off,
                             self.g_cap, self.G, self.n_rows, self.d, self.f)
 
@@ -340,6 +342,8 @@ class MoELayer:
                                  x_perm_scales=self.x_perm_scales, w13_scales=self.w13t_s,
                                  w2_scales=self.w2t_s, ws=self.gemm_ws)
         elif self.dtype == MOE_MXFP4:
+            if self.w13 is None:
+                self._decode_weights()
             self._decode_rows()
             moe_grouped_gemm_bwd(MOE_BF16, self.dy_perm, self.x_perm_d, self.gu, self.h, self.w13_d, self.w2_d,
                                  self.s_off, self.g_cap, self.dgu, self.dx_perm, self.dw13, self.dw2,

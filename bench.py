@@ -201,7 +201,7 @@ def run_gpu(args, cfg):
         mark(4)
         lay.combine(wts)
         mark(5)
-        m.moe_permute(act_dt, inp["dout"], lay.K, lay.s_dst, lay.dy_perm, src_slot=lay.s_src,
+        m.moe_permute(act_dt, inp["dout"], lay.K, lay.s_dst, lay.dy_perm, src_slot=lay.s_fill,
                       row_scale=wts, dev_err=lay.dev_err)
         mark(6)
         lay.gemm_stage(m.MOE_GEMM_DGRAD_DOWN)
@@ -255,7 +255,7 @@ def cold_cache(lay, inp, wts, act_dt, T, d, k, reps):
         "permute": lambda: lay.permute(inp["x"]),
         "combine": lambda: lay.combine(wts),
         "combine_bwd": lambda: m.moe_permute(act_dt, inp["dout"], lay.K, lay.s_dst, lay.dy_perm,
-                                             src_slot=lay.s_src, row_scale=wts, dev_err=lay.dev_err),
+                                             src_slot=lay.s_fill, row_scale=wts, dev_err=lay.dev_err),
         "permute_bwd": lambda: m.moe_unpermute_combine(act_dt, lay.dx_perm, lay.s_dst, None, lay.K, lay.dx,
                                                        dev_err=lay.dev_err),
     }

@@ -146,8 +146,10 @@ MOE_API int moe_route_topk_noalloc(const float* logits, int T, int E, int k, int
  *                 E8M0 [n_rows, d/32], as moe_quantize_mxfp4 writes them.
  * in   x          [T, d].
  * in   dst_row    [T*k] from moe_route_topk.
- * in   src_slot   [n_rows]; required when n_rows != T*k (padded): rows with
- *                 src_slot < 0 are zero-filled.  May be NULL otherwise.
+ * in   src_slot   [n_rows]: rows with src_slot < 0 are zero-filled.  Pass it for
+ *                 every padded layout (with E*C == T*k some experts drop pairs
+ *                 while others have empty rows); required when n_rows != T*k.
+ *                 NULL: no row is empty (unpadded).
  * in   row_scale  NULL, or [T*k] fp32: row (t, j) is written as
  *                 round(row_scale[t*k+j] * x[t]) (the backward of the weighted
  *                 combine).  Not combined with MOE_MXFP8 or MOE_MXFP4.
@@ -427,8 +429,8 @@ MOE_API int moe_router_logits(const void* x, const void* w_router, int T, int E,
  * out  dy_perm    [n_rows, d] bf16, optional: also writes the combine
  *                 backward dy_perm[dst] = topk_w * dout[t] (what moe_permute
  *                 with row_scale = topk_w writes) from the same dout reads.
- *                 Unpadded layouts only (n_rows == T*k): MOE_EUNSUPPORTED
- *                 otherwise, as padding rows would stay unwritten.
+ *                 Unpadded layouts only, as padding rows would stay
+ *                 unwritten: MOE_EUNSUPPORTED when n_rows != T*k.
  * out  dev_err    optional; MOE_ERR_ROW_RANGE for a destination >= n_rows
  *                 (that slot is then treated as dropped).
  * Errors: MOE_EINVAL (sizes: 1 <= k <= 8, k <= E <= 1024; null pointers),

@@ -212,7 +212,8 @@ def moe_route_topk_noalloc(logits, k, capacity, topk_idx, topk_w, counts, offset
 def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_perm_scales=None,
                 dev_err=None, stream=None):
     """x [T, d] -> x_perm [n_rows, d] (MXFP8: codes + x_perm_scales [n_rows, d/32]; MXFP4:
-    codes [n_rows, d/2] + x_perm_scales [n_rows, d/32])."""
+    codes [n_rows, d/2] + x_perm_scales [n_rows, d/32]).  src_slot [n_rows]: for a padded
+    layout; rows with src_slot < 0 become zero."""
     T, d = x.shape
     n_rows = x_perm.shape[0]
     if dtype == MOE_MXFP4:

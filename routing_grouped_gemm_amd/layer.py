@@ -66,6 +66,7 @@ class MoELayer:
         else:
             self.s_idx, self.s_w, self.s_dst, self.s_src = self.topk_idx, self.topk_w, self.dst_row, self.src_slot
             self.s_counts, self.s_off = self.counts, self.offsets
+        self.s_fill = self.s_src if capacity > 0 else None   # where a permute finds the empty rows
         # group offsets and capacity the grouped GEMM takes (shared groups: explicit offsets)
         self.g_cap = 0 if n_shared else capacity
         self.dev_err = torch.zeros(1, **i32)
@@ -253,7 +254,7 @@ class MoELayer:
                                  self.s_counts, self.s_off, self.s_dst, self.s_src)
 
     def permute(self, x):
-        moe_permute(self.dtype, x, self.K, self.s_dst, self.x_perm, src_slot=self.s_src,
+        moe_permute(self.dtype, x, self.K, self.s_dst, self.x_perm, src_slot=self.s_fill,
                     x_perm_scales=self.x_perm_scales, dev_err=self.dev_err)
 
     def gemm_fwd(self):
@@ -333,7 +334,7 @@ class MoELayer:
     def backward(self, dout, weights=None):
         self._alloc_bwd()
         act_dt = MOE_F32 if self.dtype == MOE_F32 else MOE_BF16
-        moe_permute(act_dt, dout, self.K, self.s_dst, self.dy_perm, src_slot=self.s_src,
+        moe_permute(act_dt, dout, self.K, self.s_dst, self.dy_perm, src_slot=self.s_fill,
                     row_scale=self._slot_weights(weights), dev_err=self.dev_err)
         if self.dtype == MOE_MXFP8:
             moe_grouped_gemm_bwd(self.dtype, self.dy_perm, self.x_perm, self.gu, self.h,

@@ -123,16 +123,26 @@ class MoELayer:
 
     # -------------------------------------------------------------- weights
     def set_weights(self, w13, w2):
-        """Weights [E, 2f, d] and [E, d, f] (fp32 or bf16).  For MXFP8 the forward
-        and backward MXFP8 caches are made here (once per optimizer step), for
-        MXFP4 the codes of both."""
+        """Weights [E, 2f, d] and [E, d, f] (MOE_F32: fp32, otherwise bf16).  For MXFP8
+        the forward and backward MXFP8 caches are made here (once per optimizer
+        step), for MXFP4 the codes of both; MXFP4 weights that are refused leave
+        the layer with the ones it had.  Each call makes new caches and a captured
+        graph reads those of its capture: for weights that change under a graph,
+        write them into w13 and w2 and call requantize_weights, which works in place."""
         if self.dtype == MOE_MXFP4:
             E, f, d = self.G, self.f, self.d
+            for name, w, n in (("w13", w13, E * 2 * f * d), ("w2", w2, E * d * f)):
+                if w.dtype is not torch.bfloat16 or w.numel() != n or w.get_device() != self.x_perm.get_device():
+                    raise ValueError(f"{name}: expected a torch.bfloat16 tensor of {n} elements on {self.x_perm.device}, "
+                                     f"got {w.dtype} {tuple(w.shape)} on {w.device}")
             u8 = dict(dtype=torch.uint8, device=self.device)
-            self.set_weights_mxfp4(torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
-                                   torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8))
+            codes = (torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
+                     torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8))
+            self._quantize_mxfp4(w13, w2, *codes)
+            self.set_weights_mxfp4(*codes)
             self.w13, self.w2 = w13, w2
-            self.requantize_weights()
+            if self._bwd_alloc:
+                self._decode_weights()
             return
         self.w13, self.w2 = w13, w2
         self._stages = None
@@ -169,6 +179,11 @@ class MoELayer:
         self.w13 = self.w2 = None   # these codes have no bf16 weights behind them
         self._stages = None
 
+    def _quantize_mxfp4(self, w13, w2, w13_q, w13_s, w2_q, w2_s):
+        E, f, d = self.G, self.f, self.d
+        moe_quantize_mxfp4(w13.reshape(E * 2 * f, d), w13_q.view(E * 2 * f, -1), w13_s.view(E * 2 * f, -1))
+        moe_quantize_mxfp4(w2.reshape(E * d, f), w2_q.view(E * d, -1), w2_s.view(E * d, -1))
+
     def requantize_weights(self):
         """MXFP8: rebuild the four weight caches (forward and backward direction
         of w13 and w2) from the bf16 weights in place, as an optimizer step does.
@@ -177,9 +192,7 @@ class MoELayer:
         if self.dtype == MOE_MXFP4:
             if self.w13 is None:
                 raise ValueError("requantize_weights: the layer's weights were given in 4 bits")
-            moe_quantize_mxfp4(self.w13.reshape(E * 2 * f, d), self.w13_q.view(E * 2 * f, -1),
-                               self.w13_s.view(E * 2 * f, -1))
-            moe_quantize_mxfp4(self.w2.reshape(E * d, f), self.w2_q.view(E * d, -1), self.w2_s.view(E * d, -1))
+            self._quantize_mxfp4(self.w13, self.w2, self.w13_q, self.w13_s, self.w2_q, self.w2_s)
             if self._bwd_alloc:
                 self._decode_weights()
             return

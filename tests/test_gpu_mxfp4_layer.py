@@ -1,4 +1,5 @@
-"""The MXFP4 layer between calls: codes refreshed in place reach the backward, eager and captured."""
+"""The MXFP4 layer between calls: codes refreshed in place reach the backward, eager and captured; the weight
+gradient by itself reads this batch's rows."""
 import sys
 
 import pytest
@@ -91,3 +92,29 @@ def test_codes_refreshed_in_place_reach_the_backward(moe):
             lay.gemm_stage(op)
     torch.cuda.synchronize()
     assert torch.equal(lay.dx_perm, want.dx_perm)
+
+
+def test_accumulating_after_single_stages_reads_this_batch(moe):
+    """The activation gradients stage by stage, then the weight gradient into fp32 accumulators without the
+    bf16 stage in between: it is this batch's, the rows of the batch before have been decoded there."""
+    _say("accumulate")
+    from routing_grouped_gemm_amd.layer import MoELayer
+    T, d, E, f, k = 90, 256, 4, 128, 2
+    a, b = _inputs(T, d, E, f, k, 5), _inputs(T, d, E, f, k, 6)
+    lay, want = (MoELayer(T, d, E, f, k, moe.MOE_MXFP4) for _ in range(2))
+    for x in (lay, want):
+        x.set_weights(a["w13"], a["w2"])
+    lay.forward(a["logits"], a["x"])
+    lay.backward(a["dout"])
+    acc = [[torch.zeros(E, 2 * f, d, device=DEV), torch.zeros(E, d, f, device=DEV)] for _ in range(2)]
+    for x in (lay, want):
+        x.forward(b["logits"], b["x"])
+    want.backward(b["dout"])
+    want.wgrad_accumulate(*acc[1])
+    moe.moe_permute(moe.MOE_BF16, b["dout"], k, lay.s_dst, lay.dy_perm, row_scale=lay.s_w)
+    for op in (moe.MOE_GEMM_DGRAD_DOWN, moe.MOE_GEMM_DGRAD_GATE_UP):
+        lay.gemm_stage(op)
+    lay.wgrad_accumulate(*acc[0])
+    torch.cuda.synchronize()
+    assert torch.equal(lay.dx_perm, want.dx_perm)
+    assert torch.equal(acc[0][0], acc[1][0]) and torch.equal(acc[0][1], acc[1][1])

@@ -1,11 +1,14 @@
 """The MXFP4 layer between calls: codes refreshed in place reach the backward, eager and captured; the weight
-gradient by itself reads this batch's rows."""
+gradient by itself reads this batch's rows; dw2 from the 4-bit h."""
 import sys
 
+import numpy as np
 import pytest
 import torch
 
 import moe_synth
+from tests import _plain
+from tests._chain import BF16_TOL, assert_close, np64
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -118,3 +121,71 @@ def test_accumulating_after_single_stages_reads_this_batch(moe):
     torch.cuda.synchronize()
     assert torch.equal(lay.dx_perm, want.dx_perm)
     assert torch.equal(acc[0][0], acc[1][0]) and torch.equal(acc[0][1], acc[1][1])
+
+
+@pytest.mark.parametrize("T,d,E,f,k,S,C", [(300, 256, 6, 256, 2, 0, 0), (64, 128, 8, 128, 2, 1, 0),
+                                           (120, 384, 4, 128, 2, 0, 60)])
+def test_dw2_of_the_forward_that_ran(moe, T, d, E, f, k, S, C):
+    """decode_h: dw2 is the derivative of <dout, out> in the (decoded) W2, by the formula and by differences
+    of a 64-bit forward; the other gradients are those of the layer without it."""
+    _say("dw2", T, d, E, f, k, S, C)
+    from routing_grouped_gemm_amd.layer import MoELayer
+    inp = moe_synth.make_inputs(T=T, d=d, E=E + S, f=f, k=k, seed=T)
+    inp["logits"] = inp["logits"][:, :E].contiguous()
+    g = {n: inp[n].to(DEV) for n in ("logits", "x", "w13", "w2", "dout")}
+    lays = []
+    for decode in (False, True):
+        lay = MoELayer(T, d, E, f, k, moe.MOE_MXFP4, capacity=C, n_shared=S, decode_h=decode)
+        lay.set_weights(g["w13"], g["w2"])
+        lay.forward(g["logits"], g["x"])
+        lay.backward(g["dout"])
+        lays.append(lay)
+    torch.cuda.synchronize()
+    plain, lay = lays
+    for n in ("out", "dx", "dw13"):
+        assert torch.equal(getattr(plain, n), getattr(lay, n)), n
+    off = lay.s_off.cpu().numpy().astype(np.int64)
+    if C and not S:
+        off = np.arange(E + 1) * C
+    h, w2 = np64(lay.h), np64(lay.w2_d)
+    used = np.zeros(h.shape[0], bool)
+    for a, b in zip(off[:-1], off[1:]):
+        used[a:b] = True
+    hq = np.zeros_like(h)
+    hq[used] = _plain.mxfp4_qdq(h[used])
+    np.testing.assert_array_equal(np64(lay.h_d)[used], hq[used])
+    dst, w = lay.s_dst.cpu().numpy(), np64(lay.s_w).reshape(-1)
+    K = k + S
+    dout = np64(inp["dout"])
+    dy = np.zeros((h.shape[0], d))
+    live = dst >= 0
+    dy[dst[live]] = w[live, None] * dout[np.nonzero(live)[0] // K]
+    want = np.stack([dy[a:b].T @ hq[a:b] for a, b in zip(off[:-1], off[1:])])
+    assert_close(np64(lay.dw2), want, BF16_TOL, "dw2")
+    other = np.stack([dy[a:b].T @ h[a:b] for a, b in zip(off[:-1], off[1:])])
+    assert_close(np64(plain.dw2), other, BF16_TOL, "dw2 of the saved h")
+
+    def loss(w2):
+        y = np.concatenate([hq[a:b] @ m.T for a, b, m in zip(off[:-1], off[1:], w2)])
+        y = np.concatenate([y, np.zeros((h.shape[0] - len(y), d))])
+        out = np.zeros((T, d))
+        np.add.at(out, np.nonzero(live)[0] // K, w[live, None] * y[dst[live]])
+        return (out * dout).sum()
+
+    rng = np.random.default_rng(1)
+    for _ in range(10):
+        e, i, j = rng.integers(E + S), rng.integers(d), rng.integers(f)
+        hi, lo = w2.copy(), w2.copy()
+        hi[e, i, j] += 0.5
+        lo[e, i, j] -= 0.5
+        diff = loss(hi) - loss(lo)                     # the forward is linear in W2
+        assert abs(diff - want[e, i, j]) <= 1e-9 * np.abs(want).max()
+    # stage by stage, and into fp32 accumulators
+    ref = lay.dw2.clone()
+    lay.dw2.zero_()
+    lay.gemm_stage(moe.MOE_GEMM_WGRAD)
+    a13, a2 = torch.zeros(E + S, 2 * f, d, device=DEV), torch.zeros(E + S, d, f, device=DEV)
+    lay.wgrad_accumulate(a13, a2)
+    torch.cuda.synchronize()
+    assert torch.equal(lay.dw2, ref)
+    assert_close(np64(a2), want, BF16_TOL, "dw2 accumulated")

@@ -38,3 +38,12 @@ def test_refused_weights_leave_the_earlier_ones(m, bad):
     assert all(a is b for a, b in zip((lay.w13_q, lay.w13_s, lay.w2_q, lay.w2_s), codes))
     assert lay.w13 is None and lay.w2 is None
     assert not any(bool(c.any()) for c in codes)
+
+
+def test_decode_h_is_refused_where_there_is_no_4_bit_h(m):
+    from routing_grouped_gemm_amd.layer import MoELayer
+    for dtype in (m.MOE_F32, m.MOE_BF16, m.MOE_MXFP8):
+        with pytest.raises(ValueError):
+            MoELayer(T, D, E, F, K, dtype, device="cpu", decode_h=True)
+    with pytest.raises(ValueError):
+        MoELayer(T, D, E, F, K, m.MOE_MXFP4, device="cpu", save=False, decode_h=True)

@@ -326,20 +326,30 @@ class MoELayer:
                       dev_err=self.dev_err)
         return self.dlogits
 
+    def _balance_buffers(self, n):
+        # Tensors for n sequences, out of the latest set made, which has at least as many.  Sets double in
+        # size and are kept with the layer: a captured balance_loss replays into the one it was given.
+        if not hasattr(self, "_balance_sets"):
+            self._balance_sets = []
+            self.balance_losses = torch.empty(2, dtype=torch.float32, device=self.device)
+        if not self._balance_sets or self._balance_sets[-1][0] < n:
+            m = 1 << (n - 1).bit_length()
+            dev = self.device
+            self._balance_sets.append((m, torch.empty(m, self.E, dtype=torch.int32, device=dev),
+                                       torch.empty(m, self.E, dtype=torch.float32, device=dev),
+                                       torch.empty(m + 1, dtype=torch.int32, device=dev),
+                                       torch.empty(moe_balance_workspace_bytes(self.T, self.E, m), dtype=torch.uint8,
+                                                   device=dev)))
+        _, counts, probs, tokens, self.balance_ws = self._balance_sets[-1]
+        self.balance_counts, self.balance_probs, self.balance_tokens = counts[:n], probs[:n], tokens[:n + 1]
+
     def balance_loss(self, logits, balance_coef, z_coef=0.0, seg_off=None, mask=None):
         """losses [2] fp32 on the device: the balance loss and the z loss of the router's
         logits under the last route, over the packed sequences seg_off [n_seg+1] int32
         (None: the batch as one), tokens with mask [T] uint8 = 0 left out.  The counts
-        and mean probabilities per sequence stay in balance_counts, balance_probs."""
-        n = 1 if seg_off is None else seg_off.numel() - 1
-        if getattr(self, "balance_counts", None) is None or self.balance_counts.shape[0] != n:
-            dev = self.device
-            self.balance_losses = torch.empty(2, dtype=torch.float32, device=dev)
-            self.balance_counts = torch.empty(n, self.E, dtype=torch.int32, device=dev)
-            self.balance_probs = torch.empty(n, self.E, dtype=torch.float32, device=dev)
-            self.balance_tokens = torch.empty(n + 1, dtype=torch.int32, device=dev)
-            self.balance_ws = torch.empty(moe_balance_workspace_bytes(self.T, self.E, n), dtype=torch.uint8,
-                                          device=dev)
+        and mean probabilities per sequence stay in balance_counts, balance_probs until
+        the next call."""
+        self._balance_buffers(1 if seg_off is None else seg_off.numel() - 1)
         moe_balance_loss(logits, self.topk_idx, balance_coef, z_coef, self.balance_losses, self.balance_counts,
                          self.balance_probs, None, self.balance_tokens, self.balance_ws, seg_off=seg_off, mask=mask,
                          dev_err=self.dev_err)

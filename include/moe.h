@@ -353,6 +353,10 @@ MOE_API int moe_quantize_mxfp8(const void* src, int64_t rows, int K, int colwise
  * scale per 32 elements along K.  scale = 2^e with e the smallest integer
  * such that block_max / 2^e <= 6 (clamped to [-127, 127]; an all-zero block
  * gets e = -127), stored as e + 127; codes = round-to-nearest-even(v / 2^e).
+ * The OCP specification's own conversion takes e = floor(log2 block_max) - 2
+ * and saturates at 6: the two agree except for blocks whose maximum has a
+ * significand above 1.5 (in [1, 2)), which get the next larger scale here and
+ * a clipped maximum there.  Either is read back by the same rule.
  * E2M1 has no infinity and no NaN: a block with an element that is not finite
  * gets the NaN scale 255 and zero codes, so that what is computed from it is
  * NaN rather than an ordinary number.

@@ -28,7 +28,8 @@ __device__ __forceinline__ uint32_t amax8(uint4 v)
 // Scale byte (e + 127) of a block whose largest magnitude is amax: e is the
 // smallest integer in [-127, 127] with amax <= 6 * 2^e = 1.5 * 2^(e+2).  With
 // amax = m * 2^E, m in [1, 2), that is E - 2, or E - 1 when m > 1.5; a
-// subnormal or zero amax is below 6 * 2^-127.  The elements have neither
+// subnormal or zero amax is below 6 * 2^-127.  (The OCP conversion takes E - 2
+// and saturates; where m > 1.5 this one keeps the maximum instead.)  The elements have neither
 // infinity nor NaN, so either takes the scale's NaN (255).
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax)
 {

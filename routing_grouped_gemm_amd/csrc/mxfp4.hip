@@ -16,9 +16,11 @@ namespace {
 // all, a multiple of 4), NV a thread, all of its loads in flight together;
 // runs past the grid's end are taken in turn.  STREAM: non-temporal access, for
 // sources past the 256 MB last-level cache.  Bound by the reads and writes:
-// [49152, 4096] quantises in 79 us (6.4 TB/s, with plain accesses 90) and
-// decodes in 70 (7.2 TB/s; 92), [16384, 4096] in 24 and 25.  One vector a
-// thread took 85 and 95 us, eight 82 and 73.
+// called again and again, [49152, 4096] quantises in 79 us (6.4 TB/s, with plain
+// accesses 90) and decodes in 70 (7.2 TB/s; 92); one after the other 80 and 76
+// (6.7 TB/s); with the caches full of other data 84 and 100.  [16384, 4096], which
+// the last-level cache holds, takes 24 and 25.  One vector a thread took 85 and
+// 95 us, eight 82 and 73.
 constexpr int NV = 2;
 constexpr int kMaxGrid = 1 << 20;
 typedef __attribute__((ext_vector_type(4))) uint32_t vu4;
@@ -79,10 +81,13 @@ __global__ __launch_bounds__(256) void dequant_rows4_kernel(const uint32_t* __re
 // vectors): one workgroup per token, thread v on vectors v, v + 256, ..., its
 // destinations workgroup-uniform (scalar loads, once per token); otherwise
 // thread i quantises vector (i % nvec) of token row (i / nvec).  Bound by the
-// reads and writes: 32768 tokens of 4096 to one row each 60 us (5.7 TB/s; 68
-// without ROW), 16384 of 2048 to eight 34 us (6.1 TB/s).  The codes are stored
-// for the product that reads them next: past the caches the dispatch is 50 us,
-// but dispatch and product together go from 510 to 520.
+// reads and writes: called again and again, 32768 tokens of 4096 to one row each
+// 62 us (5.5 TB/s; 68 without ROW), 16384 of 2048 to eight 33 us (6.3 TB/s);
+// without ROW 65536 of 1024 to one 31 us (5.5 TB/s), 32768 of 1024 to four 24 us,
+// 262144 of 256 to two 38 us (5.5 TB/s).  Between products, which fill the caches
+// with other data, the first takes 75 to 78 us.  The codes are stored for the
+// product that reads them next: past the caches the dispatch is 50 us called
+// again and again, but dispatch and product together go from 510 to 520.
 template <int K, bool ROW>
 __global__ __launch_bounds__(256) void permute_mx4_kernel(const uint4* __restrict__ x, int T, int nvec,
                                                           const int32_t* __restrict__ dst_row, int64_t n_rows,

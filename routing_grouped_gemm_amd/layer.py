@@ -358,7 +358,8 @@ class MoELayer:
 
     def balance_loss_grad(self, logits, dlosses=None, add_to=None):
         """dlogits [T, E]: add_to (the layer's dlogits after gate_grad, say; None: zeros) plus
-        the gradient of <dlosses, losses> of the last balance_loss."""
+        the gradient of <dlosses, losses> of the last balance_loss.  It is the one tensor that
+        gate_grad writes too: pass add_to=self.dlogits for the sum of both."""
         cb, cz, seg_off, mask = self._balance
         if getattr(self, "dlogits", None) is None:
             self.dlogits = torch.empty(self.T, self.E, dtype=torch.float32, device=logits.device)

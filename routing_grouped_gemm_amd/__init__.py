@@ -225,6 +225,8 @@ def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_p
               _dense("x_perm", x_perm, torch.uint8, n_rows, d // 2),
               _dense("x_perm_scales", x_perm_scales, torch.uint8, n_rows, d // 32), _p(dev_err))
         return
+    if torch.is_tensor(src_slot) and src_slot.numel() != n_rows:
+        raise ValueError(f"src_slot: expected {n_rows} rows, as x_perm has, got {src_slot.numel()}")
     rc = load().moe_permute(dtype, _p(x), T, d, k, _p(dst_row), _p(src_slot), _p(row_scale),
                             n_rows, _p(x_perm), _p(x_perm_scales), _p(dev_err), _s(stream))
     _check(rc, "moe_permute")

@@ -272,7 +272,8 @@ class MoELayer:
         if mx4:   # the activation gradients may have come stage by stage, which decodes no rows
             self._decode_rows()
         t = gemm_tensors(x_perm=self.x_perm_d if mx4 else self.x_perm, h=self.h_d if mx4 else self.h,
-                         dy_perm=self.dy_perm, dgu=self.dgu, dw13_f32=dw13_f32, dw2_f32=dw2_f32, ws=self.bwd_ws if mx4 else self.gemm_ws)
+                         dy_perm=self.dy_perm, dgu=self.dgu, dw13_f32=dw13_f32, dw2_f32=dw2_f32,
+                         ws=self.bwd_ws if mx4 else self.gemm_ws)
         moe_grouped_gemm_op(MOE_GEMM_WGRAD, MOE_BF16 if mx4 else self.dtype, t, self.s_off, self.g_cap, self.G,
                             self.n_rows, self.d, self.f)
 

@@ -79,3 +79,12 @@ def test_balance_workspace_grows_with_the_sequences(m):
         for E_ in (1, 8, 130, 1024):
             sizes = [m.moe_balance_workspace_bytes(T_, E_, n) for n in list(range(1, 70)) + [100, 999, 5000, 1 << 16, 1 << 20]]
             assert sizes == sorted(sizes), (T_, E_)
+
+
+def test_src_slot_of_another_length_is_refused(m):
+    """moe_permute reads a slot for each row of x_perm."""
+    x, dst = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int32)
+    out = torch.zeros(8, 64, dtype=torch.bfloat16)
+    for n in (7, 9):
+        with pytest.raises(ValueError):
+            m.moe_permute(m.MOE_BF16, x, 2, dst, out, src_slot=torch.zeros(n, dtype=torch.int32))

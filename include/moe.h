@@ -2,7 +2,8 @@
  * moe.h -- C ABI of one GPU's MoE feed-forward layer on AMD Instinct MI355X
  * (gfx950): router top-k and route map, rowwise dispatch (permute), grouped
  * SwiGLU GEMM forward and backward, weighted un-permute/combine, the MXFP8
- * and MXFP4 block quantisers, and the router's balance loss.
+ * and MXFP4 block quantisers, the router's balance loss, gated blocks of other
+ * gates with dropout, and experts in 4-bit integers for few tokens.
  *
  * The operations follow the pages describing the OLMo-core 3 MoE training
  * stack ("OLMo-core 3: MoE 训练栈..." tutorial; "Ai2 Olmo-core 3: The Secret
@@ -516,6 +517,163 @@ MOE_API int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, const
                                  int T, int E, const int32_t* counts, const int32_t* tokens, float balance_coef,
                                  float z_coef, const float* dlosses, const float* add, float* dlogits,
                                  moe_stream_t stream);
+
+/* Gates of a gated block, a(g) in h = a(g) * u. */
+enum moe_act {
+    MOE_ACT_SILU = 0,            /* g / (1 + exp(-g))                                       */
+    MOE_ACT_GELU = 1,            /* g * Phi(g), Phi the normal distribution function        */
+    MOE_ACT_GELU_TANH = 2,       /* g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))           */
+    MOE_ACT_RELU = 3             /* max(g, 0)                                               */
+};
+
+/*
+ * Dropout, without a mask in memory: whether an element is kept follows from
+ * its number i in the flat tensor, a seed and a step, by the counter-based
+ * generator Philox 4x32 with ten rounds (Salmon, Moraes, Dror and Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3", 2011).  Key: the low and high
+ * 32 bits of the seed.  Counter: the low and high 32 bits of i / 8, then those
+ * of the step.  Element 8b + j takes 16 bits of the four result words: the low
+ * (j even) or high (j odd) half of word j / 2.  It is dropped where those are
+ * below thr = min(round(65536 p), 65535), and otherwise multiplied by
+ * 65536 / (65536 - thr): p is taken to the nearest 2^-16, and the expected value
+ * is exact for the p so taken.  A dropped element is 0 whatever it was (an
+ * infinity or a NaN too).
+ *
+ * rng is a device pointer to {seed, step}: read when the kernels run, so that
+ * a captured graph draws a new mask once the caller has advanced the step.  The
+ * same {seed, step} gives the same mask in the forward and the backward;
+ * different steps, and different seeds, give independent ones.  Two tensors that
+ * must not share a mask need different {seed, step}.
+ *
+ *   out = (residual or 0) + drop(x)
+ * in   dtype      MOE_F32 or MOE_BF16 (x, residual, out), one rounding at the end.
+ * in   n          elements, a multiple of 8 (MOE_F32: 4).
+ * in   residual   [n] or NULL.
+ * in   p          0 <= p < 1.  p = 0 drops nothing and rng may be NULL.
+ * out  out        [n].  May be x or residual itself; no other overlap.
+ * The backward for x is the same call on the upstream gradient without a
+ * residual.  Errors: MOE_EUNSUPPORTED (dtype), MOE_EINVAL (sizes, p, null
+ * pointers), MOE_EALIGN (n, pointers; rng 8-byte aligned).
+ */
+MOE_API int moe_dropout(int dtype, const void* x, const void* residual, int64_t n, float p,
+                        const uint64_t* rng, void* out, moe_stream_t stream);
+
+/*
+ * moe_unpermute_combine, dropout of its result and the residual in one pass:
+ *   out[t] = (residual[t] or 0) + drop(sum over j of weights[t*k+j] * y_perm[dst_row[t*k+j]])
+ * the mask being that of moe_dropout over the [T, d] output, the sum in fp32 and
+ * rounded with the residual once.  Its backward is moe_dropout of the upstream
+ * gradient with the same rng and p, then the backward of the combine.
+ * Arguments as there and for moe_dropout; residual [T, d] may be out itself.
+ */
+MOE_API int moe_combine_dropout(int dtype, const void* y_perm, const int32_t* dst_row, const float* weights,
+                                const void* residual, int T, int k, int d, int64_t n_rows, float p,
+                                const uint64_t* rng, void* out, int32_t* dev_err, moe_stream_t stream);
+
+/*
+ * A gated block's form: its gate, a limit L on what goes into it (0: none), and
+ * dropout of h.  With g' = min(g, L) and u' = clamp(u, -L, L),
+ *   h = drop(a(g') * u')
+ * the mask over the flat [n_rows, f] tensor h as moe_dropout's.
+ */
+typedef struct moe_glu {
+    int act;                     /* MOE_ACT_*                      */
+    float limit;                 /* L > 0, or 0                    */
+    float p;                     /* 0 <= p < 1                     */
+    const uint64_t* rng;         /* device {seed, step}; p = 0: may be NULL */
+} moe_glu;
+
+/*
+ * The grouped GEMM stages, forward and backward with a gated block of this
+ * form: the projections, gate, product, limit and dropout of one stage in one
+ * kernel, MOE_F32 and MOE_BF16.  Arguments and errors as moe_grouped_gemm_op,
+ * _fwd and _bwd, which are the case SILU, L = 0, p = 0 (bit for bit).  h is saved
+ * after its dropout, and the backward makes the mask again:
+ *   dh = drop(dy Wd);  dg = dh u' a'(g') where g <= L, else 0;
+ *   du = dh a(g') where |u| <= L, else 0;  a'(0) = 0 for RELU;
+ * with g and u as saved (bf16 for MOE_BF16).  The stages that the form does not
+ * touch (DOWN, DGRAD_GATE_UP, WGRAD) are the ones of moe_grouped_gemm_op.
+ * MOE_EUNSUPPORTED for MOE_MXFP8 and MOE_MXFP4; MOE_EINVAL for a form that is
+ * NULL or out of range.
+ */
+MOE_API int moe_grouped_glu_op(int op, int dtype, const moe_glu* glu, const moe_gemm_tensors* t,
+                               const int32_t* group_off, int capacity, int E, int64_t n_rows, int d, int f,
+                               moe_stream_t stream);
+MOE_API int moe_grouped_glu_fwd(int dtype, const moe_glu* glu, const void* x_perm, const void* w13, const void* w2,
+                                const int32_t* group_off, int capacity, int E, int64_t n_rows, int d, int f,
+                                void* gu, void* h, void* y_perm, moe_stream_t stream);
+MOE_API int moe_grouped_glu_bwd(int dtype, const moe_glu* glu, const void* dy_perm, const void* x_perm,
+                                const void* gu, const void* h, const void* w13, const void* w2,
+                                const int32_t* group_off, int capacity, int E, int64_t n_rows, int d, int f,
+                                void* dgu, void* dx_perm, void* dw13, void* dw2, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/*
+ * 4-bit integers with a scale, and optionally a zero point, for each `group`
+ * (32, 64 or 128) elements along K:  value = (code - zero) * scale.
+ *   codes  [rows, K/2]: element 2i of a row in the low four bits of byte i.
+ *   scales [rows, K/group] bf16.
+ *   zeros  [rows, K/group] bytes 0 .. 15, or NULL: 8 everywhere.
+ * Quantiser, every step in fp32 and to the nearest (even at ties):
+ *   without zeros  scale = bf16(max |v| / 7),              code = 8 + clamp(round(v / scale), -8, 7)
+ *   with zeros     lo = min(v, 0), hi = max(v, 0) over the group,
+ *                  scale = bf16((hi/2 - lo/2) / 7.5),      zero = clamp(round(-lo / scale), 0, 15)
+ *                                                          code = clamp(round(v / scale) + zero, 0, 15)
+ * and at least 2^-126 for a scale.  A group with an element that is not finite
+ * gets a NaN scale, codes 8 and zero 8: its values are NaN.
+ * in   src [rows, K] bf16, K a multiple of group.
+ * Errors: MOE_EINVAL (sizes, null pointers), MOE_EUNSUPPORTED (group),
+ * MOE_EALIGN (K % group; src or codes not 16-byte aligned; scales 2-byte).
+ */
+MOE_API int moe_quantize_int4(const void* src, int64_t rows, int K, int group, uint8_t* codes, void* scales,
+                              uint8_t* zeros, moe_stream_t stream);
+
+/* The values of such codes, rounded to bf16: dst [rows, K].  Errors as above. */
+MOE_API int moe_dequantize_int4(const uint8_t* codes, const void* scales, const uint8_t* zeros, int64_t rows, int K,
+                                int group, void* dst, moe_stream_t stream);
+
+/* A weight tensor in 4-bit integers: the matrix of expert e follows that of e - 1. */
+typedef struct moe_int4 {
+    const uint8_t* codes;        /* [E, N, K/2]              */
+    const void* scales;          /* [E, N, K/group] bf16     */
+    const uint8_t* zeros;        /* [E, N, K/group], or NULL */
+} moe_int4;
+
+/* Bytes of scratch moe_int4_ffn needs for n_rows = T * k (0 for invalid sizes). */
+MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
+
+/*
+ * The layer's feed-forward over experts in 4-bit integers, for serving: from
+ * token rows to combined outputs, the dispatch and the combine included.
+ *   h_j = a(g') u' with g | u = x[t] W13[e_j]^T,   out[t] = sum_j topk_w[t, j] * (h_j W2[e_j]^T)
+ * Activations are bf16 (h is rounded to bf16), sums fp32; weights are read as they
+ * are and not rounded: a group's sum of x * (code - zero) is multiplied by its
+ * scale in fp32.  Made for few rows an expert, single tokens above all; any T is
+ * right.  Rows of many more tokens run faster as MOE_BF16 on moe_dequantize_int4
+ * of the weights.
+ * in   glu        gate and limit; p must be 0 (MOE_EUNSUPPORTED).
+ * in   x          [T, d] bf16.
+ * in   the route of moe_route_topk (capacity 0), or widened by
+ *                 moe_route_add_shared: topk_idx, topk_w, dst_row [T, k],
+ *                 src_slot [T*k], group_off [E+1].  A slot with dst_row < 0 adds
+ *                 nothing; one whose expert or row is out of range neither (flagged).
+ * in   w13        N = 2f (gate rows, then up rows), K = d.  w2: N = d, K = f.
+ * out  out        [T, d] bf16, every row written.  Must not overlap x.
+ * in   ws         moe_int4_workspace_bytes(T*k, d, f) bytes, 16-byte aligned.
+ * out  dev_err    optional; MOE_ERR_ROW_RANGE.
+ * Which of its kernels run depends on the sizes, and with that the order of the
+ * fp32 sums: a token's output may differ in the last bits between batches.
+ * A token row with an infinity or a NaN gives NaN.
+ * Errors: MOE_EINVAL (sizes: k <= 8, E <= 1024, T * k < 2^31, d and f at most
+ * 2^20; null pointers), MOE_EUNSUPPORTED (group, p), MOE_EALIGN (d or f not a
+ * multiple of group; x, out, codes not 16-byte aligned, scales not 2-byte),
+ * MOE_EWORKSPACE.
+ */
+MOE_API int moe_int4_ffn(const moe_glu* glu, const void* x, int T, int k, const int32_t* topk_idx,
+                         const float* topk_w, const int32_t* dst_row, const int32_t* src_slot,
+                         const int32_t* group_off, int E, int d, int f, int group, const moe_int4* w13,
+                         const moe_int4* w2, void* out, void* ws, size_t ws_bytes, int32_t* dev_err,
+                         moe_stream_t stream);
 
 /* Static text naming a status code. */
 MOE_API const char* moe_status_string(int status);

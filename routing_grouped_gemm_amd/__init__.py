@@ -16,7 +16,10 @@ import torch
 
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, -1, -2, -3, -4, -5
 MOE_F32, MOE_BF16, MOE_MXFP8, MOE_MXFP4 = 0, 1, 2, 3
+MOE_INT4 = 4   # of MoELayer (moe_int4_ffn has no dtype argument)
 MOE_ERR_NONFINITE_LOGIT, MOE_ERR_ROW_RANGE = 1, 2
+
+MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU = 0, 1, 2, 3
 
 MOE_GEMM_GATE_UP, MOE_GEMM_DOWN, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD = \
     0, 1, 2, 3, 4
@@ -25,7 +28,9 @@ ABI_FUNCTIONS = ("moe_route_workspace_bytes", "moe_route_topk", "moe_route_topk_
                  "moe_gemm_workspace_bytes", "moe_grouped_gemm_fwd", "moe_grouped_gemm_bwd",
                  "moe_grouped_gemm_op", "moe_unpermute_combine", "moe_quantize_mxfp8",
                  "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_route_add_shared", "moe_router_logits",
-                 "moe_gate_grad", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_bwd",
+                 "moe_gate_grad", "moe_dropout", "moe_combine_dropout", "moe_grouped_glu_op", "moe_grouped_glu_fwd",
+                 "moe_grouped_glu_bwd", "moe_quantize_int4", "moe_dequantize_int4", "moe_int4_workspace_bytes",
+                 "moe_int4_ffn", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_bwd",
                  "moe_status_string", "moe_version")
 
 GEMM_TENSOR_FIELDS = ("x_perm", "x_perm_scales", "w13", "w13_scales", "w2", "w2_scales", "gu",
@@ -37,6 +42,18 @@ class MoeGemmTensors(ctypes.Structure):
     """C struct moe_gemm_tensors (device pointers, NULL where unused)."""
     _fields_ = [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS] + [("ws_bytes", ctypes.c_size_t)] + \
         [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS_F32]
+
+
+class MoeGlu(ctypes.Structure):
+    """C struct moe_glu; made by glu(), which keeps the rng tensor alive with it."""
+    _fields_ = [("act", ctypes.c_int), ("limit", ctypes.c_float), ("p", ctypes.c_float), ("rng", ctypes.c_void_p)]
+    rng_tensor = None
+
+
+class MoeInt4(ctypes.Structure):
+    """C struct moe_int4."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -93,6 +110,26 @@ def load():
     lib.moe_gate_grad.restype = I
     lib.moe_gate_grad.argtypes = [P, P, P, P, P, I, I, I, I, I64, P, P, P, P, P]
     F = ctypes.c_float
+    lib.moe_dropout.restype = I
+    lib.moe_dropout.argtypes = [I, P, P, I64, F, P, P, P]
+    lib.moe_combine_dropout.restype = I
+    lib.moe_combine_dropout.argtypes = [I, P, P, P, P, I, I, I, I64, F, P, P, P, P]
+    GP = ctypes.POINTER(MoeGlu)
+    lib.moe_grouped_glu_op.restype = I
+    lib.moe_grouped_glu_op.argtypes = [I, I, GP, ctypes.POINTER(MoeGemmTensors), P, I, I, I64, I, I, P]
+    lib.moe_grouped_glu_fwd.restype = I
+    lib.moe_grouped_glu_fwd.argtypes = [I, GP, P, P, P, P, I, I, I64, I, I, P, P, P, P]
+    lib.moe_grouped_glu_bwd.restype = I
+    lib.moe_grouped_glu_bwd.argtypes = [I, GP, P, P, P, P, P, P, P, I, I, I64, I, I, P, P, P, P, P, SZ, P]
+    lib.moe_quantize_int4.restype = I
+    lib.moe_quantize_int4.argtypes = [P, I64, I, I, P, P, P, P]
+    lib.moe_dequantize_int4.restype = I
+    lib.moe_dequantize_int4.argtypes = [P, P, P, I64, I, I, P, P]
+    lib.moe_int4_workspace_bytes.restype = SZ
+    lib.moe_int4_workspace_bytes.argtypes = [I64, I, I]
+    lib.moe_int4_ffn.restype = I
+    lib.moe_int4_ffn.argtypes = [GP, P, I, I, P, P, P, P, P, I, I, I, I, ctypes.POINTER(MoeInt4),
+                                 ctypes.POINTER(MoeInt4), P, P, SZ, P, P]
     lib.moe_quantize_mxfp4.restype = I
     lib.moe_quantize_mxfp4.argtypes = [P, I64, I, P, P, P]
     lib.moe_dequantize_mxfp4.restype = I
@@ -339,6 +376,134 @@ def moe_gate_grad(dout, y_perm, topk_idx, topk_w, dst_row, dlogits, dw=None, dy_
     rc = load().moe_gate_grad(_p(dout), _p(y_perm), _p(topk_idx), _p(topk_w), _p(dst_row), T, E, k, d,
                               n_rows, _p(dlogits), _p(dw), _p(dy_perm), _p(dev_err), _s(stream))
     _check(rc, "moe_gate_grad")
+
+
+_FLOAT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _float_type(dtype):
+    if dtype not in _FLOAT:
+        raise MoeError(MOE_EUNSUPPORTED, "a call of fp32 or bf16 tensors")
+    return _FLOAT[dtype]
+
+
+def _rng(rng):
+    return _dense("rng", rng, torch.int64, 2)
+
+
+def moe_dropout(dtype, x, p, rng, out, residual=None, stream=None):
+    """out = (residual or 0) + drop(x): fp32 or bf16 tensors of one shape, the mask from rng [2] int64 on the
+    device, (seed, step).  The same call on the upstream gradient, without the residual, is the backward."""
+    t = _float_type(dtype)
+    _call("moe_dropout", stream, (x, residual, rng, out), dtype, _dense("x", x, t, *x.shape),
+          _dense("residual", residual, t, *x.shape), x.numel(), p, _rng(rng), _dense("out", out, t, *x.shape))
+
+
+def moe_combine_dropout(dtype, y_perm, dst_row, weights, k, p, rng, out, residual=None, dev_err=None, stream=None):
+    """out[t] = (residual[t] or 0) + drop(sum_j weights[t*k+j] * y_perm[dst_row[t*k+j]]), the mask as
+    moe_dropout's over out [T, d]."""
+    t = _float_type(dtype)
+    T, d = out.shape
+    n_rows = y_perm.shape[0]
+    if dst_row.numel() != T * k or (weights is not None and weights.numel() != T * k):
+        raise ValueError(f"dst_row and weights: expected {T * k} entries for {T} tokens of {k} slots")
+    _call("moe_combine_dropout", stream, (out, y_perm, dst_row, weights, residual, rng, dev_err), dtype,
+          _dense("y_perm", y_perm, t, n_rows, d), _dense("dst_row", dst_row, torch.int32, *dst_row.shape),
+          None if weights is None else _dense("weights", weights, torch.float32, *weights.shape),
+          _dense("residual", residual, t, T, d), T, k, d, n_rows, p, _rng(rng), _dense("out", out, t, T, d), _p(dev_err))
+
+
+def glu(act=MOE_ACT_SILU, limit=0.0, p=0.0, rng=None):
+    """A gated block's form: gate MOE_ACT_*, limit on g and u (0: none), dropout of h with probability p and
+    rng [2] int64 on the device, (seed, step)."""
+    g = MoeGlu(act, limit, p, _rng(rng))
+    g.rng_tensor = rng
+    return g
+
+
+def moe_grouped_glu_op(op, dtype, gate, tensors, group_off, capacity, E, n_rows, d, f, stream=None):
+    """One grouped GEMM stage of a gated block of the form gate (glu()); tensors is a MoeGemmTensors."""
+    _call("moe_grouped_glu_op", stream, (group_off, gate.rng_tensor), op, dtype, ctypes.byref(gate),
+          ctypes.byref(tensors), _dense("group_off", group_off, torch.int32, E + 1), capacity, E, n_rows, d, f)
+
+
+def moe_grouped_glu_fwd(dtype, gate, x_perm, w13, w2, group_off, capacity, gu, h, y_perm, stream=None):
+    """moe_grouped_gemm_fwd (fp32, bf16) with the gate, limit and dropout of gate (glu())."""
+    t = _float_type(dtype)
+    E = group_off.numel() - 1
+    n_rows, d = x_perm.shape
+    f = w2.shape[-1]
+    _call("moe_grouped_glu_fwd", stream, (x_perm, w13, w2, group_off, gu, h, y_perm, gate.rng_tensor), dtype,
+          ctypes.byref(gate), _dense("x_perm", x_perm, t, n_rows, d), _dense("w13", w13, t, E, 2 * f, d),
+          _dense("w2", w2, t, E, d, f), _dense("group_off", group_off, torch.int32, E + 1), capacity, E, n_rows, d, f,
+          _dense("gu", gu, t, n_rows, 2 * f), _dense("h", h, t, n_rows, f), _dense("y_perm", y_perm, t, n_rows, d))
+
+
+def moe_grouped_glu_bwd(dtype, gate, dy_perm, x_perm, gu, h, w13, w2, group_off, capacity, dgu, dx_perm, dw13, dw2,
+                        ws=None, stream=None):
+    """moe_grouped_gemm_bwd (fp32, bf16) of moe_grouped_glu_fwd: the same gate, with the rng it had."""
+    t = _float_type(dtype)
+    E = group_off.numel() - 1
+    n_rows, d = dy_perm.shape
+    f = w2.shape[-1]
+    _call("moe_grouped_glu_bwd", stream, (dy_perm, x_perm, gu, h, w13, w2, group_off, dgu, dx_perm, dw13, dw2, ws,
+                                          gate.rng_tensor), dtype, ctypes.byref(gate),
+          _dense("dy_perm", dy_perm, t, n_rows, d), _dense("x_perm", x_perm, t, n_rows, d),
+          _dense("gu", gu, t, n_rows, 2 * f), _dense("h", h, t, n_rows, f), _dense("w13", w13, t, E, 2 * f, d),
+          _dense("w2", w2, t, E, d, f), _dense("group_off", group_off, torch.int32, E + 1), capacity, E, n_rows, d, f,
+          _dense("dgu", dgu, t, n_rows, 2 * f), _dense("dx_perm", dx_perm, t, n_rows, d),
+          _dense("dw13", dw13, t, E, 2 * f, d), _dense("dw2", dw2, t, E, d, f), _p(ws), _nbytes(ws))
+
+
+def moe_quantize_int4(src, group, codes, scales, zeros=None, stream=None):
+    """bf16 src [rows, K] -> 4-bit codes [rows, K/2] uint8 (element 2i in the low half of byte i), scales
+    [rows, K/group] bf16 and, if given, zero points [rows, K/group] uint8."""
+    rows, K = src.shape
+    _call("moe_quantize_int4", stream, (src, codes, scales, zeros), _dense("src", src, torch.bfloat16, rows, K), rows, K,
+          group, _dense("codes", codes, torch.uint8, rows, K // 2),
+          _dense("scales", scales, torch.bfloat16, rows, K // group), _dense("zeros", zeros, torch.uint8, rows, K // group))
+
+
+def moe_dequantize_int4(codes, scales, zeros, group, dst, stream=None):
+    """(code - zero) * scale -> dst [rows, K] bf16; zeros None: 8."""
+    rows, K = dst.shape
+    _call("moe_dequantize_int4", stream, (dst, codes, scales, zeros), _dense("codes", codes, torch.uint8, rows, K // 2),
+          _dense("scales", scales, torch.bfloat16, rows, K // group), _dense("zeros", zeros, torch.uint8, rows, K // group),
+          rows, K, group, _dense("dst", dst, torch.bfloat16, rows, K))
+
+
+def moe_int4_workspace_bytes(n_rows, d, f):
+    return int(load().moe_int4_workspace_bytes(n_rows, d, f))
+
+
+def _int4(name, w, E, N, K, group):
+    codes, scales, zeros = w
+    n = K // group
+    return MoeInt4(_dense(name + " codes", codes, torch.uint8, E, N, K // 2),
+                   _dense(name + " scales", scales, torch.bfloat16, E, N, n),
+                   _dense(name + " zeros", zeros, torch.uint8, E, N, n))
+
+
+def moe_int4_ffn(gate, x, topk_idx, topk_w, dst_row, src_slot, group_off, group, w13, w2, out, ws, dev_err=None,
+                 stream=None):
+    """x [T, d] bf16 and the route of its tokens -> out [T, d]: the gated block over experts in 4-bit integers.
+    w13 and w2 are (codes, scales, zeros or None) as moe_quantize_int4 makes them: codes [E, 2f, d/2] and
+    [E, d, f/2]."""
+    T, d = x.shape
+    k = topk_idx.shape[1]
+    E = group_off.numel() - 1
+    f = 2 * w2[0].shape[-1]
+    i32 = torch.int32
+    if group not in (32, 64, 128):
+        raise MoeError(MOE_EUNSUPPORTED, "moe_int4_ffn")
+    a, b = _int4("w13", w13, E, 2 * f, d, group), _int4("w2", w2, E, d, f, group)
+    if dst_row.numel() != T * k or src_slot.numel() != T * k:
+        raise ValueError(f"dst_row and src_slot: expected {T * k} entries for {T} tokens of {k} slots")
+    _call("moe_int4_ffn", stream, (x, topk_idx, topk_w, dst_row, src_slot, group_off, *w13, *w2, out, ws, dev_err),
+          ctypes.byref(gate), _dense("x", x, torch.bfloat16, T, d), T, k, _dense("topk_idx", topk_idx, i32, T, k),
+          _dense("topk_w", topk_w, torch.float32, T, k), _dense("dst_row", dst_row, i32, *dst_row.shape),
+          _dense("src_slot", src_slot, i32, *src_slot.shape), _dense("group_off", group_off, i32, E + 1), E, d, f, group,
+          ctypes.byref(a), ctypes.byref(b), _dense("out", out, torch.bfloat16, T, d), _p(ws), _nbytes(ws), _p(dev_err))
 
 
 def moe_quantize_mxfp4(src, codes, scales, stream=None):

@@ -638,7 +638,7 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW) void gemm_grouped_m_kernel(MParams p)
     const uint16_t* Be = p.B + (int64_t)e * p.sB;
     sb.ld = p.ldb;
     sb.K = p.K;
-    if constexpr (EPI == EPI_SWIGLU_FWD) {
+    if constexpr (is_gate_up(EPI)) {
         const int n0 = nt * 128;
         sb.p0 = Be + (int64_t)n0 * p.ldb;
         sb.p1 = Be + (int64_t)(p.f + n0) * p.ldb;
@@ -1149,7 +1149,7 @@ hipError_t launch_router_logits(const uint16_t* x, const uint16_t* w, int T, int
     return hipGetLastError();
 }
 
-hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f,
+hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const GluSpec& glu, int d, int f,
                         hipStream_t s)
 {
     MParams p{};
@@ -1158,6 +1158,8 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, int d, i
     p.E = g.E;
     p.n_rows = g.n_rows;
     p.f = f;
+    p.glu = glu;
+    const bool plain = plain_swiglu(glu);
     switch (op) {
     case MOE_GEMM_GATE_UP:  // gu = x [Wg|Wu]^T, h = silu(g) * u
         p.A = (const uint16_t*)t.x_perm;
@@ -1172,6 +1174,7 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, int d, i
         p.ldc = 2 * f;
         p.H = (uint16_t*)t.h;
         p.ldh = f;
+        if (!plain) return launch_m<kBM, kBK, kNS, false, EPI_GLU_FWD, kNW>(p, g.n_rows, s);
         return launch_m<kBM, kBK, kNS, false, EPI_SWIGLU_FWD, kNW>(p, g.n_rows, s);
     case MOE_GEMM_DOWN:  // y = h Wd^T
         p.A = (const uint16_t*)t.h;
@@ -1198,6 +1201,7 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, int d, i
         p.ldc = 2 * f;
         p.G = (const uint16_t*)t.gu;
         p.ldg = 2 * f;
+        if (!plain) return launch_m<kBM, kBK, kNS, true, EPI_GLU_BWD, kNW>(p, g.n_rows, s);
         return launch_m<kBM, kBK, kNS, true, EPI_SWIGLU_BWD, kNW>(p, g.n_rows, s);
     case MOE_GEMM_DGRAD_GATE_UP:  // dx = [dg | du] [Wg ; Wu] (W13_e stored [2f, d] = [K, N])
         p.A = (const uint16_t*)t.dgu;

@@ -3,7 +3,7 @@
 // Included by gemm_bf16.hip and gemm_mxfp8.hip only.
 #pragma once
 
-#include "moe_internal.h"
+#include "glu.h"
 
 
 namespace moe {
@@ -16,7 +16,9 @@ constexpr int BN = 256;
 constexpr int NTH = 256;
 constexpr uint32_t kOOB = 0x80000000u;  // a buffer offset past every range: loads return 0
 
-enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2 };
+// GLU: the gate, limit and dropout given at run time (MParams::glu)
+enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_GLU_FWD = 3, EPI_GLU_BWD = 4 };
+constexpr bool is_gate_up(int epi) { return epi == EPI_SWIGLU_FWD || epi == EPI_GLU_FWD; }
 
 // Raw buffer descriptor over [base, base + bytes) as four scalar words
 // (base, base[47:32] with stride 0, num_records, flags).  Loads at or past
@@ -294,6 +296,7 @@ struct MParams {
     uint8_t* Mq;
     uint8_t* Ms;
     int64_t ldq;
+    GluSpec glu;           // GLU epilogues
 };
 
 // Row-wise MXFP8 of 32 bf16 held as 8 by each of four consecutive lanes
@@ -434,7 +437,7 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
             const int n = nt * BN + 8 * c;
             if (r < rows_valid && n < p.N) *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + n) = v;
         });
-    } else if constexpr (EPI == EPI_SWIGLU_FWD) {
+    } else if constexpr (is_gate_up(EPI)) {
         // tile columns 0..127 are gate columns n0.., 128..255 the up columns f + n0..
         const int n0 = nt * 128;
         stage_acc<BM, NW>(acc, lds);
@@ -443,19 +446,44 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
             if (r < rows_valid && n < p.f)
                 *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + (c < 16 ? n : p.f + n)) = v;
         });
-        // h = silu(g) * u from the unrounded fp32 accumulators
+        // h = a(g) * u from the unrounded fp32 accumulators
+        auto make_h = [&](auto&& gate) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ / 2; ++j)
+                for (int j = 0; j < NJ / 2; ++j)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float hv[4];
+                    for (int g = 0; g < 4; ++g) {
+                        float hv[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) hv[q] = silu_f(acc[i][j][4 * g + q]) * acc[i][j + NJ / 2][4 * g + q];
-                    stage_put(lds, stage_off<16>(wm * (BM / 2) + i * 32 + (lane & 31), acc_col<NW>(wn, j, g, lane)),
-                              pack4_bf16(hv[0], hv[1], hv[2], hv[3]));
+                        for (int q = 0; q < 4; ++q) hv[q] = gate(acc[i][j][4 * g + q], acc[i][j + NJ / 2][4 * g + q]);
+                        stage_put(lds, stage_off<16>(wm * (BM / 2) + i * 32 + (lane & 31), acc_col<NW>(wn, j, g, lane)),
+                                  pack4_bf16(hv[0], hv[1], hv[2], hv[3]));
+                    }
+        };
+        if constexpr (EPI == EPI_GLU_FWD) {
+            // the kept elements' factor before the rounding; the mask after it, where a lane has the eight
+            // consecutive elements of one generator block
+            const float L = p.glu.limit, scale = p.glu.drop.scale;
+            const uint32_t thr = p.glu.drop.thr;
+            with_act(p.glu.act, [&](auto A) __attribute__((always_inline)) {
+                make_h([&](float g, float u) __attribute__((always_inline)) {
+                    return act_of<decltype(A)::value, true>(limit_g(g, L)) * limit_u(u, L) * scale;
+                });
+            });
+            PhiloxKey key{};
+            if (thr) key = philox_key(p.glu.drop.rng);
+            stage_flush<BM, 16, NT>(lds, [&](int r, int c, uint4 v) __attribute__((always_inline)) {
+                const int n = n0 + 8 * c;
+                if (r < rows_valid && n < p.f) {
+                    const int64_t at = (row0 + r) * p.f + n;
+                    if (thr) v = mask_vec(v, philox(key, (uint64_t)at >> 3), thr);
+                    *reinterpret_cast<uint4*>(p.H + at) = v;
                 }
+            });
+            return;
+        }
+        make_h([](float g, float u) __attribute__((always_inline)) { return silu_f(g) * u; });
         if constexpr (MXQ) {
             // h also leaves as row-wise MXFP8: the four lanes of each 32-column block encode it together
             stage_flush<BM, 16, NT>(lds, [&](int r, int c, uint4 v) {
@@ -500,28 +528,46 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
             }
             wait_vmcnt<0>();
             __syncthreads();
+            auto make_dgu = [&](auto&& slope) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+                for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int jj = 0; jj < NJ / 2; ++jj)
+                    for (int jj = 0; jj < NJ / 2; ++jj)
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int j = (NJ / 2) * ch + jj;
-                        const uint32_t off = stage_off<16>(wm * (BM / 2) + i * 32 + (lane & 31),
-                                                           acc_col<NW>(wn, j, g, lane) - 128 * ch);
-                        float gv[4], uv[4], dgv[4], duv[4];
-                        unpack4_bf16(*reinterpret_cast<const uint2*>(lg + off), gv);
-                        unpack4_bf16(*reinterpret_cast<const uint2*>(lu + off), uv);
+                        for (int g = 0; g < 4; ++g) {
+                            const int j = (NJ / 2) * ch + jj;
+                            const uint32_t off = stage_off<16>(wm * (BM / 2) + i * 32 + (lane & 31),
+                                                               acc_col<NW>(wn, j, g, lane) - 128 * ch);
+                            float gv[4], uv[4], dgv[4], duv[4];
+                            unpack4_bf16(*reinterpret_cast<const uint2*>(lg + off), gv);
+                            unpack4_bf16(*reinterpret_cast<const uint2*>(lu + off), uv);
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const float dh = acc[i][j][4 * g + t];
-                            const float sg = sigmoid_f(gv[t]);
-                            duv[t] = dh * gv[t] * sg;
-                            dgv[t] = dh * uv[t] * sg * (1.0f + gv[t] * (1.0f - sg));
+                            for (int t = 0; t < 4; ++t) {
+                                const float dh = acc[i][j][4 * g + t];
+                                slope(dh, gv[t], uv[t], dgv[t], duv[t]);
+                            }
+                            stage_put(lg, off, pack4_bf16(dgv[0], dgv[1], dgv[2], dgv[3]));
+                            stage_put(lu, off, pack4_bf16(duv[0], duv[1], duv[2], duv[3]));
                         }
-                        stage_put(lg, off, pack4_bf16(dgv[0], dgv[1], dgv[2], dgv[3]));
-                        stage_put(lu, off, pack4_bf16(duv[0], duv[1], duv[2], duv[3]));
-                    }
+            };
+            if constexpr (EPI == EPI_GLU_BWD) {
+                const float L = p.glu.limit, scale = p.glu.drop.scale;
+                with_act(p.glu.act, [&](auto A) __attribute__((always_inline)) {
+                    make_dgu([&](float dh, float gv, float uv, float& dg, float& du) __attribute__((always_inline)) {
+                        float a, da;
+                        act_and_slope<decltype(A)::value, true>(limit_g(gv, L), a, da);
+                        dh *= scale;
+                        dg = gv > L ? 0.0f : dh * limit_u(uv, L) * da;
+                        du = uv > L || uv < -L ? 0.0f : dh * a;
+                    });
+                });
+            } else {
+                make_dgu([](float dh, float gv, float uv, float& dg, float& du) __attribute__((always_inline)) {
+                    const float sg = sigmoid_f(gv);
+                    du = dh * gv * sg;
+                    dg = dh * uv * sg * (1.0f + gv * (1.0f - sg));
+                });
+            }
             __syncthreads();
             // both tiles out as rows of dgu, all LDS reads of a thread first
             constexpr int NQ = BM * 16 * 2 / NT;
@@ -534,7 +580,27 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
                 const int r = qq >> 4, c = qq & 15;
                 v[i] = *reinterpret_cast<const uint4*>((which ? lu : lg) + r * 256 + ((c ^ (r & 15)) << 4));
             }
-            if constexpr (MXQ) {
+            if constexpr (EPI == EPI_GLU_BWD) {
+                // a thread's chunks are the same of dg and du: dropped elements of h have neither
+                static_assert(BM * 16 % NT == 0, "chunk i + NQ / 2 is the u half of chunk i");
+                const uint32_t thr = p.glu.drop.thr;
+                PhiloxKey key{};
+                if (thr) key = philox_key(p.glu.drop.rng);
+#pragma unroll
+                for (int i = 0; i < NQ / 2; ++i) {
+                    const int q = (int)threadIdx.x + i * NT;
+                    const int r = q >> 4, n = nc + 8 * (q & 15);
+                    if (r < rows_valid && n < p.N) {
+                        if (thr) {
+                            const uint4 w = philox(key, (uint64_t)((row0 + r) * p.f + n) >> 3);
+                            v[i] = mask_vec(v[i], w, thr);
+                            v[i + NQ / 2] = mask_vec(v[i + NQ / 2], w, thr);
+                        }
+                        *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + n) = v[i];
+                        *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + p.f + n) = v[i + NQ / 2];
+                    }
+                }
+            } else if constexpr (MXQ) {
                 // dgu also leaves as row-wise MXFP8 (32-column blocks never straddle dg | du)
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {

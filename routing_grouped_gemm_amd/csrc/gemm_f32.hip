@@ -4,14 +4,16 @@
 // 4 x 4 register micro-tile each, operands staged in LDS as [k][row].
 // For the SwiGLU forward a tile's 64 logical columns are 32 gate columns and
 // the same 32 up columns, so the epilogue (through LDS) forms h = silu(g) * u.
-#include "moe_internal.h"
+#include "glu.h"
 
 namespace moe {
 namespace {
 
 constexpr int TM = 64, TN = 64, TK = 16;
 
-enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2 };
+// GLU: the gate, limit and dropout given at run time (F32M::glu)
+enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_GLU_FWD = 3, EPI_GLU_BWD = 4 };
+constexpr bool is_gate_up(int epi) { return epi == EPI_SWIGLU_FWD || epi == EPI_GLU_FWD; }
 
 struct F32M {
     const float* A;        // [n_rows, K] grouped rows
@@ -30,9 +32,21 @@ struct F32M {
     const float* G;
     int64_t ldg;
     int f;
+    GluSpec glu;
 };
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+// the factor of element i of h: 0 where it is dropped.  (A generator call for
+// each element, of which it uses an eighth: this path is the small fp32 one.)
+__device__ __forceinline__ float drop_factor(const DropSpec& dr, PhiloxKey key, int64_t i)
+{
+    if (!dr.thr) return 1.0f;
+    const uint4 w = philox(key, (uint64_t)i >> 3);
+    const int j = (int)(i & 7);
+    const uint32_t r = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+    return ((j & 1) ? keep_hi(r, dr.thr) : keep_lo(r, dr.thr)) ? dr.scale : 0.0f;
+}
 
 template <int EPI>
 __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
@@ -57,7 +71,7 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
     const int64_t row0 = g0 + (int64_t)mt * TM;
     const int rows_valid = min(TM, m_e - mt * TM);
     const float* Be = p.B + (int64_t)e * p.sB;
-    const int n0 = EPI == EPI_SWIGLU_FWD ? nt * (TN / 2) : nt * TN;
+    const int n0 = is_gate_up(EPI) ? nt * (TN / 2) : nt * TN;
 
     const int tid = threadIdx.x;
     const int tx = tid % 16, ty = tid / 16;
@@ -73,7 +87,7 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
             const int k = k0 + kk;
             int64_t brow;
             bool ok;
-            if (EPI == EPI_SWIGLU_FWD) {
+            if (is_gate_up(EPI)) {
                 const int n = n0 + (c % (TN / 2));
                 ok = n < p.f;
                 brow = c < TN / 2 ? n : p.f + n;
@@ -105,7 +119,9 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) sC[ty * 4 + i][tx * 4 + j] = acc[i][j];
     __syncthreads();
-    if (EPI == EPI_SWIGLU_FWD) {
+    PhiloxKey key{};
+    if ((EPI == EPI_GLU_FWD || EPI == EPI_GLU_BWD) && p.glu.drop.thr) key = philox_key(p.glu.drop.rng);
+    if (is_gate_up(EPI)) {
         for (int idx = tid; idx < TM * (TN / 2); idx += 256) {
             const int r = idx / (TN / 2), c = idx % (TN / 2);
             const int n = n0 + c;
@@ -114,7 +130,15 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
             const int64_t row = row0 + r;
             p.C[row * p.ldc + n] = g;
             p.C[row * p.ldc + p.f + n] = u;
-            p.H[row * p.ldh + n] = silu(g) * u;
+            if constexpr (EPI == EPI_GLU_FWD) {
+                const float c = drop_factor(p.glu.drop, key, row * p.f + n), L = p.glu.limit;
+                with_act(p.glu.act, [&](auto A) {
+                    const float h = act_of<decltype(A)::value, false>(limit_g(g, L)) * limit_u(u, L);
+                    p.H[row * p.ldh + n] = c == 0.0f ? 0.0f : h * c;
+                });
+            } else {
+                p.H[row * p.ldh + n] = silu(g) * u;
+            }
         }
     } else {
         for (int idx = tid; idx < TM * TN; idx += 256) {
@@ -123,8 +147,18 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
             if (r >= rows_valid || n >= p.N) continue;
             const int64_t row = row0 + r;
             const float v = sC[r][c];
-            if (EPI == EPI_STORE) {
+            if constexpr (EPI == EPI_STORE) {
                 p.C[row * p.ldc + n] = v;
+            } else if constexpr (EPI == EPI_GLU_BWD) {
+                const float g = p.G[row * p.ldg + n], u = p.G[row * p.ldg + p.f + n];
+                const float c = drop_factor(p.glu.drop, key, row * p.f + n), L = p.glu.limit;
+                with_act(p.glu.act, [&](auto A) {
+                    float a, da;
+                    act_and_slope<decltype(A)::value, false>(limit_g(g, L), a, da);
+                    const float dh = v * c;
+                    p.C[row * p.ldc + n] = c == 0.0f || g > L ? 0.0f : dh * limit_u(u, L) * da;
+                    p.C[row * p.ldc + p.f + n] = c == 0.0f || u > L || u < -L ? 0.0f : dh * a;
+                });
             } else {
                 const float g = p.G[row * p.ldg + n], u = p.G[row * p.ldg + p.f + n];
                 const float s = 1.0f / (1.0f + expf(-g));
@@ -224,7 +258,7 @@ hipError_t launch_k(const F32K& p, hipStream_t s)
 
 }  // namespace
 
-hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f,
+hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const GluSpec& glu, int d, int f,
                        hipStream_t s)
 {
     F32M p{};
@@ -233,6 +267,8 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, in
     p.E = g.E;
     p.n_rows = g.n_rows;
     p.f = f;
+    p.glu = glu;
+    const bool plain = plain_swiglu(glu);
     switch (op) {
     case MOE_GEMM_GATE_UP:
         p.A = (const float*)t.x_perm;
@@ -248,6 +284,7 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, in
         p.ldc = 2 * f;
         p.H = (float*)t.h;
         p.ldh = f;
+        if (!plain) return launch_m<EPI_GLU_FWD>(p, g.n_rows, s);
         return launch_m<EPI_SWIGLU_FWD>(p, g.n_rows, s);
     case MOE_GEMM_DOWN:
         p.A = (const float*)t.h;
@@ -276,6 +313,7 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, in
         p.ldc = 2 * f;
         p.G = (const float*)t.gu;
         p.ldg = 2 * f;
+        if (!plain) return launch_m<EPI_GLU_BWD>(p, g.n_rows, s);
         return launch_m<EPI_SWIGLU_BWD>(p, g.n_rows, s);
     case MOE_GEMM_DGRAD_GATE_UP:
         p.A = (const float*)t.dgu;

@@ -1,6 +1,7 @@
 // C ABI entry points of libmoe: host-side argument validation, workspace
 // carving and kernel launches.  No entry point allocates, frees, copies to
 // the host or synchronises; everything is enqueued on the caller's stream.
+#include <cmath>
 #include <mutex>
 
 #include "moe_internal.h"
@@ -43,15 +44,36 @@ int check_gemm_shape(int dtype, const int32_t* group_off, int capacity, int E, i
 }
 
 // one grouped GEMM stage in the given arithmetic
-int run_gemm_op(int op, int dtype, const moe_gemm_tensors& t, const GroupSpec& g, int d, int f,
+int run_gemm_op(int op, int dtype, const moe_gemm_tensors& t, const GroupSpec& g, const GluSpec& glu, int d, int f,
                 hipStream_t s)
 {
     hipError_t e;
-    if (dtype == MOE_F32) e = gemm_op_f32(op, t, g, d, f, s);
-    else if (dtype == MOE_BF16) e = gemm_op_bf16(op, t, g, d, f, s);
+    if (dtype == MOE_F32) e = gemm_op_f32(op, t, g, glu, d, f, s);
+    else if (dtype == MOE_BF16) e = gemm_op_bf16(op, t, g, glu, d, f, s);
     else if (dtype == MOE_MXFP4) e = gemm_op_mxfp4(op, t, g, d, f, s);
     else e = gemm_op_mxfp8(op, t, g, d, f, t.ws, s);
     return status_of(e);
+}
+
+// p and rng of a dropout as the kernels take them; false: p out of range or no rng
+bool drop_spec(float p, const uint64_t* rng, DropSpec& out)
+{
+    if (!(p >= 0.0f && p < 1.0f)) return false;
+    const float t = rintf(p * 65536.0f);
+    out.thr = t > 65535.0f ? 65535u : (uint32_t)t;
+    out.scale = 65536.0f / (float)(65536u - out.thr);
+    out.rng = rng;
+    return !out.thr || (rng && (reinterpret_cast<uintptr_t>(rng) & 7u) == 0);
+}
+
+// the form of a gated block; false: not given or out of range
+bool glu_spec(const moe_glu* g, GluSpec& out)
+{
+    if (!g || g->act < MOE_ACT_SILU || g->act > MOE_ACT_RELU) return false;
+    if (!(g->limit >= 0.0f && g->limit < __builtin_inff())) return false;
+    out.act = g->act;
+    out.limit = g->limit > 0.0f ? g->limit : __builtin_inff();
+    return drop_spec(g->p, g->rng, out.drop);
 }
 
 // Scratch of moe_route_topk_noalloc: the route's per-pair ranks and per-block
@@ -84,6 +106,167 @@ hipError_t scratch_of_current_device(void** out)
     *out = g_scratch_ptr[dev];
     return *out ? hipSuccess : hipErrorInvalidSymbol;
 }
+
+// the grouped GEMM entry points for a gated block of any form (the plain ones pass kSwiglu)
+int grouped_fwd(const GluSpec& glu, int dtype, const void* x_perm, const uint8_t* x_perm_scales,
+                const void* w13, const uint8_t* w13_scales, const void* w2,
+                         const uint8_t* w2_scales, const int32_t* group_off, int capacity, int E,
+                         int64_t n_rows, int d, int f, void* gu, void* h, void* y_perm, void* ws,
+                         size_t ws_bytes, moe_stream_t stream)
+{
+    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
+    if (st != MOE_OK) return st;
+    if (!w13 || !w2) return MOE_EINVAL;
+    const bool need_saved = dtype != MOE_MXFP4;   // MXFP4: gu and h are optional
+    if (n_rows > 0 && (!x_perm || (need_saved && (!gu || !h)) || !y_perm)) return MOE_EINVAL;
+    for (const void* p : {x_perm, w13, w2, (const void*)gu, (const void*)h, (const void*)y_perm})
+        if (!aligned16(p)) return MOE_EALIGN;
+    if (dtype == MOE_MXFP8 || dtype == MOE_MXFP4) {
+        const bool no_rows = dtype == MOE_MXFP4 && n_rows == 0;
+        if ((!x_perm_scales && !no_rows) || !w13_scales || !w2_scales) return MOE_EINVAL;
+        if (dtype == MOE_MXFP4 && (!aligned16(x_perm_scales) || !aligned16(w13_scales) || !aligned16(w2_scales)))
+            return MOE_EALIGN;
+        if (!ws || ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(ws))
+            return MOE_EWORKSPACE;
+    }
+    moe_gemm_tensors t{};
+    t.x_perm = x_perm;
+    t.x_perm_scales = x_perm_scales;
+    t.w13 = w13;
+    t.w13_scales = w13_scales;
+    t.w2 = w2;
+    t.w2_scales = w2_scales;
+    t.gu = gu;
+    t.h = h;
+    t.y_perm = y_perm;
+    t.ws = ws;
+    t.ws_bytes = ws_bytes;
+    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
+    for (int op : {MOE_GEMM_GATE_UP, MOE_GEMM_DOWN}) {
+        const int st2 = run_gemm_op(op, dtype, t, g, glu, d, f, as_stream(stream));
+        if (st2 != MOE_OK) return st2;
+    }
+    return MOE_OK;
+}
+
+int grouped_bwd(const GluSpec& glu, int dtype, const void* dy_perm, const void* x_perm,
+                         const uint8_t* x_perm_scales, const void* gu, const void* h,
+                const void* w13, const uint8_t* w13_scales, const void* w2,
+                         const uint8_t* w2_scales, const int32_t* group_off, int capacity, int E,
+                         int64_t n_rows, int d, int f, void* dgu, void* dx_perm, void* dw13,
+                         void* dw2, void* ws, size_t ws_bytes, moe_stream_t stream)
+{
+    if (dtype == MOE_MXFP4) return MOE_EUNSUPPORTED;
+    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
+    if (st != MOE_OK) return st;
+    if (!w13 || !w2 || !dw13 || !dw2) return MOE_EINVAL;
+    if (n_rows > 0 && (!dy_perm || !x_perm || !gu || !h || !dgu || !dx_perm)) return MOE_EINVAL;
+    for (const void* p : {dy_perm, x_perm, gu, h, w13, w2, (const void*)dgu, (const void*)dx_perm,
+                          (const void*)dw13, (const void*)dw2})
+        if (!aligned16(p)) return MOE_EALIGN;
+    if (dtype == MOE_MXFP8 && (!x_perm_scales || !w13_scales || !w2_scales)) return MOE_EINVAL;
+    if (dtype != MOE_F32 &&
+        (!ws || ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(ws)))
+        return MOE_EWORKSPACE;
+    moe_gemm_tensors t{};
+    t.x_perm = x_perm;
+    t.x_perm_scales = x_perm_scales;
+    t.w13 = w13;
+    t.w13_scales = w13_scales;
+    t.w2 = w2;
+    t.w2_scales = w2_scales;
+    t.gu = const_cast<void*>(gu);
+    t.h = const_cast<void*>(h);
+    t.dy_perm = dy_perm;
+    t.dgu = dgu;
+    t.dx_perm = dx_perm;
+    t.dw13 = dw13;
+    t.dw2 = dw2;
+    t.ws = ws;
+    t.ws_bytes = ws_bytes;
+    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
+    for (int op : {MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD}) {
+        const int st2 = run_gemm_op(op, dtype, t, g, glu, d, f, as_stream(stream));
+        if (st2 != MOE_OK) return st2;
+    }
+    return MOE_OK;
+}
+
+int grouped_op(const GluSpec& glu, int op, int dtype, const moe_gemm_tensors* t,
+                        const int32_t* group_off, int capacity, int E, int64_t n_rows, int d,
+                        int f, moe_stream_t stream)
+{
+    if (!t) return MOE_EINVAL;
+    if (op < MOE_GEMM_GATE_UP || op > MOE_GEMM_WGRAD) return MOE_EINVAL;
+    if (dtype == MOE_MXFP4 && op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return MOE_EUNSUPPORTED;
+    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
+    if (st != MOE_OK) return st;
+    if (dtype == MOE_MXFP8) {
+        const bool w13_op = op == MOE_GEMM_GATE_UP || op == MOE_GEMM_DGRAD_GATE_UP;
+        const bool w2_op = op == MOE_GEMM_DOWN || op == MOE_GEMM_DGRAD_DOWN;
+        if ((w13_op && !t->w13_scales) || (w2_op && !t->w2_scales)) return MOE_EINVAL;
+        if ((op == MOE_GEMM_GATE_UP || op == MOE_GEMM_WGRAD) && n_rows > 0 && !t->x_perm_scales)
+            return MOE_EINVAL;
+        if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
+            return MOE_EWORKSPACE;
+    }
+    if (dtype == MOE_MXFP4) {
+        const uint8_t* ws = op == MOE_GEMM_GATE_UP ? t->w13_scales : t->w2_scales;
+        if (!ws || (op == MOE_GEMM_GATE_UP && n_rows > 0 && !t->x_perm_scales)) return MOE_EINVAL;
+        if (!aligned16(ws) || !aligned16(t->x_perm_scales)) return MOE_EALIGN;
+        if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
+            return MOE_EWORKSPACE;
+    }
+    // operands each stage reads (r) and writes (w)
+    const void* need[4] = {nullptr, nullptr, nullptr, nullptr};
+    int n = 0;
+    switch (op) {
+    case MOE_GEMM_GATE_UP: need[0] = t->x_perm; need[1] = t->w13; need[2] = t->gu; need[3] = t->h; n = 4; break;
+    case MOE_GEMM_DOWN: need[0] = t->h; need[1] = t->w2; need[2] = t->y_perm; n = 3; break;
+    case MOE_GEMM_DGRAD_DOWN: need[0] = t->dy_perm; need[1] = t->w2; need[2] = t->gu; need[3] = t->dgu; n = 4; break;
+    case MOE_GEMM_DGRAD_GATE_UP: need[0] = t->dgu; need[1] = t->w13; need[2] = t->dx_perm; n = 3; break;
+    default: break;
+    }
+    if (dtype == MOE_MXFP4) {
+        // gu and h are optional outputs, and DOWN reads the workspace's h
+        const void* opt[2] = {t->gu, t->h};
+        for (const void* p : opt)
+            if (op == MOE_GEMM_GATE_UP && !aligned16(p)) return MOE_EALIGN;
+        n = 2;
+        if (op == MOE_GEMM_DOWN) {
+            need[0] = t->y_perm;
+            need[1] = t->w2;
+        }
+    }
+    const bool acc_f32 = t->dw13_f32 || t->dw2_f32;
+    if (acc_f32) {
+        // fp32 accumulate-into weight gradients: bf16 WGRAD only, both targets
+        if (op != MOE_GEMM_WGRAD || dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+        if (!t->dw13_f32 || !t->dw2_f32) return MOE_EINVAL;
+        if (!aligned16(t->dw13_f32) || !aligned16(t->dw2_f32)) return MOE_EALIGN;
+    }
+    if (op == MOE_GEMM_WGRAD) {
+        const void* wn[6] = {t->dy_perm, t->h, acc_f32 ? (const void*)t->dw2_f32 : t->dw2, t->dgu, t->x_perm,
+                             acc_f32 ? (const void*)t->dw13_f32 : t->dw13};
+        for (const void* p : wn) {
+            if (!p) return MOE_EINVAL;
+            if (!aligned16(p)) return MOE_EALIGN;
+        }
+    } else {
+        for (int i = 0; i < n; ++i) {
+            const bool weight = need[i] == t->w13 || need[i] == t->w2;
+            if (!need[i] && (weight || n_rows > 0)) return MOE_EINVAL;
+            if (!aligned16(need[i])) return MOE_EALIGN;
+        }
+    }
+    // the bf16 weight gradient keeps its tile-mapping flag in the workspace
+    if (dtype == MOE_BF16 && op == MOE_GEMM_WGRAD &&
+        (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws)))
+        return MOE_EWORKSPACE;
+    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
+    return run_gemm_op(op, dtype, *t, g, glu, d, f, as_stream(stream));
+}
+
 
 }  // namespace
 
@@ -222,39 +405,8 @@ int moe_grouped_gemm_fwd(int dtype, const void* x_perm, const uint8_t* x_perm_sc
                          int64_t n_rows, int d, int f, void* gu, void* h, void* y_perm, void* ws,
                          size_t ws_bytes, moe_stream_t stream)
 {
-    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
-    if (st != MOE_OK) return st;
-    if (!w13 || !w2) return MOE_EINVAL;
-    const bool need_saved = dtype != MOE_MXFP4;   // MXFP4: gu and h are optional
-    if (n_rows > 0 && (!x_perm || (need_saved && (!gu || !h)) || !y_perm)) return MOE_EINVAL;
-    for (const void* p : {x_perm, w13, w2, (const void*)gu, (const void*)h, (const void*)y_perm})
-        if (!aligned16(p)) return MOE_EALIGN;
-    if (dtype == MOE_MXFP8 || dtype == MOE_MXFP4) {
-        const bool no_rows = dtype == MOE_MXFP4 && n_rows == 0;
-        if ((!x_perm_scales && !no_rows) || !w13_scales || !w2_scales) return MOE_EINVAL;
-        if (dtype == MOE_MXFP4 && (!aligned16(x_perm_scales) || !aligned16(w13_scales) || !aligned16(w2_scales)))
-            return MOE_EALIGN;
-        if (!ws || ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(ws))
-            return MOE_EWORKSPACE;
-    }
-    moe_gemm_tensors t{};
-    t.x_perm = x_perm;
-    t.x_perm_scales = x_perm_scales;
-    t.w13 = w13;
-    t.w13_scales = w13_scales;
-    t.w2 = w2;
-    t.w2_scales = w2_scales;
-    t.gu = gu;
-    t.h = h;
-    t.y_perm = y_perm;
-    t.ws = ws;
-    t.ws_bytes = ws_bytes;
-    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
-    for (int op : {MOE_GEMM_GATE_UP, MOE_GEMM_DOWN}) {
-        const int st2 = run_gemm_op(op, dtype, t, g, d, f, as_stream(stream));
-        if (st2 != MOE_OK) return st2;
-    }
-    return MOE_OK;
+    return grouped_fwd(kSwiglu, dtype, x_perm, x_perm_scales, w13, w13_scales, w2, w2_scales, group_off, capacity, E,
+                       n_rows, d, f, gu, h, y_perm, ws, ws_bytes, stream);
 }
 
 int moe_grouped_gemm_bwd(int dtype, const void* dy_perm, const void* x_perm,
@@ -264,115 +416,150 @@ int moe_grouped_gemm_bwd(int dtype, const void* dy_perm, const void* x_perm,
                          int64_t n_rows, int d, int f, void* dgu, void* dx_perm, void* dw13,
                          void* dw2, void* ws, size_t ws_bytes, moe_stream_t stream)
 {
-    if (dtype == MOE_MXFP4) return MOE_EUNSUPPORTED;
-    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
-    if (st != MOE_OK) return st;
-    if (!w13 || !w2 || !dw13 || !dw2) return MOE_EINVAL;
-    if (n_rows > 0 && (!dy_perm || !x_perm || !gu || !h || !dgu || !dx_perm)) return MOE_EINVAL;
-    for (const void* p : {dy_perm, x_perm, gu, h, w13, w2, (const void*)dgu, (const void*)dx_perm,
-                          (const void*)dw13, (const void*)dw2})
-        if (!aligned16(p)) return MOE_EALIGN;
-    if (dtype == MOE_MXFP8 && (!x_perm_scales || !w13_scales || !w2_scales)) return MOE_EINVAL;
-    if (dtype != MOE_F32 &&
-        (!ws || ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(ws)))
-        return MOE_EWORKSPACE;
-    moe_gemm_tensors t{};
-    t.x_perm = x_perm;
-    t.x_perm_scales = x_perm_scales;
-    t.w13 = w13;
-    t.w13_scales = w13_scales;
-    t.w2 = w2;
-    t.w2_scales = w2_scales;
-    t.gu = const_cast<void*>(gu);
-    t.h = const_cast<void*>(h);
-    t.dy_perm = dy_perm;
-    t.dgu = dgu;
-    t.dx_perm = dx_perm;
-    t.dw13 = dw13;
-    t.dw2 = dw2;
-    t.ws = ws;
-    t.ws_bytes = ws_bytes;
-    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
-    for (int op : {MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD}) {
-        const int st2 = run_gemm_op(op, dtype, t, g, d, f, as_stream(stream));
-        if (st2 != MOE_OK) return st2;
-    }
-    return MOE_OK;
+    return grouped_bwd(kSwiglu, dtype, dy_perm, x_perm, x_perm_scales, gu, h, w13, w13_scales, w2, w2_scales,
+                       group_off, capacity, E, n_rows, d, f, dgu, dx_perm, dw13, dw2, ws, ws_bytes, stream);
 }
 
 int moe_grouped_gemm_op(int op, int dtype, const moe_gemm_tensors* t,
                         const int32_t* group_off, int capacity, int E, int64_t n_rows, int d,
                         int f, moe_stream_t stream)
 {
-    if (!t) return MOE_EINVAL;
-    if (op < MOE_GEMM_GATE_UP || op > MOE_GEMM_WGRAD) return MOE_EINVAL;
-    if (dtype == MOE_MXFP4 && op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return MOE_EUNSUPPORTED;
-    int st = check_gemm_shape(dtype, group_off, capacity, E, n_rows, d, f);
+    return grouped_op(kSwiglu, op, dtype, t, group_off, capacity, E, n_rows, d, f, stream);
+}
+
+int moe_grouped_glu_op(int op, int dtype, const moe_glu* glu, const moe_gemm_tensors* t, const int32_t* group_off,
+                       int capacity, int E, int64_t n_rows, int d, int f, moe_stream_t stream)
+{
+    GluSpec g;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+    if (!glu_spec(glu, g)) return MOE_EINVAL;
+    return grouped_op(g, op, dtype, t, group_off, capacity, E, n_rows, d, f, stream);
+}
+
+int moe_grouped_glu_fwd(int dtype, const moe_glu* glu, const void* x_perm, const void* w13, const void* w2,
+                        const int32_t* group_off, int capacity, int E, int64_t n_rows, int d, int f, void* gu, void* h,
+                        void* y_perm, moe_stream_t stream)
+{
+    GluSpec g;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+    if (!glu_spec(glu, g)) return MOE_EINVAL;
+    return grouped_fwd(g, dtype, x_perm, nullptr, w13, nullptr, w2, nullptr, group_off, capacity, E, n_rows, d, f, gu,
+                       h, y_perm, nullptr, 0, stream);
+}
+
+int moe_grouped_glu_bwd(int dtype, const moe_glu* glu, const void* dy_perm, const void* x_perm, const void* gu,
+                        const void* h, const void* w13, const void* w2, const int32_t* group_off, int capacity, int E,
+                        int64_t n_rows, int d, int f, void* dgu, void* dx_perm, void* dw13, void* dw2, void* ws,
+                        size_t ws_bytes, moe_stream_t stream)
+{
+    GluSpec g;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+    if (!glu_spec(glu, g)) return MOE_EINVAL;
+    return grouped_bwd(g, dtype, dy_perm, x_perm, nullptr, gu, h, w13, nullptr, w2, nullptr, group_off, capacity, E,
+                       n_rows, d, f, dgu, dx_perm, dw13, dw2, ws, ws_bytes, stream);
+}
+
+int moe_dropout(int dtype, const void* x, const void* residual, int64_t n, float p, const uint64_t* rng, void* out,
+                moe_stream_t stream)
+{
+    DropSpec dr;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+    if (n < 0 || n >= ((int64_t)1 << 40) || !drop_spec(p, rng, dr)) return MOE_EINVAL;
+    if (n > 0 && (!x || !out)) return MOE_EINVAL;
+    if (n % (dtype == MOE_F32 ? 4 : 8)) return MOE_EALIGN;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(out)) return MOE_EALIGN;
+    return status_of(launch_dropout(dtype, x, residual, n, dr, out, as_stream(stream)));
+}
+
+int moe_combine_dropout(int dtype, const void* y_perm, const int32_t* dst_row, const float* weights,
+                        const void* residual, int T, int k, int d, int64_t n_rows, float p, const uint64_t* rng,
+                        void* out, int32_t* dev_err, moe_stream_t stream)
+{
+    DropSpec dr;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EUNSUPPORTED;
+    if (T < 0 || d < 1 || k < 1 || k > kMaxTopK || n_rows < 0 || n_rows >= kMaxRows || (int64_t)T * k >= kMaxRows ||
+        !drop_spec(p, rng, dr))
+        return MOE_EINVAL;
+    if (T > 0 && (!dst_row || !out || (n_rows > 0 && !y_perm))) return MOE_EINVAL;
+    if (d % (dtype == MOE_F32 ? 4 : 8)) return MOE_EALIGN;
+    if (!aligned16(y_perm) || !aligned16(residual) || !aligned16(out)) return MOE_EALIGN;
+    return status_of(launch_combine_dropout(dtype, y_perm, dst_row, weights, residual, T, k, d, n_rows, dr, out,
+                                            dev_err, as_stream(stream)));
+}
+
+// shape of a 4-bit integer tensor
+static int check_int4(int64_t rows, int K, int group)
+{
+    if (rows < 0 || rows >= kMaxRows || K < 1 || rows * (int64_t)K >= ((int64_t)1 << 40)) return MOE_EINVAL;
+    if (group != 32 && group != 64 && group != 128) return MOE_EUNSUPPORTED;
+    return K % group ? MOE_EALIGN : MOE_OK;
+}
+
+int moe_quantize_int4(const void* src, int64_t rows, int K, int group, uint8_t* codes, void* scales, uint8_t* zeros,
+                      moe_stream_t stream)
+{
+    const int st = check_int4(rows, K, group);
     if (st != MOE_OK) return st;
-    if (dtype == MOE_MXFP8) {
-        const bool w13_op = op == MOE_GEMM_GATE_UP || op == MOE_GEMM_DGRAD_GATE_UP;
-        const bool w2_op = op == MOE_GEMM_DOWN || op == MOE_GEMM_DGRAD_DOWN;
-        if ((w13_op && !t->w13_scales) || (w2_op && !t->w2_scales)) return MOE_EINVAL;
-        if ((op == MOE_GEMM_GATE_UP || op == MOE_GEMM_WGRAD) && n_rows > 0 && !t->x_perm_scales)
-            return MOE_EINVAL;
-        if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
-            return MOE_EWORKSPACE;
-    }
-    if (dtype == MOE_MXFP4) {
-        const uint8_t* ws = op == MOE_GEMM_GATE_UP ? t->w13_scales : t->w2_scales;
-        if (!ws || (op == MOE_GEMM_GATE_UP && n_rows > 0 && !t->x_perm_scales)) return MOE_EINVAL;
-        if (!aligned16(ws) || !aligned16(t->x_perm_scales)) return MOE_EALIGN;
-        if (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws))
-            return MOE_EWORKSPACE;
-    }
-    // operands each stage reads (r) and writes (w)
-    const void* need[4] = {nullptr, nullptr, nullptr, nullptr};
-    int n = 0;
-    switch (op) {
-    case MOE_GEMM_GATE_UP: need[0] = t->x_perm; need[1] = t->w13; need[2] = t->gu; need[3] = t->h; n = 4; break;
-    case MOE_GEMM_DOWN: need[0] = t->h; need[1] = t->w2; need[2] = t->y_perm; n = 3; break;
-    case MOE_GEMM_DGRAD_DOWN: need[0] = t->dy_perm; need[1] = t->w2; need[2] = t->gu; need[3] = t->dgu; n = 4; break;
-    case MOE_GEMM_DGRAD_GATE_UP: need[0] = t->dgu; need[1] = t->w13; need[2] = t->dx_perm; n = 3; break;
-    default: break;
-    }
-    if (dtype == MOE_MXFP4) {
-        // gu and h are optional outputs, and DOWN reads the workspace's h
-        const void* opt[2] = {t->gu, t->h};
-        for (const void* p : opt)
-            if (op == MOE_GEMM_GATE_UP && !aligned16(p)) return MOE_EALIGN;
-        n = 2;
-        if (op == MOE_GEMM_DOWN) {
-            need[0] = t->y_perm;
-            need[1] = t->w2;
-        }
-    }
-    const bool acc_f32 = t->dw13_f32 || t->dw2_f32;
-    if (acc_f32) {
-        // fp32 accumulate-into weight gradients: bf16 WGRAD only, both targets
-        if (op != MOE_GEMM_WGRAD || dtype != MOE_BF16) return MOE_EUNSUPPORTED;
-        if (!t->dw13_f32 || !t->dw2_f32) return MOE_EINVAL;
-        if (!aligned16(t->dw13_f32) || !aligned16(t->dw2_f32)) return MOE_EALIGN;
-    }
-    if (op == MOE_GEMM_WGRAD) {
-        const void* wn[6] = {t->dy_perm, t->h, acc_f32 ? (const void*)t->dw2_f32 : t->dw2, t->dgu, t->x_perm,
-                             acc_f32 ? (const void*)t->dw13_f32 : t->dw13};
-        for (const void* p : wn) {
-            if (!p) return MOE_EINVAL;
-            if (!aligned16(p)) return MOE_EALIGN;
-        }
-    } else {
-        for (int i = 0; i < n; ++i) {
-            const bool weight = need[i] == t->w13 || need[i] == t->w2;
-            if (!need[i] && (weight || n_rows > 0)) return MOE_EINVAL;
-            if (!aligned16(need[i])) return MOE_EALIGN;
-        }
-    }
-    // the bf16 weight gradient keeps its tile-mapping flag in the workspace
-    if (dtype == MOE_BF16 && op == MOE_GEMM_WGRAD &&
-        (!t->ws || t->ws_bytes < moe_gemm_workspace_bytes(dtype, E, n_rows, d, f) || !aligned16(t->ws)))
-        return MOE_EWORKSPACE;
-    const GroupSpec g{capacity > 0 ? nullptr : group_off, capacity, E, n_rows};
-    return run_gemm_op(op, dtype, *t, g, d, f, as_stream(stream));
+    if (rows > 0 && (!src || !codes || !scales)) return MOE_EINVAL;
+    if (!aligned16(src) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1u)) return MOE_EALIGN;
+    return status_of(launch_quantize_int4((const uint16_t*)src, rows, K, group, codes, (uint16_t*)scales, zeros,
+                                          as_stream(stream)));
+}
+
+int moe_dequantize_int4(const uint8_t* codes, const void* scales, const uint8_t* zeros, int64_t rows, int K, int group,
+                        void* dst, moe_stream_t stream)
+{
+    const int st = check_int4(rows, K, group);
+    if (st != MOE_OK) return st;
+    if (rows > 0 && (!dst || !codes || !scales)) return MOE_EINVAL;
+    if (!aligned16(dst) || !aligned16(codes) || (reinterpret_cast<uintptr_t>(scales) & 1u)) return MOE_EALIGN;
+    return status_of(launch_dequantize_int4(codes, (const uint16_t*)scales, zeros, rows, K, group, (uint16_t*)dst,
+                                            as_stream(stream)));
+}
+
+size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f)
+{
+    if (n_rows < 0 || n_rows >= kMaxRows || d < 1 || f < 1 || d > kMaxMx4Width || f > kMaxMx4Width) return 0;
+    return int4_ws_bytes(n_rows, d, f);
+}
+
+int moe_int4_ffn(const moe_glu* glu, const void* x, int T, int k, const int32_t* topk_idx, const float* topk_w,
+                 const int32_t* dst_row, const int32_t* src_slot, const int32_t* group_off, int E, int d, int f,
+                 int group, const moe_int4* w13, const moe_int4* w2, void* out, void* ws, size_t ws_bytes,
+                 int32_t* dev_err, moe_stream_t stream)
+{
+    Int4Ffn a{};
+    if (!glu_spec(glu, a.glu) || !w13 || !w2) return MOE_EINVAL;
+    if (a.glu.drop.thr) return MOE_EUNSUPPORTED;
+    if (T < 0 || k < 1 || k > kMaxTopK || E < 1 || E > kMaxExperts || (int64_t)T * k >= kMaxRows || d < 1 || f < 1 ||
+        d > kMaxMx4Width || f > kMaxMx4Width)
+        return MOE_EINVAL;
+    if (group != 32 && group != 64 && group != 128) return MOE_EUNSUPPORTED;
+    if (d % group || f % group) return MOE_EALIGN;
+    if (!group_off || !w13->codes || !w13->scales || !w2->codes || !w2->scales) return MOE_EINVAL;
+    if (T > 0 && (!x || !topk_idx || !topk_w || !dst_row || !src_slot || !out)) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(out) || !aligned16(w13->codes) || !aligned16(w2->codes) ||
+        (reinterpret_cast<uintptr_t>(w13->scales) & 1u) || (reinterpret_cast<uintptr_t>(w2->scales) & 1u))
+        return MOE_EALIGN;
+    if (!ws || ws_bytes < int4_ws_bytes((int64_t)T * k, d, f) || !aligned16(ws)) return MOE_EWORKSPACE;
+    a.x = (const uint16_t*)x;
+    a.T = T;
+    a.k = k;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.dst_row = dst_row;
+    a.src_slot = src_slot;
+    a.group_off = group_off;
+    a.E = E;
+    a.d = d;
+    a.f = f;
+    a.group = group;
+    a.w13 = *w13;
+    a.w2 = *w2;
+    a.out = (uint16_t*)out;
+    a.ws = ws;
+    a.dev_err = dev_err;
+    return status_of(launch_int4_ffn(a, as_stream(stream)));
 }
 
 int moe_router_logits(const void* x, const void* w_router, int T, int E, int d, float* logits,

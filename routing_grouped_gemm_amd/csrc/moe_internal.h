@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "../../include/moe.h"
 
@@ -154,6 +155,24 @@ constexpr int kMxColPad = 128;   // column-wise MXFP8 groups are padded to this 
 // launch's control words (written by a small kernel ahead of the launch).
 constexpr size_t kGemmCtlBytes = 256;
 
+// run f(integral_constant<int, k>) for k in 1..kMaxTopK
+template <class F>
+hipError_t with_k(int k, F&& f)
+{
+    switch (k) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    case 4: f(std::integral_constant<int, 4>{}); break;
+    case 5: f(std::integral_constant<int, 5>{}); break;
+    case 6: f(std::integral_constant<int, 6>{}); break;
+    case 7: f(std::integral_constant<int, 7>{}); break;
+    case 8: f(std::integral_constant<int, 8>{}); break;
+    default: return hipErrorInvalidValue;
+    }
+    return hipSuccess;
+}
+
 inline hipStream_t as_stream(moe_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
 // route
@@ -200,6 +219,50 @@ hipError_t launch_balance_bwd(const float* logits, const uint8_t* mask, const in
                               const int32_t* counts, const int32_t* tokens, float cb, float cz, const float* dlosses,
                               const float* add, float* dlogits, hipStream_t s);
 
+// dropout: drop where 16 random bits are below thr (0: nothing is dropped), else multiply by scale
+struct DropSpec {
+    uint32_t thr;
+    float scale;
+    const uint64_t* rng;   // device {seed, step}
+};
+hipError_t launch_dropout(int dtype, const void* x, const void* residual, int64_t n, DropSpec dr, void* out,
+                          hipStream_t s);
+hipError_t launch_combine_dropout(int dtype, const void* y_perm, const int32_t* dst_row, const float* w,
+                                  const void* residual, int T, int k, int d, int64_t n_rows, DropSpec dr, void* out,
+                                  int32_t* dev_err, hipStream_t s);
+
+// a gated block's form as the kernels take it
+struct GluSpec {
+    int act;
+    float limit;           // infinity: none
+    DropSpec drop;
+};
+inline bool plain_swiglu(const GluSpec& g) { return g.act == MOE_ACT_SILU && !(g.limit < __builtin_inff()) && !g.drop.thr; }
+constexpr GluSpec kSwiglu{MOE_ACT_SILU, __builtin_inff(), {0, 1.0f, nullptr}};
+
+// 4-bit integers
+hipError_t launch_quantize_int4(const uint16_t* src, int64_t rows, int K, int group, uint8_t* codes, uint16_t* scales,
+                                uint8_t* zeros, hipStream_t s);
+hipError_t launch_dequantize_int4(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, int64_t rows,
+                                  int K, int group, uint16_t* dst, hipStream_t s);
+size_t int4_ws_bytes(int64_t n_rows, int d, int f);
+struct Int4Ffn {
+    GluSpec glu;
+    const uint16_t* x;
+    int T, k;
+    const int32_t* topk_idx;
+    const float* topk_w;
+    const int32_t* dst_row;
+    const int32_t* src_slot;
+    const int32_t* group_off;
+    int E, d, f, group;
+    moe_int4 w13, w2;
+    uint16_t* out;
+    void* ws;
+    int32_t* dev_err;
+};
+hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s);
+
 // router scores and the gradient through the gate weights
 hipError_t launch_router_logits(const uint16_t* x, const uint16_t* w, int T, int E, int d, float* logits,
                                 hipStream_t s);
@@ -215,9 +278,9 @@ struct GroupSpec {
     int E;
     int64_t n_rows;
 };
-hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f,
+hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const GluSpec& glu, int d, int f,
                         hipStream_t s);
-hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f,
+hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const GluSpec& glu, int d, int f,
                        hipStream_t s);
 size_t gemm_ws_mxfp8(int E, int64_t n_rows, int d, int f);
 hipError_t gemm_op_mxfp8(int op, const moe_gemm_tensors& t, GroupSpec g, int d, int f, void* ws,

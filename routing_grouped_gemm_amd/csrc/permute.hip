@@ -11,8 +11,6 @@
 // MXFP8 (tutorial, MXFP8 section): one E8M0 scale per 32 elements, the
 // smallest power of two that keeps the block maximum within 448, codes by
 // round-to-nearest-even into E4M3FN.
-#include <type_traits>
-
 #include "moe_internal.h"
 
 namespace moe {
@@ -528,24 +526,6 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint4* __restrict_
             if (lane == j) dw_out[(int64_t)t * K + j] = acc[j];
     }
     if (bad && lane == 0 && dev_err) atomicOr(dev_err, (int)MOE_ERR_ROW_RANGE);
-}
-
-// run f(integral_constant<int, k>) for k in 1..kMaxTopK
-template <class F>
-hipError_t with_k(int k, F&& f)
-{
-    switch (k) {
-    case 1: f(std::integral_constant<int, 1>{}); break;
-    case 2: f(std::integral_constant<int, 2>{}); break;
-    case 3: f(std::integral_constant<int, 3>{}); break;
-    case 4: f(std::integral_constant<int, 4>{}); break;
-    case 5: f(std::integral_constant<int, 5>{}); break;
-    case 6: f(std::integral_constant<int, 6>{}); break;
-    case 7: f(std::integral_constant<int, 7>{}); break;
-    case 8: f(std::integral_constant<int, 8>{}); break;
-    default: return hipErrorInvalidValue;
-    }
-    return hipSuccess;
 }
 
 inline unsigned grid_for(int64_t n) { return (unsigned)((n + 255) / 256); }

@@ -21,16 +21,18 @@ dw2 from the 4-bit copy: the gradient of the forward that ran.
 """
 import torch
 
-from . import (MOE_BF16, MOE_F32, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP, MOE_GEMM_WGRAD,
-               MOE_MXFP4, MOE_MXFP8,
-               gemm_tensors, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes,
-               moe_dequantize_mxfp4, moe_gemm_workspace_bytes, moe_grouped_gemm_bwd, moe_grouped_gemm_fwd,
-               moe_gate_grad, moe_grouped_gemm_op, moe_permute, moe_quantize_mxfp4, moe_quantize_mxfp8,
+from . import (MOE_ACT_RELU, MOE_ACT_SILU, MOE_BF16, MOE_F32, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP,
+               MOE_GEMM_WGRAD, MOE_INT4, MOE_MXFP4, MOE_MXFP8,
+               gemm_tensors, glu, moe_balance_loss, moe_balance_loss_bwd, moe_balance_workspace_bytes,
+               moe_combine_dropout, moe_dequantize_mxfp4, moe_dropout, moe_gemm_workspace_bytes, moe_grouped_gemm_bwd,
+               moe_grouped_gemm_fwd, moe_gate_grad, moe_grouped_gemm_op, moe_grouped_glu_bwd, moe_grouped_glu_fwd,
+               moe_grouped_glu_op, moe_int4_ffn, moe_int4_workspace_bytes, moe_permute, moe_quantize_int4,
+               moe_quantize_mxfp4, moe_quantize_mxfp8,
                moe_route_add_shared, moe_route_topk, moe_route_workspace_bytes, moe_router_logits,
                moe_unpermute_combine)
 
 _ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_MXFP8: torch.bfloat16,
-        MOE_MXFP4: torch.bfloat16}
+        MOE_MXFP4: torch.bfloat16, MOE_INT4: torch.bfloat16}
 
 
 class MoELayer:
@@ -39,15 +41,61 @@ class MoELayer:
     then [E + n_shared, ...] with the shared experts last, and the buffers hold
     the routed rows followed by n_shared * T shared rows.  save=False (MXFP4
     only) keeps no activations for a backward, as serving wants it.
-    decode_h=True (MXFP4 only): dw2 from the 4-bit h."""
+    decode_h=True (MXFP4 only): dw2 from the 4-bit h.
+
+    act and limit: the gate of the experts' blocks, MOE_ACT_*, and the limit on
+    what goes into it (0: none); other ones than silu without a limit with
+    fp32, bf16 and INT4.  h_dropout: dropout of the experts' h (fp32, bf16);
+    out_dropout: of the layer's output, before the residual that forward may be
+    given.  Masks follow from rng, int64 [2, 2] on the device: (seed, step) of the
+    two.  Each forward advances both steps, by a kernel of its own, so that a
+    replayed graph draws new masks; forward(same_mask=True) does not, to
+    recompute activations.  Layers that train together need different seeds.
+    With training set to False nothing is dropped (set it before a forward and
+    leave it until its backward).
+
+    dtype=MOE_INT4 serves experts held in 4-bit integers with a scale for each
+    `group` elements, with zero points if zeros is true: forward only, unpadded,
+    activations in bf16."""
 
     def __init__(self, T, d, E, f, k, dtype=MOE_BF16, capacity=0, device="cuda", n_shared=0, save=True,
-                 decode_h=False):
-        if not save and dtype != MOE_MXFP4:
+                 decode_h=False, act=MOE_ACT_SILU, limit=0.0, h_dropout=0.0, out_dropout=0.0, seed=0, group=128,
+                 zeros=False):
+        if dtype == MOE_INT4:
+            save = False
+            if capacity:
+                raise ValueError("an INT4 layer has no padded layout")
+            if group not in (32, 64, 128) or d % group or f % group:
+                raise ValueError(f"INT4: groups of 32, 64 or 128 that divide d = {d} and f = {f}, got {group}")
+            if out_dropout:
+                raise ValueError("out_dropout: an INT4 layer serves, it has no dropout")
+        if not (MOE_ACT_SILU <= act <= MOE_ACT_RELU and 0 <= limit < float("inf")):
+            raise ValueError(f"act = {act}, limit = {limit}: expected a MOE_ACT_* and a limit >= 0 (0: none)")
+        for name, p in (("h_dropout", h_dropout), ("out_dropout", out_dropout)):
+            if not 0 <= p < 1:
+                raise ValueError(f"{name}: expected 0 <= p < 1, got {p}")
+        other_gate = act != MOE_ACT_SILU or limit > 0
+        if other_gate and dtype not in (MOE_F32, MOE_BF16, MOE_INT4):
+            raise ValueError("the MXFP8 and MXFP4 products have the silu gate without a limit")
+        if h_dropout and dtype not in (MOE_F32, MOE_BF16):
+            raise ValueError("h_dropout: fp32 and bf16 layers only")
+        if not save and dtype not in (MOE_MXFP4, MOE_INT4):
             raise ValueError("save=False: only the MXFP4 forward runs without its saved activations")
         if decode_h and (dtype != MOE_MXFP4 or not save):
             raise ValueError("decode_h=True: only an MXFP4 layer with saved activations has an h in 4 bits to decode")
         self.save, self.decode_h = save, decode_h
+        self.act, self.limit, self.h_dropout, self.out_dropout = act, limit, h_dropout, out_dropout
+        self.group, self.zeros = group, zeros
+        self.training = True
+        self._glu = None
+        self.rng = self._rng_step = None
+        if h_dropout or out_dropout:
+            # the two masks of one step are 2^62 steps apart
+            self.rng = torch.tensor([[seed, 0], [seed, 1 << 62]], dtype=torch.int64, device=device)
+            self._rng_step = self.rng[:, 1]
+        if other_gate or h_dropout:
+            rng = self.rng[0] if h_dropout else None
+            self._glu = {t: glu(act, limit, h_dropout if t else 0.0, rng) for t in (False, True)}
         self.T, self.d, self.E, self.f, self.k = T, d, E, f, k
         self.dtype, self.capacity, self.device = dtype, capacity, device
         self.S = n_shared
@@ -56,7 +104,7 @@ class MoELayer:
         self.R = E * capacity if capacity > 0 else T * k   # routed rows
         self.n_rows = self.R + n_shared * T
         R = self.n_rows
-        act = _ACT[dtype]
+        act_dtype = _ACT[dtype]
         i32 = dict(dtype=torch.int32, device=device)
         self.topk_idx = torch.empty(T, k, **i32)
         self.topk_w = torch.empty(T, k, dtype=torch.float32, device=device)
@@ -81,6 +129,12 @@ class MoELayer:
         self.dev_err = torch.zeros(1, **i32)
         self.route_ws = torch.empty(moe_route_workspace_bytes(T, E, k), dtype=torch.uint8,
                                     device=device)
+        if dtype == MOE_INT4:
+            self._glu = glu(act, limit)
+            self.out = torch.empty(T, d, dtype=act_dtype, device=device)
+            self.int4_ws = torch.empty(moe_int4_workspace_bytes(R, d, f), dtype=torch.uint8, device=device)
+            self._bwd_alloc = False
+            return
         if dtype == MOE_MXFP8:
             self.x_perm = torch.empty(R, d, dtype=torch.uint8, device=device)
             self.x_perm_scales = torch.empty(R, d // 32, dtype=torch.uint8, device=device)
@@ -88,12 +142,12 @@ class MoELayer:
             self.x_perm = torch.empty(R, d // 2, dtype=torch.uint8, device=device)
             self.x_perm_scales = torch.empty(R, d // 32, dtype=torch.uint8, device=device)
         else:
-            self.x_perm = torch.empty(R, d, dtype=act, device=device)
+            self.x_perm = torch.empty(R, d, dtype=act_dtype, device=device)
             self.x_perm_scales = None
-        self.gu = torch.empty(R, 2 * f, dtype=act, device=device) if save else None
-        self.h = torch.empty(R, f, dtype=act, device=device) if save else None
-        self.y_perm = torch.empty(R, d, dtype=act, device=device)
-        self.out = torch.empty(T, d, dtype=act, device=device)
+        self.gu = torch.empty(R, 2 * f, dtype=act_dtype, device=device) if save else None
+        self.h = torch.empty(R, f, dtype=act_dtype, device=device) if save else None
+        self.y_perm = torch.empty(R, d, dtype=act_dtype, device=device)
+        self.out = torch.empty(T, d, dtype=act_dtype, device=device)
         self.gemm_ws = None
         wsb = moe_gemm_workspace_bytes(dtype, self.G, R, d, f)
         if wsb:
@@ -104,7 +158,8 @@ class MoELayer:
         if self._bwd_alloc:
             return
         if not self.save:
-            raise RuntimeError("a layer made with save=False has no backward")
+            raise RuntimeError("an INT4 layer has no backward" if self.dtype == MOE_INT4 else
+                               "a layer made with save=False has no backward")
         R, d, f, E = self.n_rows, self.d, self.f, self.G
         act = _ACT[self.dtype]
         dev = self.device
@@ -142,7 +197,8 @@ class MoELayer:
         step), for MXFP4 the codes of both; MXFP4 weights that are refused leave
         the layer with the ones it had.  Each call makes new caches and a captured
         graph reads those of its capture: for weights that change under a graph,
-        write them into w13 and w2 and call requantize_weights, which works in place."""
+        write them into w13 and w2 and call requantize_weights, which works in place.
+        INT4: the codes are made here, and the bf16 weights are not kept."""
         if self.dtype == MOE_MXFP4:
             E, f, d = self.G, self.f, self.d
             for name, w, n in (("w13", w13, E * 2 * f * d), ("w2", w2, E * d * f)):
@@ -157,6 +213,23 @@ class MoELayer:
             self.w13, self.w2 = w13, w2
             if self._bwd_alloc:
                 self._decode_weights()
+            return
+        if self.dtype == MOE_INT4:
+            E, f, d, g = self.G, self.f, self.d, self.group
+            for name, w, n in (("w13", w13, E * 2 * f * d), ("w2", w2, E * d * f)):
+                if w.dtype is not torch.bfloat16 or w.numel() != n or w.get_device() != self.out.get_device():
+                    raise ValueError(f"{name}: expected a torch.bfloat16 tensor of {n} elements on {self.out.device}, "
+                                     f"got {w.dtype} {tuple(w.shape)} on {w.device}")
+            made = []
+            for w, N, K in ((w13, 2 * f, d), (w2, d, f)):
+                u8 = dict(dtype=torch.uint8, device=self.device)
+                codes = torch.empty(E, N, K // 2, **u8)
+                scales = torch.empty(E, N, K // g, dtype=torch.bfloat16, device=self.device)
+                zeros = torch.empty(E, N, K // g, **u8) if self.zeros else None
+                moe_quantize_int4(w.reshape(E * N, K), g, codes.view(E * N, -1), scales.view(E * N, -1),
+                                  None if zeros is None else zeros.view(E * N, -1))
+                made.append((codes, scales, zeros))
+            self.set_weights_int4(*made)
             return
         self.w13, self.w2 = w13, w2
         self._stages = None
@@ -192,6 +265,22 @@ class MoELayer:
         self.w13_q, self.w13_s, self.w2_q, self.w2_s = w13_q, w13_s, w2_q, w2_s
         self.w13 = self.w2 = None   # these codes have no bf16 weights behind them
         self._stages = None
+
+    def set_weights_int4(self, w13, w2):
+        """INT4: weights that are held in 4-bit integers already, each (codes, scales, zeros or
+        None) as moe_quantize_int4 makes them: codes [E, 2f, d/2] and [E, d, f/2] uint8, scales
+        and zeros [..., K/group].  The layer reads these tensors at each step."""
+        if self.dtype != MOE_INT4:
+            raise ValueError("set_weights_int4 needs an INT4 layer")
+        E, f, d = self.G, self.f, self.d
+        for name, w, N, K in (("w13", w13, 2 * f, d), ("w2", w2, d, f)):
+            for t, shape, dt in zip(w, ((E, N, K // 2), (E, N, K // self.group), (E, N, K // self.group)),
+                                    (torch.uint8, torch.bfloat16, torch.uint8)):
+                if t is not None and (tuple(t.shape) != shape or t.dtype is not dt or not t.is_contiguous()
+                                      or t.get_device() != self.out.get_device()):
+                    raise ValueError(f"{name}: expected a contiguous {dt} tensor of shape {shape} on {self.out.device}, "
+                                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        self.w13_4, self.w2_4 = tuple(w13), tuple(w2)
 
     def _quantize_mxfp4(self, w13, w2, w13_q, w13_s, w2_q, w2_s):
         E, f, d = self.G, self.f, self.d
@@ -243,6 +332,8 @@ class MoELayer:
         """Issue one grouped GEMM stage (MOE_GEMM_*) on the layer's buffers (the
         forward and backward calls are these stages in order).  Call
         set_weights first; the tensors are bound on first use."""
+        if self.dtype == MOE_INT4:
+            raise ValueError("an INT4 layer has no separate stages")
         if getattr(self, "_stages", None) is None:
             self._stages = self._stage_tensors()
         bwd = op in (MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP)
@@ -254,6 +345,10 @@ class MoELayer:
             elif self.w13 is None:
                 self._decode_weights()
             bwd, dtype = True, MOE_BF16
+        if self._glu is not None:
+            moe_grouped_glu_op(op, dtype, self._glu[self.training], self._stages[1 if bwd else 0], self.s_off,
+                               self.g_cap, self.G, self.n_rows, self.d, self.f)
+            return
         moe_grouped_gemm_op(op, dtype, self._stages[1 if bwd else 0], self.s_off,
                             self.g_cap, self.G, self.n_rows, self.d, self.f)
 
@@ -291,7 +386,10 @@ class MoELayer:
                     x_perm_scales=self.x_perm_scales, dev_err=self.dev_err)
 
     def gemm_fwd(self):
-        if self.dtype in (MOE_MXFP8, MOE_MXFP4):
+        if self._glu is not None:
+            moe_grouped_glu_fwd(self.dtype, self._glu[self.training], self.x_perm, self.w13, self.w2, self.s_off,
+                                self.g_cap, self.gu, self.h, self.y_perm)
+        elif self.dtype in (MOE_MXFP8, MOE_MXFP4):
             moe_grouped_gemm_fwd(self.dtype, self.x_perm, self.w13_q, self.w2_q, self.s_off,
                                  self.g_cap, self.gu, self.h, self.y_perm,
                                  x_perm_scales=self.x_perm_scales, w13_scales=self.w13_s,
@@ -306,7 +404,16 @@ class MoELayer:
         assert not self.S, "per-row weights are not combined with shared experts"
         return weights
 
-    def combine(self, weights=None):
+    def _out_drop(self):
+        return self.out_dropout if self.training else 0.0
+
+    def combine(self, weights=None, residual=None):
+        p = self._out_drop()
+        if p or residual is not None:
+            moe_combine_dropout(MOE_F32 if self.dtype == MOE_F32 else MOE_BF16, self.y_perm, self.s_dst,
+                                self._slot_weights(weights), self.K, p, self.rng[1] if p else None, self.out,
+                                residual=residual, dev_err=self.dev_err)
+            return
         moe_unpermute_combine(MOE_F32 if self.dtype == MOE_F32 else MOE_BF16, self.y_perm,
                               self.s_dst, self._slot_weights(weights), self.K, self.out,
                               dev_err=self.dev_err)
@@ -320,7 +427,9 @@ class MoELayer:
 
     def gate_grad(self, dout):
         """dlogits [T, E] fp32: the gradient of <dout, out> through the gate
-        weights of the last forward (bf16 activations; call after forward)."""
+        weights of the last forward (bf16 activations; call after forward).  dout
+        is the gradient of the layer's output, whatever was dropped of it."""
+        dout = self._drop_dout(dout)
         if getattr(self, "dlogits", None) is None:
             self.dlogits = torch.empty(self.T, self.E, dtype=torch.float32, device=dout.device)
         moe_gate_grad(dout, self.y_perm, self.topk_idx, self.topk_w, self.dst_row, self.dlogits,
@@ -368,19 +477,49 @@ class MoELayer:
                              dlosses=dlosses, add=add_to, seg_off=seg_off, mask=mask)
         return self.dlogits
 
-    def forward(self, logits, x, weights=None):
+    def next_mask(self):
+        """Advance the steps of both masks (forward does)."""
+        if self.rng is not None:
+            self._rng_step.add_(1)
+
+    def _drop_dout(self, dout):
+        # the upstream gradient under the output's mask
+        p = self._out_drop()
+        if not p:
+            return dout
+        if getattr(self, "dsum", None) is None:
+            self.dsum = torch.empty(self.T, self.d, dtype=_ACT[self.dtype], device=self.device)
+        moe_dropout(MOE_F32 if self.dtype == MOE_F32 else MOE_BF16, dout, p, self.rng[1], self.dsum)
+        return self.dsum
+
+    def forward(self, logits, x, weights=None, residual=None, same_mask=False):
+        """out [T, d]: the layer's output, dropped by out_dropout and added to residual [T, d] if
+        given (whose gradient is dout itself)."""
         self.route(logits)
+        if self.dtype == MOE_INT4:
+            if weights is not None or residual is not None:
+                raise ValueError("an INT4 layer takes neither weights nor a residual")
+            moe_int4_ffn(self._glu, x, self.s_idx, self.s_w, self.s_dst, self.s_src, self.s_off, self.group,
+                         self.w13_4, self.w2_4, self.out, self.int4_ws, dev_err=self.dev_err)
+            return self.out
+        if self.training and not same_mask:
+            self.next_mask()
         self.permute(x)
         self.gemm_fwd()
-        self.combine(weights)
+        self.combine(weights, residual)
         return self.out
 
     def backward(self, dout, weights=None):
         self._alloc_bwd()
+        dout = self._drop_dout(dout)
         act_dt = MOE_F32 if self.dtype == MOE_F32 else MOE_BF16
         moe_permute(act_dt, dout, self.K, self.s_dst, self.dy_perm, src_slot=self.s_fill,
                     row_scale=self._slot_weights(weights), dev_err=self.dev_err)
-        if self.dtype == MOE_MXFP8:
+        if self._glu is not None:
+            moe_grouped_glu_bwd(self.dtype, self._glu[self.training], self.dy_perm, self.x_perm, self.gu, self.h,
+                                self.w13, self.w2, self.s_off, self.g_cap, self.dgu, self.dx_perm, self.dw13,
+                                self.dw2, ws=self.gemm_ws)
+        elif self.dtype == MOE_MXFP8:
             moe_grouped_gemm_bwd(self.dtype, self.dy_perm, self.x_perm, self.gu, self.h,
                                  self.w13t_q, self.w2t_q, self.s_off, self.g_cap, self.dgu,
                                  self.dx_perm, self.dw13, self.dw2,

@@ -664,8 +664,8 @@ MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
  * Which of its kernels run depends on the sizes, and with that the order of the
  * fp32 sums: a token's output may differ in the last bits between batches.
  * A token row with an infinity or a NaN gives NaN.
- * Errors: MOE_EINVAL (sizes: k <= 8, E <= 1024, T * k < 2^31, d and f at most
- * 2^20; null pointers), MOE_EUNSUPPORTED (group, p), MOE_EALIGN (d or f not a
+ * Errors: MOE_EINVAL (sizes: k <= 8, E <= 1024; T * d and T * k * f below 2^30,
+ * d * f below 2^31, d and f at most 2^20; null pointers), MOE_EUNSUPPORTED (group, p), MOE_EALIGN (d or f not a
  * multiple of group; x, out, codes not 16-byte aligned, scales not 2-byte),
  * MOE_EWORKSPACE.
  */

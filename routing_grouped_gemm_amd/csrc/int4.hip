@@ -112,11 +112,50 @@ __global__ __launch_bounds__(256) void dequantize_int4_kernel(const uint32_t* __
 // ---------------------------------------------------------------- products
 __device__ __forceinline__ bf16x8 as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-// the bf16 numbers 16 + q of eight codes: pairs (0,4) (1,5) (2,6) (3,7)
-__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w)
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
 {
-    return make_uint4(((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                      ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u);
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+}
+
+// The constants of a conversion, one in a vector register: with two literals the and-or would be two instructions
+struct Conv {
+    uint32_t mask, base;
+};
+__device__ __forceinline__ Conv conv()
+{
+    Conv c{0x00780078u, 0x41804180u};
+    asm("" : "+s"(c.mask));
+    asm("" : "+v"(c.base));
+    return c;
+}
+
+// the bf16 numbers 16 + q of eight codes: pairs (0,4) (1,5) (2,6) (3,7)
+__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w, Conv c)
+{
+    return make_uint4(((w << 3) & c.mask) | c.base, ((w >> 1) & c.mask) | c.base, ((w >> 5) & c.mask) | c.base,
+                      ((w >> 9) & c.mask) | c.base);
+}
+
+// The products' zero points come off by a matrix instruction too: X, a row's sum of x over a group, as three bf16
+// numbers that add up to it exactly, times -(16 + z).  x side: lane group 0 has the three (row = lane & 15), the
+// others zeros; weight side: the bf16 number -(16 + z) of the lane's column.  (The same 32-deep instruction as the
+// products': a 16-deep one would do, but a product that took its result as the sum to add to read it too soon,
+// without the wait states that mixed depths need.)
+__device__ __forceinline__ uint4 split_sum(float X)
+{
+    const uint32_t hi = __float_as_uint(X) & 0xffff0000u;
+    const float r = X - __uint_as_float(hi);
+    const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
+    const uint32_t lo = __float_as_uint(r - __uint_as_float(mid));
+    return make_uint4((hi >> 16) | mid, lo >> 16, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 minus_zeros(uint4 X, uint32_t z)
+{
+    const uint32_t v = 0xc180c180u + z * 0x00080008u;
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(X), as_bf16x8(make_uint4(v, v, v, v)), f32x4{0, 0, 0, 0}, 0, 0, 0);
 }
 
 // eight x in the same order
@@ -136,83 +175,239 @@ __device__ __forceinline__ uint4 exchange4(uint4 v)
     return make_uint4(c[0], c[1], d[0], d[1]);
 }
 
-// one weight row of a lane: codes, scales and zero points from the row's start
-struct WRow {
-    const uint8_t* codes;
-    const uint16_t* scales;
-    const uint8_t* zeros;    // or nullptr
+// Buffer descriptors over one expert's matrix (zeros: over nothing if there are none, so that they load as 0).
+// Sizes stay below 2^31 bytes (checked on the host).
+struct WBuf {
+    __amdgpu_buffer_rsrc_t codes, scales, zeros;
 };
 
-__device__ __forceinline__ WRow w_row(const moe_int4& w, int64_t row, int K, int group)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_of(const void* p, int64_t bytes)
 {
-    const int64_t n = row * (K / group);
-    return {w.codes + row * (K / 2), (const uint16_t*)w.scales + n, w.zeros ? w.zeros + n : nullptr};
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// acc[t] += (x rows) . (weight rows of column tile t) over chunk c of 128 codes.
-// x: the lane's row (nullptr: a row of zeros).  Nothing past K is read.
-template <int G, int NT>
-__device__ __forceinline__ void chunk_product(f32x4 (&acc)[NT], const uint16_t* x, const WRow (&w)[NT], int c, int K,
-                                              float factor)
+__device__ __forceinline__ WBuf w_buf(const moe_int4& w, int e, int N, int K, int group)
 {
-    const int g = (threadIdx.x & 63) >> 4;
-    const int kb = c * 128;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 q[NT];
+    const int64_t n = (int64_t)N * K, ng = n / group;
+    return {buf_of(w.codes + e * (n / 2), n / 2), buf_of((const uint16_t*)w.scales + e * ng, ng * 2),
+            buf_of(w.zeros + (w.zeros ? e * ng : 0), w.zeros ? ng : 0)};
+}
+
+// (the whole offset in the lane's register: the hardware checks it against the size, and a scalar offset past the
+// size of a small buffer could wrap that check)
+__device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
+{
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+
+// 2 P consecutive chunks of 128 codes of NT column tiles on their way: P pairs of chunks, 16 rows x 128 bytes each in
+// two loads, eight neighbouring lanes a row's 128 bytes.  (Each lane loading the codes of its own column, as the
+// matrix operand has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 16% slower.)
+// Scale and zero point: lane 4r + j has those of row r and every fourth group, from the j-th on.
+template <int G, int NT, int P>
+struct Codes {
+    static constexpr int NS = (P * 256 / G + 3) / 4;
+    uint4 q[P][NT][2];
+    uint32_t s[NS][NT], z[NS][NT];
+};
+
+// Where a step's codes lie: the expert's matrix, and the lane's offsets of its rows' first codes and scales.  A step
+// that loads nothing has offsets past every buffer.
+template <int NT>
+struct Where {
+    WBuf w;
+    uint32_t code[NT], scale[NT];
+    int left;                // groups from this lane's first on to the row's end
+};
+constexpr uint32_t kPast = 0x80000000u;
+
+// column tiles from row0[t] on, chunks from c on
+template <int G, int NT>
+__device__ __forceinline__ Where<NT> where_of(const WBuf& w, const int (&row0)[NT], int c, int K, bool live)
+{
+    const int lane = threadIdx.x & 63;
+    // (chunks past the row's end within a wave's share are other rows' codes, and not used)
+    const uint32_t past = live && c * 128 < K ? 0 : kPast;
+    Where<NT> p;
+    p.w = w;
+    p.left = K / G - c * (128 / G) - (lane & 3);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-        q[t] = kb + 32 * g < K ? *reinterpret_cast<const uint4*>(w[t].codes + kb / 2 + 16 * g) : zero;
-    bf16x8 xf[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int block = G == 128 ? g : i;             // which 32 codes
-        const int k = kb + 32 * block + 8 * (G == 128 ? i : g);
-        const uint4 v = x && kb + 32 * block < K ? *reinterpret_cast<const uint4*>(x + k) : zero;
-        xf[i] = as_bf16x8(pair_order(v));
+    for (int t = 0; t < NT; ++t) {
+        p.code[t] = (uint32_t)((row0[t] + (lane >> 3)) * (K / 2) + c * 64 + 16 * (lane & 7)) | past;
+        p.scale[t] = (uint32_t)((row0[t] + (lane >> 2)) * (K / G) + c * (128 / G) + (lane & 3)) | past >> 1;
     }
-    if constexpr (G != 128) {
+    return p;
+}
+
+template <int G, int NT, int P>
+__device__ __forceinline__ void load_pair(Codes<G, NT, P>& o, const Where<NT>& p, int v, int K)
+{
 #pragma unroll
-        for (int t = 0; t < NT; ++t) q[t] = exchange4(q[t]);
+    for (int t = 0; t < NT; ++t) {
+        o.q[v][t][0] = load16(p.w.codes, p.code[t] + 128 * v);
+        o.q[v][t][1] = load16(p.w.codes, p.code[t] + 4 * K + 128 * v);     // eight rows on
     }
-    constexpr int PER = G / 32;                          // MFMAs of a group
+}
+
+template <int G, int NT, int P>
+__device__ __forceinline__ void load_scales(Codes<G, NT, P>& o, const Where<NT>& p, int i)
+{
 #pragma unroll
-    for (int b = 0; b < 4 / PER; ++b) {
-        if (kb + b * G >= K) break;
+    for (int t = 0; t < NT; ++t) {
+        // a group past the row's end is the next row's, whose scale may be a NaN: none is loaded for it
+        const uint32_t past = p.left > 4 * i ? 0 : kPast;
+        o.s[i][t] = __builtin_amdgcn_raw_buffer_load_b16(p.w.scales, (int)((p.scale[t] * 2 + 8 * i) | past), 0, 0);
+        o.z[i][t] = __builtin_amdgcn_raw_buffer_load_b8(p.w.zeros, (int)((p.scale[t] + 4 * i) | past), 0, 0);
+    }
+}
+
+template <int G, int NT, int P>
+__device__ __forceinline__ void load_all(Codes<G, NT, P>& o, const Where<NT>& p, int K)
+{
+    // in the order in which they will be waited for, here as in the loop: the compiler counts the loads in flight
+    constexpr int GC = 128 / G;
+#pragma unroll
+    for (int u = 0; u < 2 * P; ++u) {
+        if (u * GC % 4 == 0) load_scales(o, p, u * GC / 4);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u % 2 == 0) load_pair(o, p, u / 2, K);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// A wave's own LDS: a pair of chunks passes through it from the lanes that loaded it to those whose column it is.
+// Part p (16 bytes) of row r lies at part p ^ (r / 2), so that the sixteen rows of a lane group's read and the eight
+// parts of a row's write each fall on different banks.
+template <int NT>
+struct Turn {
+    uint4 part[NT][16][8];
+};
+
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int G, int NT, int P>
+__device__ __forceinline__ void put_pair(Turn<NT>& turn, const Codes<G, NT, P>& w, int v)
+{
+    const int lane = threadIdx.x & 63, r = lane >> 3, p = lane & 7;
+    wave_fence();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        turn.part[t][r][p ^ (r >> 1)] = w.q[v][t][0];
+        turn.part[t][r + 8][p ^ ((r + 8) >> 1)] = w.q[v][t][1];
+    }
+    wave_fence();
+}
+
+// 2 P chunks of a lane's x row as matrix operands, and each group's sum over the row (lane group 0; 0 in the others)
+template <int G, int U>
+struct XRows {
+    static constexpr int PER = G / 32;                           // MFMAs of a group
+    static constexpr int GROUPS = U * 128 / G;
+    bf16x8 f[U][4];
+    float X[GROUPS];
+
+    // chunks c .. c + U - 1 of the row at byte `at`
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, uint32_t at, int c, int K)
+    {
+        const int g = (threadIdx.x & 63) >> 4;
+        const uint32_t off = at + c * 256 + (G == 128 ? 64 * g : 16 * g);
+        uint4 v[U][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[u][i] = load16(x, off + 256 * u + (G == 128 ? 16 : 64) * i);
+        if ((c + U) * 128 > K) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if ((c + u) * 128 + 32 * (G == 128 ? g : i) >= K) v[u][i] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[u][i] = as_bf16x8(pair_order(v[u][i]));
         const bf16x8 ones = as_bf16x8(make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
-        f32x4 X = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < PER; ++i) X = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[b * PER + i], ones, X, 0, 0, 0);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const uint32_t qw[4] = {q[t].x, q[t].y, q[t].z, q[t].w};
-            f32x4 p = {0, 0, 0, 0};
+        for (int n = 0; n < GROUPS; ++n) {
+            f32x4 s = {0, 0, 0, 0};                              // ones on the weight side's place: column = row of x
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[b * PER + i], as_bf16x8(codes_to_bf16(qw[b * PER + i])), p,
-                                                            0, 0, 0);
-            const int gi = (kb + b * G) / G;
-            const float s = bf16_to_f32(w[t].scales[gi]) * factor;
-            const float z = 16.0f + (w[t].zeros ? (float)w[t].zeros[gi] : 8.0f);
+                s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, f[(n * PER + i) / 4][(n * PER + i) % 4], s, 0, 0, 0);
+            X[n] = g == 0 ? s[0] : 0.0f;
+        }
+    }
+};
+
+// acc[t] += (x rows) . (weight rows) over the first n chunks.  ahead(v) is called when pair v's codes have
+// left their registers, ahead_scales(i) when the i-th scales have.
+template <int G, int NT, int P, class F, class S>
+__device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G, 2 * P>& x, Codes<G, NT, P>& w, Turn<NT>& turn,
+                                        uint32_t z8, int n, Conv cv, F&& ahead, S&& ahead_scales)
+{
+    constexpr int PER = G / 32, GC = 128 / G;                    // MFMAs of a group, groups of a chunk
+    const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    uint32_t sz[NT][4];      // bf16 scale in the upper half, zero point below
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(s, fmaf(-z, X[r], p[r]), acc[t][r]);
+    for (int u = 0; u < 2 * P; ++u) {
+        if (u * GC % 4 == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t v = (w.s[u * GC / 4][t] << 16) | (w.z[u * GC / 4][t] + z8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sz[t][j] = __builtin_amdgcn_ds_bpermute(4 * (4 * m + j), (int)v);
+            }
+            ahead_scales(u * GC / 4);
+        }
+        if (u % 2 == 0) {
+            put_pair(turn, w, u / 2);
+            ahead(u / 2);
+        }
+        if (u < n) {
+            uint4 q[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                q[t] = turn.part[t][m][(4 * (u & 1) + g) ^ (m >> 1)];
+                if constexpr (G != 128) q[t] = exchange4(q[t]);
+            }
+#pragma unroll
+            for (int b = 0; b < GC; ++b) {
+                const int gi = u * GC + b;
+                const uint4 X = split_sum(x.X[gi]);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const uint32_t qw[4] = {q[t].x, q[t].y, q[t].z, q[t].w};
+                    f32x4 p = minus_zeros(X, sz[t][gi % 4] & 0xffu);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.f[u][b * PER + i],
+                                                                    as_bf16x8(codes_to_bf16(qw[b * PER + i], cv)), p, 0, 0, 0);
+                    const float sc = bf16_hi(sz[t][gi % 4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sc, p[r], acc[t][r]);
+                }
+            }
         }
     }
 }
 
-constexpr int kW = 4;   // waves of a workgroup: they split K and add up in LDS
+constexpr int kWaves = 8;      // most waves of a workgroup
 
 // sum over the waves of element idx (row idx / 16, column idx % 16) of column tile t
 template <int NT>
-__device__ __forceinline__ float wave_sum(const float (&red)[kW][NT][256], int t, int idx)
+__device__ __forceinline__ float wave_sum(const float (*red)[NT][256], int waves, int t, int idx)
 {
     float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) v += red[w][t][idx];
+    for (int w = 0; w < waves; ++w) v += red[w][t][idx];
     return v;
 }
 
 template <int NT>
-__device__ __forceinline__ void put_acc(float (&red)[kW][NT][256], const f32x4 (&acc)[NT])
+__device__ __forceinline__ void put_acc(float (*red)[NT][256], const f32x4 (&acc)[NT])
 {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
@@ -222,113 +417,578 @@ __device__ __forceinline__ void put_acc(float (&red)[kW][NT][256], const f32x4 (
     __syncthreads();
 }
 
-struct Rows {
-    int e;             // expert
-    int64_t row0;      // first row of h (and y)
-    int valid;         // rows of the tile
-    int nt;            // column tile
+// s_pref[e] = tiles of the experts before e (ceil(rows / 16) * ntn each), s_pref[E] = all: the first wave scans the
+// offsets, up to 16 experts a lane
+__device__ __forceinline__ int tile_prefix(const Int4Ffn& a, int ntn, int* s_pref)
+{
+    if (threadIdx.x < 64) {
+        const int per = (a.E + 63) >> 6, g0 = threadIdx.x * per;
+        const int64_t R = (int64_t)a.T * a.k;
+        int cnt = 0;
+        for (int i = 0; i < per && g0 + i < a.E; ++i) cnt += (int)((group_rows(a.group_off, 0, g0 + i, R) + 15) / 16) * ntn;
+        int incl = cnt;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(incl, off, 64);
+            if ((int)threadIdx.x >= off) incl += v;
+        }
+        int run = incl - cnt;
+        for (int i = 0; i < per && g0 + i < a.E; ++i) {
+            s_pref[g0 + i] = run;
+            run += (int)((group_rows(a.group_off, 0, g0 + i, R) + 15) / 16) * ntn;
+        }
+        if (threadIdx.x == 63) s_pref[a.E] = incl;
+    }
+    __syncthreads();
+    return s_pref[a.E];
+}
+
+// The products of up to 16 rows of an expert with 16 NC of its columns (a tile), tiles expert after expert, rows
+// then columns.  A workgroup takes a run of tiles; its W waves share K.  The rows' operands and sums stay in
+// registers from tile to tile, and the next tile's codes are on their way while one is multiplied, so that a
+// workgroup's loads never stop.  K over 128 W U takes several steps a tile, which load the rows each time.
+//   GATE_UP  h = a(g') u': column tiles 0 .. NC - 1 are the gate's, then the up ones.
+//   else     y = h W2^T
+template <int G, int P, int NC, bool GATE_UP>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_rows_kernel(
+    Int4Ffn a, uint16_t* __restrict__ h, uint16_t* __restrict__ y)
+{
+    constexpr int NT = GATE_UP ? 2 * NC : NC, U = 2 * P;
+    const int W = blockDim.x >> 6;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Turn<NT>* turn = reinterpret_cast<Turn<NT>*>(smem);
+    float (*red)[NT][256] = reinterpret_cast<float (*)[NT][256]>(smem + W * sizeof(Turn<NT>));   // [2 W]
+    __shared__ int ok[2][16];
+    __shared__ int s_pref[kMaxExperts + 1];
+    const int N = GATE_UP ? a.f : a.d, K = GATE_UP ? a.d : a.f;
+    const int ntn = (N + 16 * NC - 1) / (16 * NC);
+    const int total = tile_prefix(a, ntn, s_pref);
+    const int first = (int)((int64_t)blockIdx.x * total / gridDim.x);
+    const int last = (int)((int64_t)(blockIdx.x + 1) * total / gridDim.x);
+    if (first >= last) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int m = lane & 15;
+    const int chunks = (K + 127) / 128;
+    const int blocks = (chunks + W * U - 1) / (W * U);           // steps a tile
+
+    struct Tile {
+        int e, nt, valid;
+        int64_t row0;
+    };
+    const int64_t R = (int64_t)a.T * a.k;
+    auto tile_at = [&](int L) __attribute__((always_inline)) {
+        Tile t;
+        t.e = find_group(s_pref, a.E, L);
+        const int local = L - s_pref[t.e], mt = local / ntn;
+        t.nt = local - mt * ntn;
+        t.row0 = group_begin(a.group_off, 0, t.e, R) + 16 * mt;
+        t.valid = (int)min((int64_t)16, group_rows(a.group_off, 0, t.e, R) - 16 * mt);
+        return t;
+    };
+
+    const int steps = (last - first) * blocks;
+    const auto xb = GATE_UP ? buf_of(a.x, (int64_t)a.T * a.d * 2) : buf_of(h, R * a.f * 2);
+    uint32_t xat = 0;
+    bool in = true;
+    int64_t have = -1;       // row of h whose tile's operands are held
+    XRows<G, U> x;
+    f32x4 acc[NT];
+    int buf = 0;
+
+    auto where = [&](const Tile& t, int kb, bool live) __attribute__((always_inline)) {
+        int row[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) row[i] = (i < NC ? 0 : N) + min((t.nt * NC + i % NC) * 16, N - 16);
+        return where_of<G>(w_buf(GATE_UP ? a.w13 : a.w2, t.e, GATE_UP ? 2 * N : N, K, G), row, (kb * W + wave) * U, K, live);
+    };
+    const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
+    const Conv cv = conv();
+    auto step = [&](Codes<G, NT, P>& c, const Tile& t, int kb, const Where<NT>& p) __attribute__((always_inline)) {
+        const int c0 = (kb * W + wave) * U, n = min(U, chunks - c0);
+        if (have != t.row0 || blocks > 1) {
+            if (have != t.row0) {
+                // rows past the tile's last are that one again
+                const int64_t row = t.row0 + min(m, t.valid - 1);
+                if constexpr (GATE_UP) {
+                    const int64_t slot = a.src_slot[row];
+                    in = slot >= 0 && slot < R;
+                    if (slot >= R && a.dev_err && threadIdx.x < 16)
+                        atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
+                    xat = in ? (uint32_t)(slot / a.k * a.d * 2) : 0;
+                } else {
+                    xat = (uint32_t)(row * a.f * 2);
+                }
+                have = t.row0;
+            }
+            x.load(xb, xat, c0, K);
+        }
+        if (kb == 0) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+        }
+        product<G, NT, P>(acc, x, c, turn[wave], z8, n, cv,
+                          [&](int v) __attribute__((always_inline)) { load_pair(c, p, v, K); },
+                          [&](int i) __attribute__((always_inline)) { load_scales(c, p, i); });
+        if (kb + 1 < blocks) return;
+        if (threadIdx.x < 16) ok[buf][m] = in;
+        put_acc<NT>(red + buf * W, acc);
+        for (int i = threadIdx.x; i < NC * 256; i += 64 * W) {
+            const int idx = i & 255, j = i >> 8, r = idx >> 4, col = (t.nt * NC + j) * 16 + (idx & 15);
+            if (r >= t.valid || col >= N) continue;
+            float v = wave_sum<NT>(red + buf * W, W, j, idx);
+            if constexpr (GATE_UP) {
+                const float L = a.glu.limit, g = limit_g(v, L), u = limit_u(wave_sum<NT>(red + buf * W, W, j + NC, idx), L);
+                with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) { v = act_of<decltype(A)::value, true>(g) * u; });
+                h[(t.row0 + r) * a.f + col] = ok[buf][r] ? (uint16_t)f32_to_bf16_bits(v) : 0;
+            } else {
+                y[(t.row0 + r) * a.d + col] = (uint16_t)f32_to_bf16_bits(v);
+            }
+        }
+        buf ^= 1;
+    };
+    // a chunk's registers take the next step's codes as soon as they are used
+    Codes<G, NT, P> codes;
+    Tile t = tile_at(first), tn = t;
+    load_all(codes, where(t, 0, true), K);
+    for (int s = 0, at = first, kb = 0; s < steps; ++s) {
+        int kn = kb + 1;
+        if (kn == blocks) {
+            kn = 0;
+            ++at;
+            if (++tn.nt == ntn && at < last) tn = tile_at(at);
+        }
+        step(codes, t, kb, where(tn, kn, s + 1 < steps));
+        t = tn;
+        kb = kn;
+    }
+}
+
+// ---------------------------------------------------------------- many rows an expert
+// Tiles of 64 rows: each of eight waves has 32 columns (16 and 16 of gate and up) of its own and all
+// the rows, so that a code is converted once for 64 products.  x passes through LDS in chunks of 128, in the codes' order and with each group's row sums,
+// two chunks in turn and one barrier a chunk; codes as in the kernel for few rows.
+constexpr int kTileRows = 64, kTileWaves = 4;
+
+struct XStage {
+    uint4 part[2][kTileRows][16];            // part p of row r at p ^ (r & 15)
+    uint4 sum[2][4][kTileRows];              // a row's sum over group b of the chunk, as split_sum has it
+    uint4 none[kTileRows];                   // zeros, what lane groups 1 to 3 take for it
 };
 
-// PAIR: one row a workgroup, that of slot blockIdx.y, whose expert topk_idx names
-// (row = slot).  Otherwise up to 16 rows of an expert's group.
-template <bool PAIR>
-__device__ __forceinline__ bool find_rows(const Int4Ffn& a, int ntn, Rows& o)
+template <int G, bool GATE_UP>
+__global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_tile_kernel(
+    Int4Ffn a, uint16_t* __restrict__ h, uint16_t* __restrict__ y)
 {
-    if constexpr (PAIR) {
-        const int p = blockIdx.y;
-        o.e = a.topk_idx[p];
-        const int32_t dst = a.dst_row[p];
-        const bool bad = o.e < 0 || o.e >= a.E || dst >= a.T * a.k;
-        if (bad && a.dev_err && threadIdx.x == 0) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
-        o.row0 = p;
-        o.valid = 1;
-        o.nt = blockIdx.x;
-        return !bad && dst >= 0;
-    } else {
-        gemm::MTile m;
-        if (!gemm::schedule_m<16>(a.group_off, 0, a.E, (int64_t)a.T * a.k, ntn, m)) return false;
-        o = Rows{m.e, m.row0, m.rows_valid, m.nt};
-        return true;
-    }
-}
+    constexpr int NT = 2, NC = GATE_UP ? 1 : 2, MT = kTileRows / 16, GC = 128 / G, PER = G / 32;
+    constexpr int XR = kTileRows / (4 * kTileWaves);     // rows that a thread brings in
+    extern __shared__ __align__(16) uint8_t smem[];
+    XStage& xs = *reinterpret_cast<XStage*>(smem);
+    Turn<NT>* turn = reinterpret_cast<Turn<NT>*>(smem + sizeof(XStage));
+    const int N = GATE_UP ? a.f : a.d, K = GATE_UP ? a.d : a.f;
+    const int64_t R = (int64_t)a.T * a.k;
+    gemm::MTile tile;
+    if (!gemm::schedule_m<kTileRows>(a.group_off, 0, a.E, R, (N + 16 * NC * kTileWaves - 1) / (16 * NC * kTileWaves), tile)) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int m = lane & 15, g = lane >> 4;
+    const int chunks = (K + 127) / 128;
 
-// h = a(g') u' of 16 columns
-template <int G, bool PAIR>
-__global__ __launch_bounds__(64 * kW) void int4_gate_up_kernel(Int4Ffn a, uint16_t* __restrict__ h)
-{
-    __shared__ float red[kW][2][256];
-    Rows o;
-    if (!find_rows<PAIR>(a, a.f / 16, o)) return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int m = lane & 15;
-    const uint16_t* x = nullptr;
-    if (m < o.valid) {
-        const int64_t slot = PAIR ? o.row0 : a.src_slot[o.row0 + m];
-        if (slot >= 0 && slot < (int64_t)a.T * a.k) x = a.x + slot / a.k * a.d;
-        else if (slot >= 0 && a.dev_err) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
-    }
-    const int64_t n = (int64_t)o.e * 2 * a.f + o.nt * 16 + m;
-    const WRow w[2] = {w_row(a.w13, n, a.d, G), w_row(a.w13, n + a.f, a.d, G)};
-    f32x4 acc[2] = {};
-    const int chunks = (a.d + 127) / 128;
-    for (int c = wave; c < chunks; c += kW) chunk_product<G, 2>(acc, x, w, c, a.d, 1.0f);
-    put_acc(red, acc);
-    const int idx = threadIdx.x, r = idx >> 4;
-    if (r >= o.valid) return;
-    const float L = a.glu.limit;
-    const float g = limit_g(wave_sum(red, 0, idx), L), u = limit_u(wave_sum(red, 1, idx), L);
-    float v = 0.0f;
-    with_act(a.glu.act, [&](auto A) { v = act_of<decltype(A)::value, true>(g) * u; });
-    h[(o.row0 + r) * a.f + o.nt * 16 + (idx & 15)] = (uint16_t)f32_to_bf16_bits(v);
-}
-
-// y = h W2^T of 32 columns
-template <int G>
-__global__ __launch_bounds__(64 * kW) void int4_down_kernel(Int4Ffn a, const uint16_t* __restrict__ h,
-                                                            uint16_t* __restrict__ y)
-{
-    __shared__ float red[kW][2][256];
-    Rows o;
-    if (!find_rows<false>(a, a.d / 32, o)) return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int m = lane & 15;
-    const uint16_t* x = m < o.valid ? h + (o.row0 + m) * a.f : nullptr;
-    const int64_t n = (int64_t)o.e * a.d + o.nt * 32 + m;
-    const WRow w[2] = {w_row(a.w2, n, a.f, G), w_row(a.w2, n + 16, a.f, G)};
-    f32x4 acc[2] = {};
-    const int chunks = (a.f + 127) / 128;
-    for (int c = wave; c < chunks; c += kW) chunk_product<G, 2>(acc, x, w, c, a.f, 1.0f);
-    put_acc(red, acc);
-    const int idx = threadIdx.x, r = idx >> 4;
-    if (r >= o.valid) return;
+    // this thread's rows (threadIdx.x / 16 + 32 i) and 16 bytes of each chunk
+    const auto xb = GATE_UP ? buf_of(a.x, (int64_t)a.T * K * 2) : buf_of(h, R * K * 2);
+    const int xp = threadIdx.x & 15;
+    uint32_t xat[XR];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-        y[(o.row0 + r) * a.d + o.nt * 32 + 16 * t + (idx & 15)] = (uint16_t)f32_to_bf16_bits(wave_sum(red, t, idx));
+    for (int i = 0; i < XR; ++i) {
+        const int r = (threadIdx.x >> 4) + 4 * kTileWaves * i;
+        const int64_t row = tile.row0 + min(r, tile.rows_valid - 1);
+        if constexpr (GATE_UP) {
+            const int64_t slot = a.src_slot[row];
+            const bool in = slot >= 0 && slot < R;
+            if (slot >= R && xp == 0 && a.dev_err) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
+            xat[i] = in ? (uint32_t)(slot / a.k * K * 2) : kPast;        // a foreign row is one of zeros: so is its h
+        } else {
+            xat[i] = (uint32_t)(row * K * 2);
+        }
+    }
+    uint4 xr[XR];
+    auto load_x = [&](int c) __attribute__((always_inline)) {
+        const uint32_t past = c * 128 + 8 * xp < K ? 0 : kPast;
+#pragma unroll
+        for (int i = 0; i < XR; ++i) xr[i] = load16(xb, (xat[i] + c * 256 + 16 * xp) | past);
+    };
+    auto put_x = [&](int c) __attribute__((always_inline)) {
+        constexpr uint32_t one = 0x3f803f80u;
+#pragma unroll
+        for (int i = 0; i < XR; ++i) {
+            const int r = (threadIdx.x >> 4) + 4 * kTileWaves * i;
+            const uint4 v = pair_order(xr[i]);
+            xs.part[c & 1][r][xp ^ (r & 15)] = v;
+            float sum = dot2(v.x, one, dot2(v.y, one, dot2(v.z, one, dot2(v.w, one, 0.0f))));
+            // over a group's G / 8 threads
+            sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xF, 0xF, true));
+            sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xF, 0xF, true));
+            if constexpr (G >= 64) sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x141, 0xF, 0xF, true));
+            if constexpr (G >= 128) sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x140, 0xF, 0xF, true));
+            if (xp % (G / 8) == 0) xs.sum[c & 1][xp / (G / 8)][r] = split_sum(sum);
+        }
+    };
+
+    int row0[NT];
+    const int wn = tile.nt * kTileWaves + wave;      // this wave's columns
+#pragma unroll
+    for (int t = 0; t < NT; ++t) row0[t] = (t < NC ? 0 : N) + min((wn * NC + t % NC) * 16, N - 16);
+    const WBuf wb = w_buf(GATE_UP ? a.w13 : a.w2, tile.e, GATE_UP ? 2 * N : N, K, G);
+    const bool live = wn * NC * 16 < N;
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+    Codes<G, NT, 1> w;
+    uint32_t sz[NT][4];
+    const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
+    const Conv cv = conv();
+    if (threadIdx.x < kTileRows) xs.none[threadIdx.x] = make_uint4(0, 0, 0, 0);
+    load_all(w, where_of<G>(wb, row0, 0, K, live), K);
+    load_x(0);
+    put_x(0);
+    load_x(1);
+    __syncthreads();
+    auto chunk = [&](int c, auto U_) __attribute__((always_inline)) {
+        constexpr int u = decltype(U_)::value;           // which of the pair
+        if (u * GC % 4 == 0) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const uint32_t v = (w.s[u * GC / 4][t] << 16) | (w.z[u * GC / 4][t] + z8);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sz[t][j] = __builtin_amdgcn_ds_bpermute(4 * (4 * m + j), (int)v);
+            }
+            load_scales(w, where_of<G>(wb, row0, c + 2 - u, K, live), u * GC / 4);
+        }
+        if (u == 0) {
+            put_pair(turn[wave], w, 0);
+            load_pair(w, where_of<G>(wb, row0, c + 2, K, live), 0, K);
+        }
+        if (c < chunks) {
+            uint4 q[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                q[t] = turn[wave].part[t][m][(4 * u + g) ^ (m >> 1)];
+                if constexpr (G != 128) q[t] = exchange4(q[t]);
+            }
+#pragma unroll
+            for (int b = 0; b < GC; ++b) {
+                const int gi = (u * GC + b) % 4;
+                f32x4 p[MT][NT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint4 X = (g == 0 ? xs.sum[c & 1][b] : xs.none)[16 * mt + m];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) p[mt][t] = minus_zeros(X, sz[t][gi] & 0xffu);
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int j = b * PER + i;
+                    bf16x8 wf[NT];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) wf[t] = as_bf16x8(codes_to_bf16(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, cv));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const bf16x8 xf = as_bf16x8(xs.part[c & 1][16 * mt + m][(G == 128 ? 4 * g + i : 4 * j + g) ^ m]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            p[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, wf[t], p[mt][t], 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float sc = bf16_hi(sz[t][gi]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[mt][t][r] = fmaf(sc, p[mt][t][r], acc[mt][t][r]);
+                }
+
+            }
+        }
+        put_x(c + 1);
+        load_x(c + 2);
+        __syncthreads();
+    };
+    for (int c = 0; c < chunks; c += 2) {
+        chunk(c, std::integral_constant<int, 0>{});
+        chunk(c + 1, std::integral_constant<int, 1>{});
+    }
+
+    // the tile leaves through LDS as rows (the loop's last barrier has freed it)
+    constexpr int COLS = 16 * NC * kTileWaves, PITCH = COLS + 8;
+    static_assert(kTileRows * PITCH * 2 <= sizeof(XStage) + kTileWaves * sizeof(Turn<NT>), "the tile fits");
+    uint16_t* out = reinterpret_cast<uint16_t*>(smem);
+    const float L = a.glu.limit;
+    auto stage = [&](auto&& value) __attribute__((always_inline)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int t = 0; t < NC; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    out[(16 * mt + 4 * g + r) * PITCH + (wave * NC + t) * 16 + m] = (uint16_t)f32_to_bf16_bits(value(mt, t, r));
+    };
+    if constexpr (GATE_UP) {
+        with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) {
+            stage([&](int mt, int t, int r) __attribute__((always_inline)) {
+                return act_of<decltype(A)::value, true>(limit_g(acc[mt][t][r], L)) * limit_u(acc[mt][t + NC][r], L);
+            });
+        });
+    } else {
+        stage([&](int mt, int t, int r) __attribute__((always_inline)) { return acc[mt][t][r]; });
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < tile.rows_valid * (COLS / 8); i += 64 * kTileWaves) {
+        const int r = i / (COLS / 8), c = 8 * (i % (COLS / 8)), col = tile.nt * COLS + c;
+        if (col < N)
+            *reinterpret_cast<uint4*>((GATE_UP ? h : y) + (tile.row0 + r) * N + col) = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
+    }
 }
 
-// out[t] = sum_j topk_w_j (h_j W2[e_j]^T) of 16 columns of token blockIdx.y: the
-// slots' K ranges are one long sum, each slot's scales times its weight
-template <int G>
-__global__ __launch_bounds__(64 * kW) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h)
-{
-    __shared__ float red[kW][1][256];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int t = blockIdx.y, m = lane & 15;
-    const int chunks = (a.f + 127) / 128;
-    f32x4 acc[1] = {};
-    for (int i = wave; i < a.k * chunks; i += kW) {
-        const int j = i / chunks;
-        const int64_t p = (int64_t)t * a.k + j;
-        const int e = a.topk_idx[p], dst = a.dst_row[p];
-        if (e < 0 || e >= a.E || dst < 0 || dst >= a.T * a.k) continue;
-        const uint16_t* x = m == 0 ? h + p * a.f : nullptr;
-        const WRow w[1] = {w_row(a.w2, (int64_t)e * a.d + blockIdx.x * 16 + m, a.f, G)};
-        chunk_product<G, 1>(acc, x, w, i - j * chunks, a.f, a.topk_w[p]);
+// ---------------------------------------------------------------- one row at a time
+// A single row of x has no use for a matrix instruction.  Here a lane multiplies the codes where they arrive: eight
+// neighbouring lanes have 256 consecutive codes of a row, 32 each, the same 32 of every row that passes, so that the
+// lane's x stay in registers; a wave instruction is eight rows x 128 bytes.  Two products an instruction
+// (v_dot2c_f32_bf16) on the same 16 + q operands.
+// 32 consecutive x of a lane in the codes' order, and their sum
+struct X32 {
+    uint4 v[4];
+    float sum;
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, uint32_t at)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load16(x, at + 16 * i);
     }
-    put_acc(red, acc);
-    if (threadIdx.x < 16)
-        a.out[(int64_t)t * a.d + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(wave_sum(red, 0, threadIdx.x));
+    __device__ __forceinline__ void order()
+    {
+        float a = 0.0f, b = 0.0f;
+        constexpr uint32_t one = 0x3f803f80u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = pair_order(v[i]);
+            a = dot2(v[i].x, one, a);
+            b = dot2(v[i].y, one, b);
+            a = dot2(v[i].z, one, a);
+            b = dot2(v[i].w, one, b);
+        }
+        sum = a + b;
+    }
+};
+
+// sum x (q - zero) over a lane's 32 codes
+__device__ __forceinline__ float dot32(uint4 q, const X32& x, float zero16, Conv cv)
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 c = codes_to_bf16(w[i], cv);
+        a = dot2(c.x, x.v[i].x, a);
+        b = dot2(c.y, x.v[i].y, b);
+        a = dot2(c.z, x.v[i].z, a);
+        b = dot2(c.w, x.v[i].w, b);
+    }
+    return fmaf(-zero16, x.sum, a + b);
 }
+
+// one load of a lane: its 32 codes of a row, their scale and zero point
+struct Q32 {
+    uint4 q;
+    uint32_t s, z;
+
+    __device__ __forceinline__ void load(const WBuf& w, int row, int k0, int K, int G, uint32_t past)
+    {
+        const uint32_t at = row * (K / G) + k0 / G;
+        q = load16(w.codes, (uint32_t)(row * (K / 2) + k0 / 2) | past);
+        s = __builtin_amdgcn_raw_buffer_load_b16(w.scales, (int)(at * 2 | past), 0, 0);
+        z = __builtin_amdgcn_raw_buffer_load_b8(w.zeros, (int)(at | past), 0, 0);
+    }
+    __device__ __forceinline__ float times(const X32& x, uint32_t z8, Conv cv) const
+    {
+        return bf16_lo(s) * dot32(q, x, (float)(16 + z8 + z), cv);
+    }
+};
+
+// sum over eight neighbouring lanes, in each of them
+__device__ __forceinline__ float sum8(float v)
+{
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, true));   // 7 - lane
+    return v;
+}
+
+// the expert of slot p, or -1 for a slot that adds nothing (flagged if it is out of range)
+__device__ __forceinline__ int expert_of(const Int4Ffn& a, int64_t p, bool flag)
+{
+    const int e = a.topk_idx[p], dst = a.dst_row[p];
+    const bool bad = e < 0 || e >= a.E || dst >= a.T * a.k;
+    if (bad && flag && a.dev_err && threadIdx.x == 0) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
+    return bad || dst < 0 ? -1 : e;
+}
+
+// h = a(g') u' of 16 columns for slot blockIdx.y: eight waves share K in slices of 256, two at a time
+template <int G>
+__global__ __launch_bounds__(64 * kWaves) void int4_gate_up_token_kernel(Int4Ffn a, uint16_t* __restrict__ h)
+{
+    constexpr int U = 2;
+    __shared__ float red[kWaves][32];
+    const int64_t p = blockIdx.y;
+    const int e = expert_of(a, p, blockIdx.x == 0);
+    if (e < 0) return;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int K = a.d, slices = (K + 255) / 256;
+    const WBuf w = w_buf(a.w13, e, 2 * a.f, K, G);
+    const auto xb = buf_of(a.x, (int64_t)a.T * K * 2);
+    const uint32_t xat = (uint32_t)(p / a.k * K * 2), z8 = a.w13.zeros ? 0 : 8;
+    const int row = blockIdx.x * 16 + (lane >> 3);
+    const Conv cv = conv();
+    float acc[4] = {};
+    for (int s0 = wave * U; s0 < slices; s0 += kWaves * U) {
+        Q32 q[U][4];
+        X32 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k0 = (s0 + u) * 256 + 32 * (lane & 7);
+            const uint32_t past = k0 < K ? 0 : kPast;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[u][i].load(w, row + (i & 1) * 8 + (i >> 1) * a.f, k0, K, G, past);
+            x[u].load(xb, (xat + k0 * 2) | past);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u].order();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] += q[u][i].times(x[u], z8, cv);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float v = sum8(acc[i]);
+        if ((lane & 7) == 0) red[wave][i * 8 + (lane >> 3)] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 16) return;
+    float g = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        g += red[i][threadIdx.x];
+        u += red[i][16 + threadIdx.x];
+    }
+    g = limit_g(g, a.glu.limit);
+    u = limit_u(u, a.glu.limit);
+    float v = 0.0f;
+    with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) { v = act_of<decltype(A)::value, true>(g) * u; });
+    h[p * a.f + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+// out[t] = sum_j topk_w_j (h_j W2[e_j]^T) of 16 columns of token blockIdx.y: the slices of all its slots are shared by
+// eight waves, three at a time, a slice's sum times its slot's weight, so that one sum over the waves is the combine
+template <int G>
+__global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h)
+{
+    constexpr int U = 3;
+    __shared__ float red[kWaves][16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t t = blockIdx.y;
+    const int K = a.f, slices = (K + 255) / 256, items = a.k * slices;
+    const auto hb = buf_of(h, (int64_t)a.T * a.k * K * 2);
+    const uint32_t z8 = a.w2.zeros ? 0 : 8;
+    const int row = blockIdx.x * 16 + (lane >> 3);
+    const Conv cv = conv();
+    float acc[2] = {};
+    for (int i0 = wave; i0 < items; i0 += kWaves * U) {
+        Q32 q[U][2];
+        X32 x[U];
+        float c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = min(i0 + u * kWaves, items - 1);
+            const int j = i / slices;
+            const int64_t p = t * a.k + j;
+            const int e = expert_of(a, p, false);
+            const bool on = e >= 0 && i0 + u * kWaves < items;
+            c[u] = on ? a.topk_w[p] : 0.0f;
+            const int k0 = (i - j * slices) * 256 + 32 * (lane & 7);
+            const uint32_t past = on && k0 < K ? 0 : kPast;
+            const WBuf w = w_buf(a.w2, max(e, 0), a.d, K, G);
+            q[u][0].load(w, row, k0, K, G, past);
+            q[u][1].load(w, row + 8, k0, K, G, past);
+            x[u].load(hb, (uint32_t)((p * K + k0) * 2) | past);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            x[u].order();
+            acc[0] = fmaf(c[u], q[u][0].times(x[u], z8, cv), acc[0]);
+            acc[1] = fmaf(c[u], q[u][1].times(x[u], z8, cv), acc[1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float v = sum8(acc[i]);
+        if ((lane & 7) == 0) red[wave][i * 8 + (lane >> 3)] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 16) return;
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += red[i][threadIdx.x];
+    a.out[t * a.d + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+// CUs of the current device
+int cu_count()
+{
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1)
+        n = 256;
+    return n;
+}
+
+template <int G, class GateUp>
+void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, uint16_t* y, hipStream_t s)
+{
+    constexpr bool UP = GateUp::value;
+    const int N = UP ? a.f : a.d, K = UP ? a.d : a.f, chunks = (K + 127) / 128;
+    const int64_t R = (int64_t)a.T * a.k;
+    // tiles of up to 16 rows: no more than the rows, nor than the full ones and one of each expert
+    const int64_t mt = R < R / 16 + a.E ? R : R / 16 + a.E;
+    auto go = [&](auto P_, auto NC_, int waves_per_cu) {
+        constexpr int P = decltype(P_)::value, NC = decltype(NC_)::value, NT = UP ? 2 * NC : NC;
+        const int need = (chunks + 2 * P - 1) / (2 * P), W = need < kWaves ? need : kWaves;
+        const size_t lds = W * (sizeof(Turn<NT>) + 2 * NT * 1024);
+        const int64_t fit = (int64_t)(156 << 10) / (lds + 4 * kMaxExperts + 256), per_cu = fit < waves_per_cu / W ? fit : waves_per_cu / W;
+        const int64_t tiles = mt * ((N + 16 * NC - 1) / (16 * NC)), cap = cu_count() * (per_cu < 1 ? 1 : per_cu);
+        hipLaunchKernelGGL((int4_rows_kernel<G, P, NC, UP>), dim3((unsigned)(tiles < cap ? tiles : cap)), dim3(64 * W), lds, s,
+                           a, h, y);
+    };
+    using std::integral_constant;
+    if (chunks > 2 * kWaves) {
+        go(integral_constant<int, 2>{}, integral_constant<int, UP ? 1 : 2>{}, 8);
+    } else {
+        go(integral_constant<int, 1>{}, integral_constant<int, UP ? 1 : 3>{}, 12);
+    }
+}
+
+template <int G, class GateUp>
+void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, uint16_t* y, hipStream_t s)
+{
+    constexpr bool UP = GateUp::value;
+    constexpr int COLS = (UP ? 16 : 32) * kTileWaves;
+    const int64_t R = (int64_t)a.T * a.k, mt = R / kTileRows + (R < a.E ? R : a.E), ntn = ((UP ? a.f : a.d) + COLS - 1) / COLS;
+    hipLaunchKernelGGL((int4_tile_kernel<G, UP>), dim3((unsigned)((mt * ntn + 7) / 8 * 8)), dim3(64 * kTileWaves),
+                       sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, h, y);
+}
+
+constexpr int kTokenSlots = 32, kTileMinRows = 32;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -387,22 +1047,27 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     const int64_t R = (int64_t)a.T * a.k;
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws);
     uint16_t* y = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
-    const dim3 blk(64 * kW);
-    if (a.T == 1) {
+    hipError_t e;
+    if (R <= kTokenSlots && 2 * R <= 3 * a.E) {
         return with_group(a.group, [&](auto g) {
             constexpr int G = decltype(g)::value;
-            hipLaunchKernelGGL((int4_gate_up_kernel<G, true>), dim3(a.f / 16, (unsigned)R), blk, 0, s, a, h);
-            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), blk, 0, s, a, h);
+            hipLaunchKernelGGL((int4_gate_up_token_kernel<G>), dim3(a.f / 16, (unsigned)R), dim3(64 * kWaves), 0, s, a, h);
+            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), dim3(64 * kWaves), 0, s, a, h);
         });
     }
-    // tiles of up to 16 rows: no more than the rows, nor than the full ones and one of each expert
-    const int64_t mt = R < R / 16 + a.E ? R : R / 16 + a.E;
-    auto grid = [&](int ntn) { return dim3((unsigned)((mt * ntn + 7) / 8 * 8)); };
-    const hipError_t e = with_group(a.group, [&](auto g) {
-        constexpr int G = decltype(g)::value;
-        hipLaunchKernelGGL((int4_gate_up_kernel<G, false>), grid(a.f / 16), blk, 0, s, a, h);
-        hipLaunchKernelGGL((int4_down_kernel<G>), grid(a.d / 32), blk, 0, s, a, h, y);
-    });
+    using Up = std::true_type;
+    using Down = std::false_type;
+    if (R >= (int64_t)kTileMinRows * a.E) {
+        e = with_group(a.group, [&](auto g) {
+            launch_tile<decltype(g)::value>(a, Up{}, h, y, s);
+            launch_tile<decltype(g)::value>(a, Down{}, h, y, s);
+        });
+    } else {
+        e = with_group(a.group, [&](auto g) {
+            launch_rows<decltype(g)::value>(a, Up{}, h, y, s);
+            launch_rows<decltype(g)::value>(a, Down{}, h, y, s);
+        });
+    }
     if (e != hipSuccess) return e;
     return launch_combine(MOE_BF16, y, a.dst_row, a.topk_w, a.T, a.k, a.d, R, a.out, a.dev_err, s);
 }

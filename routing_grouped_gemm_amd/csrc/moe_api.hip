@@ -534,6 +534,8 @@ int moe_int4_ffn(const moe_glu* glu, const void* x, int T, int k, const int32_t*
     if (T < 0 || k < 1 || k > kMaxTopK || E < 1 || E > kMaxExperts || (int64_t)T * k >= kMaxRows || d < 1 || f < 1 ||
         d > kMaxMx4Width || f > kMaxMx4Width)
         return MOE_EINVAL;
+    // byte offsets into x, into h and into one expert's matrices stay below 2^31
+    if ((int64_t)T * d >= kMaxRows / 2 || (int64_t)T * k * f >= kMaxRows / 2 || (int64_t)d * f >= kMaxRows) return MOE_EINVAL;
     if (group != 32 && group != 64 && group != 128) return MOE_EUNSUPPORTED;
     if (d % group || f % group) return MOE_EALIGN;
     if (!group_off || !w13->codes || !w13->scales || !w2->codes || !w2->scales) return MOE_EINVAL;

@@ -198,6 +198,28 @@ def test_ffn(moe, T, E, d, f, k, group, zeros):
     assert int(c.err) == 0
 
 
+@pytest.mark.parametrize("T,E,d,f", [(1, 2, 4352, 64), (10, 2, 4352, 4480), (40, 1, 4352, 4224), (7, 200, 64, 64),
+                                     (300, 1024, 128, 32)])
+def test_long_rows_and_many_experts(moe, T, E, d, f):
+    """Sums longer than a workgroup's share of one step, and more experts than lanes."""
+    c = Ffn(moe, T, E, d, f, 1, 32, True, seed=T)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("T", [1, 20, 70])
+def test_a_nan_scale_keeps_to_its_column(moe, T, group):
+    """Rows that end inside a chunk of 128 codes: what follows is the next row's first group, whose NaN scale makes that
+    row's column NaN and no other."""
+    c = Ffn(moe, T, 2, 160 if group == 32 else 192, 160 if group == 32 else 192, 2, group, False, seed=6)
+    clean = c.run()
+    for e in range(2):
+        c.w[1][1][e, 77, 0] = float("nan")
+    out = c.run()
+    keep = torch.arange(c.d) != 77
+    assert torch.equal(out[:, keep], clean[:, keep]) and bool(torch.isnan(out[:, 77]).all())
+
+
 @pytest.mark.parametrize("T", [1, 2, 90])
 @pytest.mark.parametrize("act", pl.ACTS)
 def test_gates(moe, act, T):

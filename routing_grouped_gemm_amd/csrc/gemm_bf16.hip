@@ -412,9 +412,14 @@ struct ColHalfLoaderMN {
 // after the last read of the K-step two back, at an earlier tick.  B halves
 // are rows 0..127 / 128..255 of a K-major tile and k-rows 0..31 / 32..63 of
 // an MN-major one; both groups read all of B.
-template <bool A_MN, bool B_MN>
+// ahead() runs when the first loads are out, before they are waited for; it
+// must issue no vector memory operations.
+struct Nothing {
+    __device__ __forceinline__ void operator()() const {}
+};
+template <bool A_MN, bool B_MN, class F = Nothing>
 __device__ __forceinline__ void mainloop_pp(const TileSrc& sa, const TileSrc& sb, f32x16 (&acc)[4][2],
-                                            uint16_t* smem)
+                                            uint16_t* smem, F&& ahead = {})
 {
     constexpr int BM = 256, BK = 64, MI = 4, NJ = 2;
     constexpr int STAGE = (BM + BN) * BK;   // elements per stage
@@ -446,6 +451,7 @@ __device__ __forceinline__ void mainloop_pp(const TileSrc& sa, const TileSrc& sb
         ha.issue(STAGE * 2, 1);
         hb.issue(STAGE * 2, 1);
     }
+    ahead();
     if (nk > 1) wait_vmcnt<8>();
     else wait_vmcnt<0>();
     __syncthreads();
@@ -656,6 +662,11 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW) void gemm_grouped_m_kernel(MParams p)
         sb.rows1 = max(min(128, p.N - n0 - 128), 0);
     }
 
+    PhiloxKey key{};
+    if constexpr (EPI == EPI_GLU_FWD || EPI == EPI_GLU_BWD) {
+        if (p.glu.drop.thr) key = philox_key(p.glu.drop.rng);
+    }
+
     if constexpr (BM == 256) {
         // the last M-tile of an expert with at most 64 (128) rows: a 64-row
         // (128-row) tile, with a quarter (half) of the MFMAs and of the A
@@ -666,9 +677,11 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW) void gemm_grouped_m_kernel(MParams p)
             st.p1 = st.p0 + (int64_t)(BMS / 2) * p.lda;
             st.rows0 = min(rows_valid, BMS / 2);
             st.rows1 = max(rows_valid - BMS / 2, 0);
+            DropBits<BMS, EPI, WL<NW>::NT> drop;
+            drop.make(p, key, row0, nt);
             f32x16 acc_s[BMS / 64][WL<NW>::NJ];
             mainloop<BMS, BK, KAL ? tail_stages<BMS>() : NS, false, B_MN, NW, KAL>(st, sb, acc_s, smem);
-            epilogue_m<BMS, EPI, NW>(acc_s, p, row0, rows_valid, nt, reinterpret_cast<uint8_t*>(smem));
+            epilogue_m<BMS, EPI, NW>(acc_s, p, row0, rows_valid, nt, reinterpret_cast<uint8_t*>(smem), drop);
         };
         if (rows_valid <= 64) {
             small(std::integral_constant<int, 64>{});
@@ -680,11 +693,15 @@ __global__ MOE_GEMM_KERNEL_ATTRS_NW(NW) void gemm_grouped_m_kernel(MParams p)
         }
     }
     f32x16 acc[BM / 64][WL<NW>::NJ];
-    if constexpr (KAL && NW == 8 && BM == 256 && BK == 64)
-        mainloop_pp<false, B_MN>(sa, sb, acc, smem);
-    else
+    DropBits<BM, EPI, WL<NW>::NT> drop;
+    auto make_drop = [&]() __attribute__((always_inline)) { drop.make(p, key, row0, nt); };
+    if constexpr (KAL && NW == 8 && BM == 256 && BK == 64) {
+        mainloop_pp<false, B_MN>(sa, sb, acc, smem, make_drop);
+    } else {
+        make_drop();
         mainloop<BM, BK, NS, false, B_MN, NW, KAL>(sa, sb, acc, smem);
-    epilogue_m<BM, EPI, NW>(acc, p, row0, rows_valid, nt, reinterpret_cast<uint8_t*>(smem));
+    }
+    epilogue_m<BM, EPI, NW>(acc, p, row0, rows_valid, nt, reinterpret_cast<uint8_t*>(smem), drop);
 }
 
 

@@ -419,11 +419,42 @@ __device__ __forceinline__ void stage_acc(const f32x16 (&acc)[BM / 64][WL<NW>::N
                                      acc[i][j][4 * g + 3]));
 }
 
+// The dropout decisions of a GLU tile's h, for the chunks of eight columns that this thread stores: made before the
+// tile's products, while its first loads are on their way (dgrad-down of 32768 rows, 16 experts, d 4096, f 1536: 9 us
+// of 504, in the epilogue 23), and carried through the main loop in two to four registers.  Chunk i is row
+// tid / 16 + i NT / 16, columns 8 (tid % 16) of the tile (backward: of each 128-column half, half after half).
+template <int BM, int EPI, int NT>
+struct DropBits {
+    static constexpr int HALF = BM * 16 / NT;                          // chunks of 128 columns
+    static constexpr int N = EPI == EPI_GLU_FWD ? HALF : EPI == EPI_GLU_BWD ? 2 * HALF : 0;
+    uint32_t w[N ? (N + 3) / 4 : 1];
+
+    __device__ __forceinline__ void make(const MParams& p, PhiloxKey key, int64_t row0, int nt)
+    {
+        if constexpr (N > 0) {
+            const uint32_t thr = p.glu.drop.thr;
+            if (!thr) return;
+            const int tid = threadIdx.x;
+            const uint64_t first =
+                (uint64_t)((row0 + (tid >> 4)) * p.f + nt * (EPI == EPI_GLU_FWD ? 128 : 256) + 8 * (tid & 15)) >> 3;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t on = (uint32_t)(i % HALF) * (NT / 16) * (uint32_t)(p.f >> 3) + 16 * (i / HALF);
+                w[i / 4] = push_bits(i % 4 ? w[i / 4] : 0, philox(key, first + on), thr);
+                if (i == N - 1 && N % 4) w[i / 4] <<= 8 * (4 - N % 4);
+            }
+        }
+    }
+    // chunk i of v
+    __device__ __forceinline__ uint4 mask(uint4 v, int i) const { return mask_vec(v, w[i / 4], i % 4); }
+};
+
 // MXQ: the SwiGLU epilogues also write the row-wise MXFP8 copy of their
 // bf16 output (h or dgu) to p.Mq / p.Ms
 template <int BM, int EPI, int NW = 4, bool MXQ = false>
 __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::NJ], const MParams& p,
-                                           int64_t row0, int rows_valid, int nt, uint8_t* lds)
+                                           int64_t row0, int rows_valid, int nt, uint8_t* lds,
+                                           const DropBits<BM, EPI, WL<NW>::NT>& drop = {})
 {
     constexpr int MI = BM / 64;
     constexpr int NJ = WL<NW>::NJ;
@@ -462,24 +493,20 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
                     }
         };
         if constexpr (EPI == EPI_GLU_FWD) {
-            // the kept elements' factor before the rounding; the mask after it, where a lane has the eight
-            // consecutive elements of one generator block
-            const float L = p.glu.limit, scale = p.glu.drop.scale;
+            // the kept elements' factor before the rounding; the mask after it, on whole chunks
+            const float scale = p.glu.drop.scale;
             const uint32_t thr = p.glu.drop.thr;
-            with_act(p.glu.act, [&](auto A) __attribute__((always_inline)) {
+            with_glu(p.glu, [&](auto A, auto L) __attribute__((always_inline)) {
                 make_h([&](float g, float u) __attribute__((always_inline)) {
-                    return act_of<decltype(A)::value, true>(limit_g(g, L)) * limit_u(u, L) * scale;
+                    return act_of<decltype(A)::value, true>(L.g(g)) * L.u(u) * scale;
                 });
             });
-            PhiloxKey key{};
-            if (thr) key = philox_key(p.glu.drop.rng);
+            int i = 0;
             stage_flush<BM, 16, NT>(lds, [&](int r, int c, uint4 v) __attribute__((always_inline)) {
                 const int n = n0 + 8 * c;
-                if (r < rows_valid && n < p.f) {
-                    const int64_t at = (row0 + r) * p.f + n;
-                    if (thr) v = mask_vec(v, philox(key, (uint64_t)at >> 3), thr);
-                    *reinterpret_cast<uint4*>(p.H + at) = v;
-                }
+                if (thr) v = drop.mask(v, i);
+                ++i;
+                if (r < rows_valid && n < p.f) *reinterpret_cast<uint4*>(p.H + (row0 + r) * p.f + n) = v;
             });
             return;
         }
@@ -551,14 +578,14 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
                         }
             };
             if constexpr (EPI == EPI_GLU_BWD) {
-                const float L = p.glu.limit, scale = p.glu.drop.scale;
-                with_act(p.glu.act, [&](auto A) __attribute__((always_inline)) {
+                const float scale = p.glu.drop.scale;
+                with_glu(p.glu, [&](auto A, auto L) __attribute__((always_inline)) {
                     make_dgu([&](float dh, float gv, float uv, float& dg, float& du) __attribute__((always_inline)) {
                         float a, da;
-                        act_and_slope<decltype(A)::value, true>(limit_g(gv, L), a, da);
+                        act_and_slope<decltype(A)::value, true>(L.g(gv), a, da);
                         dh *= scale;
-                        dg = gv > L ? 0.0f : dh * limit_u(uv, L) * da;
-                        du = uv > L || uv < -L ? 0.0f : dh * a;
+                        dg = L.slope_g(gv, dh * L.u(uv) * da);
+                        du = L.slope_u(uv, dh * a);
                     });
                 });
             } else {
@@ -584,18 +611,15 @@ __device__ __forceinline__ void epilogue_m(const f32x16 (&acc)[BM / 64][WL<NW>::
                 // a thread's chunks are the same of dg and du: dropped elements of h have neither
                 static_assert(BM * 16 % NT == 0, "chunk i + NQ / 2 is the u half of chunk i");
                 const uint32_t thr = p.glu.drop.thr;
-                PhiloxKey key{};
-                if (thr) key = philox_key(p.glu.drop.rng);
 #pragma unroll
                 for (int i = 0; i < NQ / 2; ++i) {
                     const int q = (int)threadIdx.x + i * NT;
                     const int r = q >> 4, n = nc + 8 * (q & 15);
+                    if (thr) {
+                        v[i] = drop.mask(v[i], ch * (NQ / 2) + i);
+                        v[i + NQ / 2] = drop.mask(v[i + NQ / 2], ch * (NQ / 2) + i);
+                    }
                     if (r < rows_valid && n < p.N) {
-                        if (thr) {
-                            const uint4 w = philox(key, (uint64_t)((row0 + r) * p.f + n) >> 3);
-                            v[i] = mask_vec(v[i], w, thr);
-                            v[i + NQ / 2] = mask_vec(v[i + NQ / 2], w, thr);
-                        }
                         *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + n) = v[i];
                         *reinterpret_cast<uint4*>(p.C + (row0 + r) * p.ldc + p.f + n) = v[i + NQ / 2];
                     }

@@ -15,6 +15,17 @@ namespace moe {
 __device__ __forceinline__ float limit_g(float g, float L) { return g > L ? L : g; }
 __device__ __forceinline__ float limit_u(float u, float L) { return u > L ? L : (u < -L ? -L : u); }
 
+// the same, or nothing where it is known that there is no limit (LIM false): the comparisons are a third of relu's
+// backward epilogue
+template <bool LIM>
+struct Limit {
+    float L;
+    __device__ __forceinline__ float g(float v) const { return LIM ? limit_g(v, L) : v; }
+    __device__ __forceinline__ float u(float v) const { return LIM ? limit_u(v, L) : v; }
+    __device__ __forceinline__ float slope_g(float v, float d) const { return LIM && v > L ? 0.0f : d; }
+    __device__ __forceinline__ float slope_u(float v, float d) const { return LIM && (v > L || v < -L) ? 0.0f : d; }
+};
+
 // 1 / (1 + exp(-z)).  FAST: the hardware's exp2 and reciprocal (bf16 results:
 // their 2^-22 is far below the rounding), else the library's.
 template <bool FAST>
@@ -52,11 +63,12 @@ __device__ __forceinline__ void normal_of(float g, float& Phi, float& ex)
 
 // the tanh form's s = sigmoid(z) with z = 2 sqrt(2/pi) (g + 0.044715 g^3), and
 // dz/dg.  Past |g| = 12 s is 0 or 1 in fp32 (z = 142), so g^3 is formed from
-// g held there: no infinity meets a zero.
+// g held there: no infinity meets a zero.  (A NaN is lost here and kept by
+// the products with g itself.)
 template <bool FAST>
 __device__ __forceinline__ float gelu_tanh_sigmoid(float g, float& dz)
 {
-    const float c = g > 12.0f ? 12.0f : (g < -12.0f ? -12.0f : g);
+    const float c = __builtin_amdgcn_fmed3f(g, -12.0f, 12.0f);
     const float c2 = c * c;
     dz = fmaf(0.2140644481f, c2, 1.5957691216f);               // 2 sqrt(2/pi) (1 + 3 * 0.044715 g^2)
     return sigmoid_of<FAST>(c * fmaf(0.0713548160f, c2, 1.5957691216f));
@@ -113,6 +125,16 @@ __device__ __forceinline__ void with_act(int act, F&& f)
     case MOE_ACT_GELU_TANH: f(std::integral_constant<int, MOE_ACT_GELU_TANH>{}); break;
     default: f(std::integral_constant<int, MOE_ACT_RELU>{}); break;
     }
+}
+
+// f(integral_constant<int, act>, Limit)
+template <class F>
+__device__ __forceinline__ void with_glu(const GluSpec& glu, F&& f)
+{
+    with_act(glu.act, [&](auto A) __attribute__((always_inline)) {
+        if (glu.limit < __builtin_inff()) f(A, Limit<true>{glu.limit});
+        else f(A, Limit<false>{glu.limit});
+    });
 }
 
 }  // namespace moe

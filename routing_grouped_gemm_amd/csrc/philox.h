@@ -45,15 +45,31 @@ __device__ __forceinline__ uint4 philox(PhiloxKey k, uint64_t block)
 __device__ __forceinline__ bool keep_lo(uint32_t r, uint32_t thr) { return (r & 0xffffu) >= thr; }
 __device__ __forceinline__ bool keep_hi(uint32_t r, uint32_t thr) { return (r >> 16) >= thr; }
 
-// two bf16 of a word, dropped ones zero
-__device__ __forceinline__ uint32_t mask_pair(uint32_t v, uint32_t r, uint32_t thr)
+// The decisions of four blocks as bits: element j of block i is dropped where bit 31 - (8 i + j) is set.
+// push_bits() takes the blocks in order.
+__device__ __forceinline__ uint32_t push_bits(uint32_t bits, uint4 r, uint32_t thr)
 {
-    return (keep_lo(r, thr) ? v & 0xffffu : 0u) | (keep_hi(r, thr) ? v & 0xffff0000u : 0u);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        // the sign of the difference shifted in
+        bits = __builtin_amdgcn_alignbit(bits, (w[q] & 0xffffu) - thr, 31);
+        bits = __builtin_amdgcn_alignbit(bits, (w[q] >> 16) - thr, 31);
+    }
+    return bits;
 }
-__device__ __forceinline__ uint4 mask_vec(uint4 v, uint4 r, uint32_t thr)
+
+// eight bf16 with the dropped ones of block i zero
+__device__ __forceinline__ uint4 mask_vec(uint4 v, uint32_t bits, int i)
 {
-    return make_uint4(mask_pair(v.x, r.x, thr), mask_pair(v.y, r.y, thr), mask_pair(v.z, r.z, thr),
-                      mask_pair(v.w, r.w, thr));
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = (uint32_t)((int32_t)(bits << (8 * i + 2 * q)) >> 31);
+        const uint32_t hi = (uint32_t)((int32_t)(bits << (8 * i + 2 * q + 1)) >> 31);
+        w[q] &= ~((lo & 0xffffu) | (hi & 0xffff0000u));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace moe

@@ -4,6 +4,9 @@
 // 4 x 4 register micro-tile each, operands staged in LDS as [k][row].
 // For the SwiGLU forward a tile's 64 logical columns are 32 gate columns and
 // the same 32 up columns, so the epilogue (through LDS) forms h = silu(g) * u.
+// The activation-side stages take 32 x 32 tiles (2 x 2 a thread) where 64 x 64
+// ones would not fill the GPU twice.  Either way an element is one chain of fmaf
+// over ascending k, so the tile does not change a bit of the result.
 #include "glu.h"
 
 namespace moe {
@@ -48,11 +51,15 @@ __device__ __forceinline__ float drop_factor(const DropSpec& dr, PhiloxKey key, 
     return ((j & 1) ? keep_hi(r, dr.thr) : keep_lo(r, dr.thr)) ? dr.scale : 0.0f;
 }
 
-template <int EPI>
+// Bound by latency at the sizes this path is for, so the next K-step's operands are on their way in registers
+// while one is multiplied, and two LDS stages leave one barrier a K-step (512 rows of 8 experts, d = 128, f = 256:
+// 12 and 15 us for the two forward stages; 64 x 64 tiles with loads between the barriers took 24 and 38).
+template <int EPI, int T>
 __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
 {
-    __shared__ float sA[TK][TM + 4];
-    __shared__ float sB[TK][TN + 4];
+    constexpr int TM = T, TN = T, M = T / 16, TK = 1024 / T;
+    __shared__ __align__(16) float sA[2][TK][TM + 4];
+    __shared__ __align__(16) float sB[2][TK][TN + 4];
     __shared__ float sC[TM][TN + 1];
     __shared__ int s_pref[kMaxExperts + 1];
     __shared__ int s_part[256];
@@ -75,49 +82,64 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
 
     const int tid = threadIdx.x;
     const int tx = tid % 16, ty = tid / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += TK) {
-        for (int idx = tid; idx < TM * TK; idx += 256) {
-            const int r = idx / TK, kk = idx % TK;
-            const int k = k0 + kk;
-            sA[kk][r] = (r < rows_valid && k < p.K) ? p.A[(row0 + r) * p.lda + k] : 0.0f;
+    // one 16-byte piece of A and of B a thread and K-step: row (or column) r, k .. k + 3; a [K, N] weight: k-row kb,
+    // columns nb .. nb + 3.  K and N are multiples of 4, so a piece is inside or outside as a whole.
+    const int r = tid / (TK / 4), k = 4 * (tid % (TK / 4));
+    const int kb = tid / (TN / 4), nb = 4 * (tid % (TN / 4));
+    const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    int64_t brow = n0 + r;
+    bool b_ok = brow < p.N;
+    if (is_gate_up(EPI)) {
+        const int n = n0 + r % (TN / 2);
+        b_ok = n < p.f;
+        brow = r < TN / 2 ? n : p.f + n;
+    }
+    float4 a4, b4;
+    auto load = [&](int k0) {
+        a4 = r < rows_valid && k0 + k < p.K ? *reinterpret_cast<const float4*>(p.A + (row0 + r) * p.lda + k0 + k) : zero4;
+        if (p.b_mn)
+            b4 = k0 + kb < p.K && n0 + nb < p.N ? *reinterpret_cast<const float4*>(Be + (int64_t)(k0 + kb) * p.ldb + n0 + nb)
+                                                : zero4;
+        else
+            b4 = b_ok && k0 + k < p.K ? *reinterpret_cast<const float4*>(Be + brow * p.ldb + k0 + k) : zero4;
+    };
+    auto store = [&](int st) {
+        sA[st][k][r] = a4.x;
+        sA[st][k + 1][r] = a4.y;
+        sA[st][k + 2][r] = a4.z;
+        sA[st][k + 3][r] = a4.w;
+        if (p.b_mn) {
+            *reinterpret_cast<float4*>(&sB[st][kb][nb]) = b4;
+        } else {
+            sB[st][k][r] = b4.x;
+            sB[st][k + 1][r] = b4.y;
+            sB[st][k + 2][r] = b4.z;
+            sB[st][k + 3][r] = b4.w;
         }
-        for (int idx = tid; idx < TN * TK; idx += 256) {
-            const int c = idx / TK, kk = idx % TK;
-            const int k = k0 + kk;
-            int64_t brow;
-            bool ok;
-            if (is_gate_up(EPI)) {
-                const int n = n0 + (c % (TN / 2));
-                ok = n < p.f;
-                brow = c < TN / 2 ? n : p.f + n;
-            } else {
-                brow = n0 + c;
-                ok = brow < p.N;
-            }
-            float v = 0.0f;
-            if (ok && k < p.K) v = p.b_mn ? Be[(int64_t)k * p.ldb + brow] : Be[brow * p.ldb + k];
-            sB[kk][c] = v;
-        }
+    };
+    float acc[M][M] = {};
+    load(0);
+    for (int k0 = 0, st = 0; k0 < p.K; k0 += TK, st ^= 1) {
+        store(st);
         __syncthreads();
+        load(k0 + TK);
 #pragma unroll
         for (int kk = 0; kk < TK; ++kk) {
-            float a[4], b[4];
+            float a[M], b[M];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sA[kk][ty * 4 + i];
+            for (int i = 0; i < M; ++i) a[i] = sA[st][kk][ty * M + i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = sB[kk][tx * 4 + j];
+            for (int j = 0; j < M; ++j) b[j] = sB[st][kk][tx * M + j];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < M; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < M; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
         }
-        __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < M; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sC[ty * 4 + i][tx * 4 + j] = acc[i][j];
+        for (int j = 0; j < M; ++j) sC[ty * M + i][tx * M + j] = acc[i][j];
     __syncthreads();
     PhiloxKey key{};
     if ((EPI == EPI_GLU_FWD || EPI == EPI_GLU_BWD) && p.glu.drop.thr) key = philox_key(p.glu.drop.rng);
@@ -240,10 +262,21 @@ __global__ __launch_bounds__(256) void f32_grouped_k_kernel(F32K p)
 }
 
 template <int EPI>
-hipError_t launch_m(const F32M& p, int64_t n_rows, hipStream_t s)
+hipError_t launch_m(F32M p, int64_t n_rows, hipStream_t s)
 {
-    const int64_t grid = (n_rows / TM + p.E) * (int64_t)p.ntn;
-    if (grid > 0) hipLaunchKernelGGL((f32_grouped_m_kernel<EPI>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    const int cols = is_gate_up(EPI) ? 2 * p.N : p.N;
+    auto grid = [&](int T) {
+        p.ntn = (cols + T - 1) / T;
+        return (n_rows / T + p.E) * (int64_t)p.ntn;
+    };
+    // 64 x 64 tiles from two for each of 256 CUs on (an upper bound of their number is what is known here)
+    const int64_t big = grid(64);
+    if (big >= 512) {
+        hipLaunchKernelGGL((f32_grouped_m_kernel<EPI, 64>), dim3((unsigned)big), dim3(256), 0, s, p);
+    } else {
+        const int64_t n = grid(32);
+        if (n > 0) hipLaunchKernelGGL((f32_grouped_m_kernel<EPI, 32>), dim3((unsigned)n), dim3(256), 0, s, p);
+    }
     return hipGetLastError();
 }
 
@@ -279,7 +312,6 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const Glu
         p.b_mn = false;
         p.N = f;
         p.K = d;
-        p.ntn = (f + TN / 2 - 1) / (TN / 2);
         p.C = (float*)t.gu;
         p.ldc = 2 * f;
         p.H = (float*)t.h;
@@ -295,7 +327,6 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const Glu
         p.b_mn = false;
         p.N = d;
         p.K = f;
-        p.ntn = (d + TN - 1) / TN;
         p.C = (float*)t.y_perm;
         p.ldc = d;
         return launch_m<EPI_STORE>(p, g.n_rows, s);
@@ -308,7 +339,6 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const Glu
         p.b_mn = true;
         p.N = f;
         p.K = d;
-        p.ntn = (f + TN - 1) / TN;
         p.C = (float*)t.dgu;
         p.ldc = 2 * f;
         p.G = (const float*)t.gu;
@@ -324,7 +354,6 @@ hipError_t gemm_op_f32(int op, const moe_gemm_tensors& t, GroupSpec g, const Glu
         p.b_mn = true;
         p.N = d;
         p.K = 2 * f;
-        p.ntn = (d + TN - 1) / TN;
         p.C = (float*)t.dx_perm;
         p.ldc = d;
         return launch_m<EPI_STORE>(p, g.n_rows, s);

@@ -538,7 +538,7 @@ __device__ __forceinline__ int tile_prefix(const Int4Ffn& a, int ntn, int* s_pre
 //   else     y = h W2^T
 template <int G, int P, int NC, bool GATE_UP>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_rows_kernel(
-    Int4Ffn a, uint16_t* __restrict__ h, uint16_t* __restrict__ y)
+    Int4Ffn a, uint16_t* __restrict__ h, float* __restrict__ y)
 {
     constexpr int NT = GATE_UP ? 2 * NC : NC, U = 2 * P;
     const int W = blockDim.x >> 6;
@@ -628,7 +628,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
                 with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) { v = act_of<decltype(A)::value, true>(g) * u; });
                 h[(t.row0 + r) * a.f + col] = ok[buf][r] ? (uint16_t)f32_to_bf16_bits(v) : 0;
             } else {
-                y[(t.row0 + r) * a.d + col] = (uint16_t)f32_to_bf16_bits(v);
+                y[(t.row0 + r) * a.d + col] = v;
             }
         }
         buf ^= 1;
@@ -664,7 +664,7 @@ struct XStage {
 
 template <int G, bool GATE_UP>
 __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_tile_kernel(
-    Int4Ffn a, uint16_t* __restrict__ h, uint16_t* __restrict__ y)
+    Int4Ffn a, uint16_t* __restrict__ h, float* __restrict__ y)
 {
     constexpr int NT = 2, NC = GATE_UP ? 1 : 2, MT = kTileRows / 16, GC = 128 / G, PER = G / 32;
     constexpr int XR = kTileRows / (4 * kTileWaves);     // rows that a thread brings in
@@ -808,33 +808,37 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     }
 
     // the tile leaves through LDS as rows (the loop's last barrier has freed it)
-    constexpr int COLS = 16 * NC * kTileWaves, PITCH = COLS + 8;
-    static_assert(kTileRows * PITCH * 2 <= sizeof(XStage) + kTileWaves * sizeof(Turn<NT>), "the tile fits");
-    uint16_t* out = reinterpret_cast<uint16_t*>(smem);
-    const float L = a.glu.limit;
+    using Out = std::conditional_t<GATE_UP, uint16_t, float>;
+    constexpr int COLS = 16 * NC * kTileWaves, VEC = 16 / sizeof(Out), PITCH = COLS + VEC;
+    static_assert(kTileRows * PITCH * sizeof(Out) <= sizeof(XStage) + kTileWaves * sizeof(Turn<NT>), "the tile fits");
+    Out* out = reinterpret_cast<Out*>(smem);
     auto stage = [&](auto&& value) __attribute__((always_inline)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int t = 0; t < NC; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    out[(16 * mt + 4 * g + r) * PITCH + (wave * NC + t) * 16 + m] = (uint16_t)f32_to_bf16_bits(value(mt, t, r));
+                for (int r = 0; r < 4; ++r) out[(16 * mt + 4 * g + r) * PITCH + (wave * NC + t) * 16 + m] = value(mt, t, r);
     };
     if constexpr (GATE_UP) {
+        const float L = a.glu.limit;
         with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) {
             stage([&](int mt, int t, int r) __attribute__((always_inline)) {
-                return act_of<decltype(A)::value, true>(limit_g(acc[mt][t][r], L)) * limit_u(acc[mt][t + NC][r], L);
+                return (uint16_t)f32_to_bf16_bits(act_of<decltype(A)::value, true>(limit_g(acc[mt][t][r], L)) *
+                                                  limit_u(acc[mt][t + NC][r], L));
             });
         });
     } else {
         stage([&](int mt, int t, int r) __attribute__((always_inline)) { return acc[mt][t][r]; });
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tile.rows_valid * (COLS / 8); i += 64 * kTileWaves) {
-        const int r = i / (COLS / 8), c = 8 * (i % (COLS / 8)), col = tile.nt * COLS + c;
+    Out* to;
+    if constexpr (GATE_UP) to = h;
+    else to = y;
+    for (int i = threadIdx.x; i < tile.rows_valid * (COLS / VEC); i += 64 * kTileWaves) {
+        const int r = i / (COLS / VEC), c = VEC * (i % (COLS / VEC)), col = tile.nt * COLS + c;
         if (col < N)
-            *reinterpret_cast<uint4*>((GATE_UP ? h : y) + (tile.row0 + r) * N + col) = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
+            *reinterpret_cast<uint4*>(to + (tile.row0 + r) * N + col) = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
     }
 }
 
@@ -1030,6 +1034,42 @@ __global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a,
     a.out[t * a.d + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
 }
 
+// out[t] = sum_j topk_w[t, j] * y[dst_row[t, j]] over the slots that have a row, rounded once: y is fp32, as a
+// rounding of it to bf16 would cost more of the result's accuracy than the one of h does.  A thread makes 8 columns.
+template <int K>
+__global__ __launch_bounds__(256) void int4_combine_kernel(const float4* __restrict__ y, const int32_t* __restrict__ dst_row,
+                                                           const float* __restrict__ w, int T, int d8, uint4* __restrict__ out,
+                                                           int32_t* dev_err)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)T * d8; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / d8;
+        const int v = (int)(i - t * d8);
+        float4 a[K], b[K];
+        float c[K];
+        bool on[K], bad = false;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const int32_t dst = dst_row[t * K + j];
+            on[j] = dst >= 0 && dst < T * K;
+            bad |= dst >= T * K;
+            c[j] = w[t * K + j];
+            const int64_t at = ((int64_t)(on[j] ? dst : 0) * d8 + v) * 2;
+            a[j] = y[at];
+            b[j] = y[at + 1];
+        }
+        float o[8] = {};
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            if (!on[j]) continue;
+            const float e[8] = {a[j].x, a[j].y, a[j].z, a[j].w, b[j].x, b[j].y, b[j].z, b[j].w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = fmaf(c[j], e[q], o[q]);
+        }
+        out[i] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+        if (bad && dev_err) atomicOr(dev_err, (int)MOE_ERR_ROW_RANGE);
+    }
+}
+
 // CUs of the current device
 int cu_count()
 {
@@ -1041,7 +1081,7 @@ int cu_count()
 }
 
 template <int G, class GateUp>
-void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, uint16_t* y, hipStream_t s)
+void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
 {
     constexpr bool UP = GateUp::value;
     const int N = UP ? a.f : a.d, K = UP ? a.d : a.f, chunks = (K + 127) / 128;
@@ -1066,7 +1106,7 @@ void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, uint16_t* y, hipStream_t
 }
 
 template <int G, class GateUp>
-void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, uint16_t* y, hipStream_t s)
+void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
 {
     constexpr bool UP = GateUp::value;
     constexpr int COLS = (UP ? 16 : 32) * kTileWaves;
@@ -1138,7 +1178,7 @@ hipError_t launch_dequantize_int4(const uint8_t* codes, const uint16_t* scales, 
 
 size_t int4_ws_bytes(int64_t n_rows, int d, int f)
 {
-    return up256((size_t)n_rows * f * 2) + up256((size_t)n_rows * d * 2) + 256;
+    return up256((size_t)n_rows * f * 2) + up256((size_t)n_rows * d * 4) + 256;
 }
 
 hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
@@ -1146,7 +1186,7 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     if (a.T == 0) return hipSuccess;
     const int64_t R = (int64_t)a.T * a.k;
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws);
-    uint16_t* y = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
+    float* y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
     hipError_t e;
     if (R <= kTokenSlots && 2 * R <= 3 * a.E) {
         return with_group(a.group, [&](auto g) {
@@ -1169,7 +1209,13 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
         });
     }
     if (e != hipSuccess) return e;
-    return launch_combine(MOE_BF16, y, a.dst_row, a.topk_w, a.T, a.k, a.d, R, a.out, a.dev_err, s);
+    const int64_t n = (int64_t)a.T * (a.d / 8), blocks = (n + 255) / 256;
+    e = with_k(a.k, [&](auto kc) {
+        hipLaunchKernelGGL((int4_combine_kernel<decltype(kc)::value>), dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)),
+                           dim3(256), 0, s, (const float4*)y, a.dst_row, a.topk_w, a.T, a.d / 8, (uint4*)a.out, a.dev_err);
+    });
+    if (e != hipSuccess) return e;
+    return hipGetLastError();
 }
 
 }  // namespace moe

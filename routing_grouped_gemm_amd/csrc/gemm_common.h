@@ -1,6 +1,6 @@
 // Shared device code of the grouped GEMMs (bf16 and MXFP8): operand buffer
 // descriptors, the device tile schedule, accumulator layout and epilogues.
-// Included by gemm_bf16.hip and gemm_mxfp8.hip only.
+// Included by the GEMM sources and by int4.hip.
 #pragma once
 
 #include "glu.h"
@@ -420,8 +420,8 @@ __device__ __forceinline__ void stage_acc(const f32x16 (&acc)[BM / 64][WL<NW>::N
 }
 
 // The dropout decisions of a GLU tile's h, for the chunks of eight columns that this thread stores: made before the
-// tile's products, while its first loads are on their way (dgrad-down of 32768 rows, 16 experts, d 4096, f 1536: 9 us
-// of 504, in the epilogue 23), and carried through the main loop in two to four registers.  Chunk i is row
+// tile's products, while its first loads are on their way (dgrad-down of 32768 rows, 16 experts, d 4096, f 1536,
+// gelu_tanh: 484 us, in the epilogue 517, without dropout 469), and carried through the main loop in two to four registers.  Chunk i is row
 // tid / 16 + i NT / 16, columns 8 (tid % 16) of the tile (backward: of each 128-column half, half after half).
 template <int BM, int EPI, int NT>
 struct DropBits {

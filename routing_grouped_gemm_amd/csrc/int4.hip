@@ -200,7 +200,6 @@ __global__ __launch_bounds__(256) void dequantize_int4_kernel(const uint32_t* __
 // ---------------------------------------------------------------- products
 __device__ __forceinline__ bf16x8 as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8, v); }
 
-
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
 {
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
@@ -289,7 +288,8 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
 
 // 2 P consecutive chunks of 128 codes of NT column tiles on their way: P pairs of chunks, 16 rows x 128 bytes each in
 // two loads, eight neighbouring lanes a row's 128 bytes.  (Each lane loading the codes of its own column, as the
-// matrix operand has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 16% slower.)
+// matrix operand has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 168 us
+// instead of 145 for the gate and up products of the few-row kernel's example.)
 // Scale and zero point: lane 4r + j has those of row r and every fourth group, from the j-th on.
 template <int G, int NT, int P>
 struct Codes {
@@ -534,6 +534,9 @@ __device__ __forceinline__ int tile_prefix(const Int4Ffn& a, int ntn, int* s_pre
 // then columns.  A workgroup takes a run of tiles; its W waves share K.  The rows' operands and sums stay in
 // registers from tile to tile, and the next tile's codes are on their way while one is multiplied, so that a
 // workgroup's loads never stop.  K over 128 W U takes several steps a tile, which load the rows each time.
+// 67 tokens, top-4 of 128 experts, d 4096, f 1536, groups of 128 with zero points: 145 us for the gate and up products
+// (5.1 TB/s of codes and scales), 88 for the down one (4.2 TB/s: its tiles are
+// shorter, and each ends with a sum over the waves).
 //   GATE_UP  h = a(g') u': column tiles 0 .. NC - 1 are the gate's, then the up ones.
 //   else     y = h W2^T
 template <int G, int P, int NC, bool GATE_UP>
@@ -651,9 +654,12 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
 }
 
 // ---------------------------------------------------------------- many rows an expert
-// Tiles of 64 rows: each of eight waves has 32 columns (16 and 16 of gate and up) of its own and all
-// the rows, so that a code is converted once for 64 products.  x passes through LDS in chunks of 128, in the codes' order and with each group's row sums,
-// two chunks in turn and one barrier a chunk; codes as in the kernel for few rows.
+// Tiles of 64 rows: each of four waves has 32 columns (16 and 16 of gate and up) of its own and all the rows, so that
+// a code is converted once for 64 products.  x passes through LDS in chunks of 128, in the codes' order and with each
+// group's row sums, two chunks in turn and one barrier a chunk; codes as in the kernel for few rows.  Bound by the
+// vector instructions, 315 a wave and chunk with groups of 64 for its 48 matrix ones (64 apply scales, 64 convert
+// codes, 75 bring x in).  1000 tokens, top-2 of 8 experts, d 2048, f 1152: 62 us for the gate and up products, 39 for
+// the down one, 305 and 240 TFLOP/s (eight waves a workgroup, which share x among more columns: 71).
 constexpr int kTileRows = 64, kTileWaves = 4;
 
 struct XStage {
@@ -679,7 +685,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     const int m = lane & 15, g = lane >> 4;
     const int chunks = (K + 127) / 128;
 
-    // this thread's rows (threadIdx.x / 16 + 32 i) and 16 bytes of each chunk
+    // this thread's rows (threadIdx.x / 16 + 16 i) and 16 bytes of each chunk
     const auto xb = GATE_UP ? buf_of(a.x, (int64_t)a.T * K * 2) : buf_of(h, R * K * 2);
     const int xp = threadIdx.x & 15;
     uint32_t xat[XR];
@@ -795,7 +801,6 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
 #pragma unroll
                         for (int r = 0; r < 4; ++r) acc[mt][t][r] = fmaf(sc, p[mt][t][r], acc[mt][t][r]);
                 }
-
             }
         }
         put_x(c + 1);
@@ -846,7 +851,9 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
 // A single row of x has no use for a matrix instruction.  Here a lane multiplies the codes where they arrive: eight
 // neighbouring lanes have 256 consecutive codes of a row, 32 each, the same 32 of every row that passes, so that the
 // lane's x stay in registers; a wave instruction is eight rows x 128 bytes.  Two products an instruction
-// (v_dot2c_f32_bf16) on the same 16 + q operands.
+// (v_dot2c_f32_bf16) on the same 16 + q operands.  One token, 4 of 128 experts, d 4096, f 1536: 9.0 and 5.3 us for the
+// two kernels, a launch and one chain of load latencies each (its 39 MB take 6.1 us at 6.4 TB/s); with the few-row
+// kernel 20 us for the pass.
 // 32 consecutive x of a lane in the codes' order, and their sum
 struct X32 {
     uint4 v[4];
@@ -1034,12 +1041,12 @@ __global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a,
     a.out[t * a.d + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
 }
 
-// out[t] = sum_j topk_w[t, j] * y[dst_row[t, j]] over the slots that have a row, rounded once: y is fp32, as a
+// out[t] = sum_j topk_w[t, j] * y[dst_row[t, j]] over the slots that have an expert and a row, rounded once: y is fp32, as a
 // rounding of it to bf16 would cost more of the result's accuracy than the one of h does.  A thread makes 8 columns.
 template <int K>
-__global__ __launch_bounds__(256) void int4_combine_kernel(const float4* __restrict__ y, const int32_t* __restrict__ dst_row,
-                                                           const float* __restrict__ w, int T, int d8, uint4* __restrict__ out,
-                                                           int32_t* dev_err)
+__global__ __launch_bounds__(256) void int4_combine_kernel(const float4* __restrict__ y, const int32_t* __restrict__ topk_idx,
+                                                           const int32_t* __restrict__ dst_row, const float* __restrict__ w,
+                                                           int T, int E, int d8, uint4* __restrict__ out, int32_t* dev_err)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)T * d8; i += (int64_t)gridDim.x * 256) {
         const int64_t t = i / d8;
@@ -1050,8 +1057,9 @@ __global__ __launch_bounds__(256) void int4_combine_kernel(const float4* __restr
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             const int32_t dst = dst_row[t * K + j];
-            on[j] = dst >= 0 && dst < T * K;
-            bad |= dst >= T * K;
+            const bool foreign = (uint32_t)topk_idx[t * K + j] >= (uint32_t)E || dst >= T * K;
+            on[j] = !foreign && dst >= 0;
+            bad |= foreign;
             c[j] = w[t * K + j];
             const int64_t at = ((int64_t)(on[j] ? dst : 0) * d8 + v) * 2;
             a[j] = y[at];
@@ -1097,6 +1105,10 @@ void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
         hipLaunchKernelGGL((int4_rows_kernel<G, P, NC, UP>), dim3((unsigned)(tiles < cap ? tiles : cap)), dim3(64 * W), lds, s,
                            a, h, y);
     };
+    // Up to 4096 codes of K are one step of eight waves with two pairs of chunks each; up to 2048, one pair each, so
+    // that the workgroup has eight waves there too.  More columns a tile where registers allow it, as many workgroups
+    // as fit.  (The down product of the example above, K = 1536: all of one or two pairs, one to four column tiles and
+    // one to three workgroups a CU take 85 to 94 us, this choice 88.)
     using std::integral_constant;
     if (chunks > 2 * kWaves) {
         go(integral_constant<int, 2>{}, integral_constant<int, UP ? 1 : 2>{}, 8);
@@ -1115,6 +1127,19 @@ void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
                        sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, h, y);
 }
 
+// Which kernels.  Times of a whole pass, us, in a graph; A: d 4096, f 1536, top-4 of 128; B: d 2048, f 1024, top-2 of 8.
+// Slot by slot or rows together: a slot by itself reads its expert's matrices once more, which costs nothing while
+// few slots share one.
+//   slots      A: 32  48  64      B: 8   12
+//   by slot       75  106 147        22  26
+//   rows          87  109 138        25  25
+// so up to 32 slots, and up to one and a half an expert (B's 8 are 1 an expert, 12 are 1.5; with top-4
+// of its 8 experts 16 slots take 27 and 28).
+// Tiles of 16 or of 64 rows: with 16, each tile reads its matrices anew, from the caches.
+//   rows an expert   A: 16  32      B: 32  48
+//   tiles of 16         426 692        42  52
+//   tiles of 64         480 507        46  48
+// so tiles of 64 from 32 rows an expert on.
 constexpr int kTokenSlots = 32, kTileMinRows = 32;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1212,7 +1237,8 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     const int64_t n = (int64_t)a.T * (a.d / 8), blocks = (n + 255) / 256;
     e = with_k(a.k, [&](auto kc) {
         hipLaunchKernelGGL((int4_combine_kernel<decltype(kc)::value>), dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)),
-                           dim3(256), 0, s, (const float4*)y, a.dst_row, a.topk_w, a.T, a.d / 8, (uint4*)a.out, a.dev_err);
+                           dim3(256), 0, s, (const float4*)y, a.topk_idx, a.dst_row, a.topk_w, a.T, a.E, a.d / 8, (uint4*)a.out,
+                           a.dev_err);
     });
     if (e != hipSuccess) return e;
     return hipGetLastError();

@@ -274,6 +274,8 @@ class MoELayer:
             raise ValueError("set_weights_int4 needs an INT4 layer")
         E, f, d = self.G, self.f, self.d
         for name, w, N, K in (("w13", w13, 2 * f, d), ("w2", w2, d, f)):
+            if len(w) != 3 or w[0] is None or w[1] is None:
+                raise ValueError(f"{name}: expected (codes, scales, zeros or None)")
             for t, shape, dt in zip(w, ((E, N, K // 2), (E, N, K // self.group), (E, N, K // self.group)),
                                     (torch.uint8, torch.bfloat16, torch.uint8)):
                 if t is not None and (tuple(t.shape) != shape or t.dtype is not dt or not t.is_contiguous()
@@ -332,8 +334,7 @@ class MoELayer:
         """Issue one grouped GEMM stage (MOE_GEMM_*) on the layer's buffers (the
         forward and backward calls are these stages in order).  Call
         set_weights first; the tensors are bound on first use."""
-        if self.dtype == MOE_INT4:
-            raise ValueError("an INT4 layer has no separate stages")
+        self._no_int4()
         if getattr(self, "_stages", None) is None:
             self._stages = self._stage_tensors()
         bwd = op in (MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP)
@@ -381,11 +382,17 @@ class MoELayer:
                                  self.counts, self.offsets, self.src_slot, self.s_idx, self.s_w,
                                  self.s_counts, self.s_off, self.s_dst, self.s_src)
 
+    def _no_int4(self):
+        if self.dtype == MOE_INT4:
+            raise ValueError("an INT4 layer has no separate stages: forward is one call")
+
     def permute(self, x):
+        self._no_int4()
         moe_permute(self.dtype, x, self.K, self.s_dst, self.x_perm, src_slot=self.s_fill,
                     x_perm_scales=self.x_perm_scales, dev_err=self.dev_err)
 
     def gemm_fwd(self):
+        self._no_int4()
         if self._glu is not None:
             moe_grouped_glu_fwd(self.dtype, self._glu[self.training], self.x_perm, self.w13, self.w2, self.s_off,
                                 self.g_cap, self.gu, self.h, self.y_perm)
@@ -408,6 +415,7 @@ class MoELayer:
         return self.out_dropout if self.training else 0.0
 
     def combine(self, weights=None, residual=None):
+        self._no_int4()
         p = self._out_drop()
         if p or residual is not None:
             moe_combine_dropout(MOE_F32 if self.dtype == MOE_F32 else MOE_BF16, self.y_perm, self.s_dst,
@@ -429,6 +437,7 @@ class MoELayer:
         """dlogits [T, E] fp32: the gradient of <dout, out> through the gate
         weights of the last forward (bf16 activations; call after forward).  dout
         is the gradient of the layer's output, whatever was dropped of it."""
+        self._no_int4()
         dout = self._drop_dout(dout)
         if getattr(self, "dlogits", None) is None:
             self.dlogits = torch.empty(self.T, self.E, dtype=torch.float32, device=dout.device)

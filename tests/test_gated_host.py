@@ -256,3 +256,17 @@ def test_int4_layer_refusals(m):
         lay.backward(torch.zeros(8, 128, dtype=bf))
     with pytest.raises(ValueError):
         MoELayer(8, 128, 4, 128, 2, device="cpu").set_weights_int4(w(256, 128), w(128, 128))
+
+
+def test_int4_layer_parts_are_refused(m):
+    from routing_grouped_gemm_amd.layer import MoELayer
+    lay = MoELayer(8, 128, 4, 128, 2, m.MOE_INT4, device="cpu", group=64)
+    x = torch.zeros(8, 128, dtype=torch.bfloat16)
+    for call in (lambda: lay.permute(x), lay.gemm_fwd, lay.combine, lambda: lay.gate_grad(x)):
+        with pytest.raises(ValueError):
+            call()
+    codes = torch.zeros(4, 256, 64, dtype=torch.uint8), torch.zeros(4, 256, 2, dtype=torch.bfloat16)
+    down = torch.zeros(4, 128, 64, dtype=torch.uint8), torch.zeros(4, 128, 2, dtype=torch.bfloat16), None
+    for bad in (codes, (codes[0], None, None), (None, codes[1], None)):
+        with pytest.raises(ValueError):
+            lay.set_weights_int4(bad, down)

@@ -351,3 +351,135 @@ def test_streams_and_replays(moe):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(a[-2].cpu(), w)
+
+
+@pytest.mark.parametrize("T", [30, 100])
+@pytest.mark.parametrize("bad", [8, -1, 2 ** 30])
+def test_foreign_experts_are_flagged_in_batches(moe, T, bad):
+    """An expert past the experts, in the forms for many tokens: flagged, and its slot adds nothing."""
+    c = Ffn(moe, T, 8, 128, 128, 2, 64, False, seed=2)
+    live = torch.ones(T, 2, dtype=torch.bool)
+    live[3, 1] = False
+    keep = c.route["topk_idx"].clone()
+    c.route["topk_idx"][3, 1] = bad
+    out = c.run()
+    c.route["topk_idx"] = keep
+    c.check(out, live)
+    assert int(c.err) == moe.MOE_ERR_ROW_RANGE
+
+
+def _reroute(c, idx):
+    order = torch.argsort(idx.reshape(-1), stable=True)
+    dst = torch.empty_like(order)
+    dst[order] = torch.arange(order.numel())
+    off = torch.cat([torch.zeros(1, dtype=torch.long), torch.bincount(idx.reshape(-1), minlength=c.E).cumsum(0)])
+    c.route.update(topk_idx=idx.int(), dst_row=dst.int(), src_slot=order.int(), group_off=off.int())
+
+
+@pytest.mark.parametrize("T", [1, 5, 60])
+def test_the_same_expert_twice(moe, T):
+    c = Ffn(moe, T, 6, 128, 96, 3, 32, True, seed=9)
+    _reroute(c, torch.arange(T)[:, None].expand(T, 3) % 2 * 5)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T", [1, 4, 40])
+def test_eight_slots_of_a_thousand_experts(moe, T):
+    c = Ffn(moe, T, 1024, 64, 32, 8, 32, True, seed=T)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T", [1, 20, 90])
+def test_parameters_at_odd_addresses(moe, T):
+    """Scales at any even address, zero points at any."""
+    c = Ffn(moe, T, 3, 128, 64, 2, 32, True, seed=5)
+    c.check(c.run())
+    want = c.run()
+    for i, (codes, s, z) in enumerate(c.w):
+        wide_s = torch.full((s.numel() + 9,), float("nan"), dtype=BF, device=DEV)
+        wide_z = torch.full((z.numel() + 9,), 255, dtype=torch.uint8, device=DEV)
+        s2, z2 = wide_s[1:1 + s.numel()].view(s.shape), wide_z[3:3 + z.numel()].view(z.shape)
+        s2.copy_(s)
+        z2.copy_(z)
+        c.w[i] = (codes, s2, z2)
+    assert torch.equal(c.run(), want)
+
+
+def _big(moe, T, E, d, f, k, group):
+    """A call on the device whose codes are random bytes, scales 2^-7 and zero points 8."""
+    g = torch.Generator(DEV).manual_seed(1)
+    w = []
+    for N, K in ((2 * f, d), (d, f)):
+        codes = torch.randint(0, 256, (E, N, K // 2), generator=g, dtype=torch.uint8, device=DEV)
+        w.append((codes, torch.full((E, N, K // group), 2.0 ** -7 if K < 1024 else 2.0 ** -11, dtype=BF, device=DEV), None))
+    x = torch.empty(T, d, dtype=BF, device=DEV)
+    for a in range(0, T, 1 << 18):
+        x[a:a + (1 << 18)].normal_(generator=g)
+    r = _route(T, E, k, 3)
+    out = torch.empty(T, d, dtype=BF, device=DEV)
+    ws = torch.empty(moe.moe_int4_workspace_bytes(T * k, d, f), dtype=torch.uint8, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    moe.moe_int4_ffn(moe.glu(), x, *(r[n].to(DEV) for n in ("topk_idx", "topk_w", "dst_row", "src_slot", "group_off")), group,
+                     *w, out, ws, dev_err=err)
+    assert int(err) == 0
+    return x, r, w, out
+
+
+def _big_values(w, e, rows):
+    codes, s, _ = w
+    c = codes[e, rows]
+    return (torch.stack([c & 15, c >> 4], -1).flatten(1).double() - 8) * float(s.flatten()[0])
+
+
+def _big_check(x, r, w, out, tokens):
+    """Some tokens in 64 bits.  The bounds of Ffn.check with one scale: fp32 sums of K terms below 31 |x| s each, in
+    two steps, then the roundings of h and of the output."""
+    f, d = w[1][0].shape[2] * 2, x.shape[1]
+    for t in tokens:
+        want = torch.zeros(d, dtype=torch.float64, device=DEV)
+        tol = torch.zeros_like(want)
+        v = x[t].double()
+        for j in range(r["topk_idx"].shape[1]):
+            e, c = int(r["topk_idx"][t, j]), float(r["topk_w"][t, j])
+            gu, mag = [], []
+            for a in range(0, 2 * f, 128):
+                m = _big_values(w[0], e, slice(a, min(a + 128, 2 * f)))
+                gu.append(m @ v)
+                mag.append(m.abs() @ v.abs())
+            gu, mag = torch.cat(gu), torch.cat(mag)
+            s = float(w[0][1].flatten()[0])
+            eps = 2.0 ** -23 * (2 * 31 * 132 * s * float(v.abs().sum()) + (d // 32 + 12) * mag)
+            g, u, dg, du = gu[:f], gu[f:], eps[:f], eps[f:]
+            h = g * torch.sigmoid(g) * u
+            dh = 1.13 * dg * (u.abs() + du) + (g * torch.sigmoid(g)).abs() * du + GATE * h.abs()
+            dh = dh + 2.0 ** -8 * (h.abs() + dh)
+            for a in range(0, d, 1 << 16):
+                m = _big_values(w[1], e, slice(a, min(a + (1 << 16), d)))
+                y = m @ h
+                s = float(w[1][1].flatten()[0])
+                dy = 2.0 ** -23 * (2 * 31 * 132 * s * float(h.abs().sum()) + (f // 32 + 12) * (m.abs() @ h.abs())) * 1.01
+                dy = dy + m.abs() @ dh
+                want[a:a + (1 << 16)] += c * y
+                tol[a:a + (1 << 16)] += c * (dy + 2.0 ** -20 * y.abs())
+        err = (out[t].double() - want).abs()
+        tol += 2.0 ** -8 * want.abs() + 1e-35
+        assert bool((err <= tol).all()), (t, float((err / tol).max()))
+        assert float(err.norm()) <= 2.0 ** -6 * float(want.norm())
+
+
+def test_as_many_tokens_as_32_bits_hold(moe):
+    """x and h of just under 2^31 bytes, fp32 expert outputs past 2^32."""
+    T = 2 ** 23 - 1
+    _say("int4 many tokens")
+    x, r, w, out = _big(moe, T, 8, 128, 128, 1, 64)
+    _big_check(x, r, w, out, [0, 1, T // 2, T - 2, T - 1])
+    src = r["src_slot"][torch.tensor([0, T - 1, T // 3])]
+    _big_check(x, r, w, out, src.tolist())
+
+
+@pytest.mark.parametrize("T", [1, 9, 70])
+def test_the_widest_rows(moe, T):
+    """d of 2^20: offsets into an expert's codes up to 2^30, 8192 chunks of K."""
+    _say("int4 wide rows", T)
+    x, r, w, out = _big(moe, T, 2, 2 ** 20, 1024, 2 if T < 20 else 1, 128)
+    _big_check(x, r, w, out, sorted({0, T // 2, T - 1}))

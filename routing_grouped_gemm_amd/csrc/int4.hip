@@ -655,11 +655,13 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
 
 // ---------------------------------------------------------------- many rows an expert
 // Tiles of 64 rows: each of four waves has 32 columns (16 and 16 of gate and up) of its own and all the rows, so that
-// a code is converted once for 64 products.  x passes through LDS in chunks of 128, in the codes' order and with each
-// group's row sums, two chunks in turn and one barrier a chunk; codes as in the kernel for few rows.  Bound by the
-// vector instructions, 315 a wave and chunk with groups of 64 for its 48 matrix ones (64 apply scales, 64 convert
-// codes, 75 bring x in).  1000 tokens, top-2 of 8 experts, d 2048, f 1152: 62 us for the gate and up products, 39 for
-// the down one, 305 and 240 TFLOP/s (eight waves a workgroup, which share x among more columns: 71).
+// a code is converted once for 64 products.  x passes through LDS in chunks of 128, two in turn and one barrier a chunk;
+// codes as in the kernel for few rows.  Bound by the issue of vector instructions, so what a row needs once is not done
+// again for each tile of columns: rows come in the codes' order with their sums (fp32, over each 32), x from
+// int4_order_kernel, h from the gate and up products' tiles.
+// 1000 tokens, top-2 of 8 experts, d 2048, f 1152, groups of 64 with zero points: 54 us for the gate and up products, 33
+// for the down one (350 and 290 TFLOP/s), 5 for the order of x; with order and sums made in every tile and the compiler's
+// order of loads from LDS 62 and 39.  Eight waves a workgroup, which share x among more columns: 71.
 constexpr int kTileRows = 64, kTileWaves = 4;
 
 struct XStage {
@@ -668,9 +670,33 @@ struct XStage {
     uint4 none[kTileRows];                   // zeros, what lane groups 1 to 3 take for it
 };
 
+// eight elements of a row in the codes' order, and in each of four neighbouring lanes the sum of their 32
+__device__ __forceinline__ uint4 order_and_sum(uint4 v, float& sum)
+{
+    constexpr uint32_t one = 0x3f803f80u;
+    v = pair_order(v);
+    sum = dot2(v.x, one, dot2(v.y, one, dot2(v.z, one, dot2(v.w, one, 0.0f))));
+    sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xF, 0xF, true));
+    sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xF, 0xF, true));
+    return v;
+}
+
+// x [n8 vectors] in that order, and its sums
+__global__ __launch_bounds__(256) void int4_order_kernel(const uint4* __restrict__ x, int64_t n8, uint4* __restrict__ xo,
+                                                         float* __restrict__ sums)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+        float sum;
+        xo[i] = order_and_sum(x[i], sum);
+        if (threadIdx.x % 4 == 0) sums[i / 4] = sum;
+    }
+}
+
+// rows of x (GATE_UP: of h) and their sums as above; h and hsum alike
 template <int G, bool GATE_UP>
 __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_tile_kernel(
-    Int4Ffn a, uint16_t* __restrict__ h, float* __restrict__ y)
+    Int4Ffn a, const uint16_t* __restrict__ rows, const float* __restrict__ sums, uint16_t* __restrict__ h,
+    float* __restrict__ hsum, float* __restrict__ y)
 {
     constexpr int NT = 2, NC = GATE_UP ? 1 : 2, MT = kTileRows / 16, GC = 128 / G, PER = G / 32;
     constexpr int XR = kTileRows / (4 * kTileWaves);     // rows that a thread brings in
@@ -685,44 +711,45 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     const int m = lane & 15, g = lane >> 4;
     const int chunks = (K + 127) / 128;
 
-    // this thread's rows (threadIdx.x / 16 + 16 i) and 16 bytes of each chunk
-    const auto xb = GATE_UP ? buf_of(a.x, (int64_t)a.T * K * 2) : buf_of(h, R * K * 2);
-    const int xp = threadIdx.x & 15;
-    uint32_t xat[XR];
-#pragma unroll
-    for (int i = 0; i < XR; ++i) {
-        const int r = (threadIdx.x >> 4) + 4 * kTileWaves * i;
+    // this thread's rows (threadIdx.x / 16 + 16 i) and 16 bytes of each chunk; and one row's sum over 32
+    const int64_t n = GATE_UP ? a.T : R;
+    const auto xb = buf_of(rows, n * K * 2), sb = buf_of(sums, n * (K / 32) * 4);
+    auto row_of = [&](int r) __attribute__((always_inline)) {
         const int64_t row = tile.row0 + min(r, tile.rows_valid - 1);
         if constexpr (GATE_UP) {
             const int64_t slot = a.src_slot[row];
-            const bool in = slot >= 0 && slot < R;
-            if (slot >= R && xp == 0 && a.dev_err) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
-            xat[i] = in ? (uint32_t)(slot / a.k * K * 2) : kPast;        // a foreign row is one of zeros: so is its h
+            if (slot >= R && a.dev_err) atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
+            return slot >= 0 && slot < R ? slot / a.k : (int64_t)-1;     // a foreign row is one of zeros: so is its h
         } else {
-            xat[i] = (uint32_t)(row * K * 2);
+            return row;
         }
-    }
-    uint4 xr[XR];
-    auto load_x = [&](int c) __attribute__((always_inline)) {
-        const uint32_t past = c * 128 + 8 * xp < K ? 0 : kPast;
-#pragma unroll
-        for (int i = 0; i < XR; ++i) xr[i] = load16(xb, (xat[i] + c * 256 + 16 * xp) | past);
     };
-    auto put_x = [&](int c) __attribute__((always_inline)) {
-        constexpr uint32_t one = 0x3f803f80u;
+    const int xp = threadIdx.x & 15, sr = 16 * wave + (lane >> 2), s32 = lane & 3;
+    uint32_t xat[XR];
 #pragma unroll
-        for (int i = 0; i < XR; ++i) {
-            const int r = (threadIdx.x >> 4) + 4 * kTileWaves * i;
-            const uint4 v = pair_order(xr[i]);
-            xs.part[c & 1][r][xp ^ (r & 15)] = v;
-            float sum = dot2(v.x, one, dot2(v.y, one, dot2(v.z, one, dot2(v.w, one, 0.0f))));
-            // over a group's G / 8 threads
-            sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xF, 0xF, true));
-            sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xF, 0xF, true));
-            if constexpr (G >= 64) sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x141, 0xF, 0xF, true));
-            if constexpr (G >= 128) sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x140, 0xF, 0xF, true));
-            if (xp % (G / 8) == 0) xs.sum[c & 1][xp / (G / 8)][r] = split_sum(sum);
-        }
+    for (int i = 0; i < XR; ++i) {
+        const int64_t row = row_of((threadIdx.x >> 4) + 4 * kTileWaves * i);
+        xat[i] = row < 0 ? kPast : (uint32_t)(row * K * 2 + 16 * xp);
+    }
+    const int64_t srow = row_of(sr);
+    const uint32_t sat = srow < 0 ? kPast : (uint32_t)((srow * (K / 32) + s32) * 4);
+    uint4 xr[XR];
+    float xsum;
+    auto load_x = [&](int c, int i) __attribute__((always_inline)) {
+        xr[i] = load16(xb, (xat[i] + c * 256) | (c * 128 + 8 * xp < K ? 0 : kPast));
+    };
+    auto load_sum = [&](int c) __attribute__((always_inline)) {
+        xsum = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sb, (int)((sat + c * 16) | (c * 128 + 32 * s32 < K ? 0 : kPast)), 0, 0));
+    };
+    auto put_x = [&](int st, int i) __attribute__((always_inline)) {
+        const int r = (threadIdx.x >> 4) + 4 * kTileWaves * i;
+        xs.part[st][r][xp ^ (r & 15)] = xr[i];
+    };
+    auto put_sum = [&](int st) __attribute__((always_inline)) {
+        float v = xsum;
+        if constexpr (G >= 64) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
+        if constexpr (G >= 128) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
+        xs.sum[st][s32 / (G / 32)][sr] = split_sum(v);       // (by each of a group's lanes: no branch among the products)
     };
 
     int row0[NT];
@@ -743,10 +770,19 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     const Conv cv = conv();
     if (threadIdx.x < kTileRows) xs.none[threadIdx.x] = make_uint4(0, 0, 0, 0);
     load_all(w, where_of<G>(wb, row0, 0, K, live), K);
-    load_x(0);
-    put_x(0);
-    load_x(1);
+#pragma unroll
+    for (int i = 0; i < XR; ++i) load_x(0, i);
+    load_sum(0);
+#pragma unroll
+    for (int i = 0; i < XR; ++i) {
+        put_x(0, i);
+        load_x(1, i);
+    }
+    put_sum(0);
+    load_sum(1);
     __syncthreads();
+    // Four 32-deep steps a chunk.  Each has the next one's operands on their way from LDS, and brings in a share of the
+    // next chunk's x beside its products; the barriers to the scheduler keep that order.
     auto chunk = [&](int c, auto U_) __attribute__((always_inline)) {
         constexpr int u = decltype(U_)::value;           // which of the pair
         if (u * GC % 4 == 0) {
@@ -762,55 +798,72 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
             put_pair(turn[wave], w, 0);
             load_pair(w, where_of<G>(wb, row0, c + 2, K, live), 0, K);
         }
-        if (c < chunks) {
-            uint4 q[NT];
+        uint4 q[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) q[t] = turn[wave].part[t][m][(4 * u + g) ^ (m >> 1)];
+        bf16x8 xf[2][MT];
+        uint4 X[MT];
+        auto read = [&](int j) __attribute__((always_inline)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (j % PER == 0) X[mt] = (g == 0 ? xs.sum[u][j / PER] : xs.none)[16 * mt + m];
+                xf[j & 1][mt] = as_bf16x8(xs.part[u][16 * mt + m][(G == 128 ? 4 * g + j : 4 * j + g) ^ m]);
+            }
+        };
+        read(0);
+        if constexpr (G != 128) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) q[t] = exchange4(q[t]);
+        }
+        f32x4 p[MT][NT];
+        auto begin = [&](int t, int b) __attribute__((always_inline)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) p[mt][t] = minus_zeros(X[mt], sz[t][(u * GC + b) % 4] & 0xffu);
+        };
+#pragma unroll
+        for (int t = 0; t < NT; ++t) begin(t, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (j < 3) read(j + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                q[t] = turn[wave].part[t][m][(4 * u + g) ^ (m >> 1)];
-                if constexpr (G != 128) q[t] = exchange4(q[t]);
+                const bf16x8 wf = as_bf16x8(codes_to_bf16(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, cv));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    p[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j & 1][mt], wf, p[mt][t], 0, 0, 0);
             }
 #pragma unroll
-            for (int b = 0; b < GC; ++b) {
-                const int gi = (u * GC + b) % 4;
-                f32x4 p[MT][NT];
+            for (int i = j * XR / 4; i < (j + 1) * XR / 4; ++i) {
+                put_x(1 - u, i);
+                load_x(c + 2, i);
+            }
+            if (j == 3) {
+                put_sum(1 - u);
+                load_sum(c + 2);
+            }
+            if (j % PER < PER - 1) continue;
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint4 X = (g == 0 ? xs.sum[c & 1][b] : xs.none)[16 * mt + m];
+            for (int t = 0; t < NT; ++t) {
+                // (one column tile's sums are scaled while the other's next group begins)
+                const float sc = bf16_hi(sz[t][(u * GC + j / PER) % 4]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) p[mt][t] = minus_zeros(X, sz[t][gi] & 0xffu);
-                }
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int j = b * PER + i;
-                    bf16x8 wf[NT];
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) wf[t] = as_bf16x8(codes_to_bf16(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, cv));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const bf16x8 xf = as_bf16x8(xs.part[c & 1][16 * mt + m][(G == 128 ? 4 * g + i : 4 * j + g) ^ m]);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            p[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, wf[t], p[mt][t], 0, 0, 0);
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const float sc = bf16_hi(sz[t][gi]);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[mt][t][r] = fmaf(sc, p[mt][t][r], acc[mt][t][r]);
-                }
+                    for (int r = 0; r < 4; ++r) acc[mt][t][r] = fmaf(sc, p[mt][t][r], acc[mt][t][r]);
+                __builtin_amdgcn_sched_barrier(0);
+                if (j < 3) begin(t, (j + 1) / PER);
             }
         }
-        put_x(c + 1);
-        load_x(c + 2);
         __syncthreads();
     };
-    for (int c = 0; c < chunks; c += 2) {
+    for (int c = 0; c + 1 < chunks; c += 2) {
         chunk(c, std::integral_constant<int, 0>{});
         chunk(c + 1, std::integral_constant<int, 1>{});
     }
+    if (chunks & 1) chunk(chunks - 1, std::integral_constant<int, 0>{});
 
     // the tile leaves through LDS as rows (the loop's last barrier has freed it)
     using Out = std::conditional_t<GATE_UP, uint16_t, float>;
@@ -837,13 +890,18 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
         stage([&](int mt, int t, int r) __attribute__((always_inline)) { return acc[mt][t][r]; });
     }
     __syncthreads();
-    Out* to;
-    if constexpr (GATE_UP) to = h;
-    else to = y;
     for (int i = threadIdx.x; i < tile.rows_valid * (COLS / VEC); i += 64 * kTileWaves) {
         const int r = i / (COLS / VEC), c = VEC * (i % (COLS / VEC)), col = tile.nt * COLS + c;
-        if (col < N)
-            *reinterpret_cast<uint4*>(to + (tile.row0 + r) * N + col) = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
+        if (col >= N) continue;                  // (N is a multiple of 32: four neighbours stay together)
+        uint4 v = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
+        if constexpr (GATE_UP) {
+            float sum;
+            v = order_and_sum(v, sum);
+            if (i % 4 == 0) hsum[(tile.row0 + r) * (N / 32) + col / 32] = sum;
+            *reinterpret_cast<uint4*>(h + (tile.row0 + r) * N + col) = v;
+        } else {
+            *reinterpret_cast<uint4*>(y + (tile.row0 + r) * N + col) = v;
+        }
     }
 }
 
@@ -1117,14 +1175,25 @@ void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
     }
 }
 
-template <int G, class GateUp>
-void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
+template <int G>
+void launch_tiles(const Int4Ffn& a, uint16_t* h, float* hsum, float* y, hipStream_t s)
 {
-    constexpr bool UP = GateUp::value;
-    constexpr int COLS = (UP ? 16 : 32) * kTileWaves;
-    const int64_t R = (int64_t)a.T * a.k, mt = R / kTileRows + (R < a.E ? R : a.E), ntn = ((UP ? a.f : a.d) + COLS - 1) / COLS;
-    hipLaunchKernelGGL((int4_tile_kernel<G, UP>), dim3((unsigned)((mt * ntn + 7) / 8 * 8)), dim3(64 * kTileWaves),
-                       sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, h, y);
+    const int64_t R = (int64_t)a.T * a.k, mt = R / kTileRows + (R < a.E ? R : a.E);
+    auto go = [&](auto UP_, const uint16_t* rows, const float* sums) {
+        constexpr bool UP = decltype(UP_)::value;
+        constexpr int COLS = (UP ? 16 : 32) * kTileWaves;
+        const int64_t ntn = ((UP ? a.f : a.d) + COLS - 1) / COLS;
+        hipLaunchKernelGGL((int4_tile_kernel<G, UP>), dim3((unsigned)((mt * ntn + 7) / 8 * 8)), dim3(64 * kTileWaves),
+                           sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, rows, sums, h, hsum, y);
+    };
+    // x in the codes' order and its sums lie where y will, which is longer
+    const int64_t n8 = (int64_t)a.T * (a.d / 8), blocks = (n8 + 255) / 256;
+    uint16_t* xo = reinterpret_cast<uint16_t*>(y);
+    float* xsum = reinterpret_cast<float*>(xo + (int64_t)a.T * a.d);
+    hipLaunchKernelGGL(int4_order_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0, s,
+                       (const uint4*)a.x, n8, (uint4*)xo, xsum);
+    go(std::true_type{}, xo, xsum);
+    go(std::false_type{}, h, hsum);
 }
 
 // Which kernels.  Times of a whole pass, us, in a graph; A: d 4096, f 1536, top-4 of 128; B: d 2048, f 1024, top-2 of 8.
@@ -1136,9 +1205,9 @@ void launch_tile(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
 // so up to 32 slots, and up to one and a half an expert (B's 8 are 1 an expert, 12 are 1.5; with top-4
 // of its 8 experts 16 slots take 27 and 28).
 // Tiles of 16 or of 64 rows: with 16, each tile reads its matrices anew, from the caches.
-//   rows an expert   A: 16  32      B: 32  48
-//   tiles of 16         426 692        42  52
-//   tiles of 64         480 507        46  48
+//   rows an expert   A: 16  24  32      B: 32  48  64
+//   tiles of 16         389 484 656        39  46  54
+//   tiles of 64         458 470 485        44  45  46
 // so tiles of 64 from 32 rows an expert on.
 constexpr int kTokenSlots = 32, kTileMinRows = 32;
 
@@ -1203,7 +1272,7 @@ hipError_t launch_dequantize_int4(const uint8_t* codes, const uint16_t* scales, 
 
 size_t int4_ws_bytes(int64_t n_rows, int d, int f)
 {
-    return up256((size_t)n_rows * f * 2) + up256((size_t)n_rows * d * 4) + 256;
+    return up256((size_t)n_rows * f * 2) + up256((size_t)n_rows * (f / 32) * 4) + up256((size_t)n_rows * d * 4) + 256;
 }
 
 hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
@@ -1211,7 +1280,8 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     if (a.T == 0) return hipSuccess;
     const int64_t R = (int64_t)a.T * a.k;
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws);
-    float* y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
+    float* hsum = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
+    float* y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hsum) + up256((size_t)R * (a.f / 32) * 4));
     hipError_t e;
     if (R <= kTokenSlots && 2 * R <= 3 * a.E) {
         return with_group(a.group, [&](auto g) {
@@ -1223,10 +1293,7 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     using Up = std::true_type;
     using Down = std::false_type;
     if (R >= (int64_t)kTileMinRows * a.E) {
-        e = with_group(a.group, [&](auto g) {
-            launch_tile<decltype(g)::value>(a, Up{}, h, y, s);
-            launch_tile<decltype(g)::value>(a, Down{}, h, y, s);
-        });
+        e = with_group(a.group, [&](auto g) { launch_tiles<decltype(g)::value>(a, h, hsum, y, s); });
     } else {
         e = with_group(a.group, [&](auto g) {
             launch_rows<decltype(g)::value>(a, Up{}, h, y, s);

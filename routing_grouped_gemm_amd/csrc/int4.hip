@@ -286,15 +286,15 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
     return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
 
-// 2 P consecutive chunks of 128 codes of NT column tiles on their way: P pairs of chunks, 16 rows x 128 bytes each in
-// two loads, eight neighbouring lanes a row's 128 bytes.  (Each lane loading the codes of its own column, as the
-// matrix operand has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 168 us
-// instead of 145 for the gate and up products of the few-row kernel's example.)
+// A pair of consecutive chunks of 128 codes of NT column tiles on their way: 16 rows x 128 bytes each in two loads,
+// eight neighbouring lanes a row's 128 bytes.  (Each lane loading the codes of its own column, as the matrix operand
+// has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 168 us instead of 145 for the
+// gate and up products of the few-row kernel's example.)
 // Scale and zero point: lane 4r + j has those of row r and every fourth group, from the j-th on.
-template <int G, int NT, int P>
+template <int G, int NT>
 struct Codes {
-    static constexpr int NS = (P * 256 / G + 3) / 4;
-    uint4 q[P][NT][2];
+    static constexpr int NS = (256 / G + 3) / 4;
+    uint4 q[NT][2];
     uint32_t s[NS][NT], z[NS][NT];
 };
 
@@ -326,18 +326,18 @@ __device__ __forceinline__ Where<NT> where_of(const WBuf& w, const int (&row0)[N
     return p;
 }
 
-template <int G, int NT, int P>
-__device__ __forceinline__ void load_pair(Codes<G, NT, P>& o, const Where<NT>& p, int v, int K)
+template <int G, int NT>
+__device__ __forceinline__ void load_pair(Codes<G, NT>& o, const Where<NT>& p, int K)
 {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        o.q[v][t][0] = load16(p.w.codes, p.code[t] + 128 * v);
-        o.q[v][t][1] = load16(p.w.codes, p.code[t] + 4 * K + 128 * v);     // eight rows on
+        o.q[t][0] = load16(p.w.codes, p.code[t]);
+        o.q[t][1] = load16(p.w.codes, p.code[t] + 4 * K);     // eight rows on
     }
 }
 
-template <int G, int NT, int P>
-__device__ __forceinline__ void load_scales(Codes<G, NT, P>& o, const Where<NT>& p, int i)
+template <int G, int NT>
+__device__ __forceinline__ void load_scales(Codes<G, NT>& o, const Where<NT>& p, int i)
 {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -348,18 +348,16 @@ __device__ __forceinline__ void load_scales(Codes<G, NT, P>& o, const Where<NT>&
     }
 }
 
-template <int G, int NT, int P>
-__device__ __forceinline__ void load_all(Codes<G, NT, P>& o, const Where<NT>& p, int K)
+template <int G, int NT>
+__device__ __forceinline__ void load_all(Codes<G, NT>& o, const Where<NT>& p, int K)
 {
     // in the order in which they will be waited for, here as in the loop: the compiler counts the loads in flight
-    constexpr int GC = 128 / G;
-#pragma unroll
-    for (int u = 0; u < 2 * P; ++u) {
-        if (u * GC % 4 == 0) load_scales(o, p, u * GC / 4);
-        __builtin_amdgcn_sched_barrier(0);
-        if (u % 2 == 0) load_pair(o, p, u / 2, K);
-        __builtin_amdgcn_sched_barrier(0);
-    }
+    load_scales(o, p, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_pair(o, p, K);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (Codes<G, NT>::NS == 2) load_scales(o, p, 1);
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // A wave's own LDS: a pair of chunks passes through it from the lanes that loaded it to those whose column it is.
@@ -376,28 +374,29 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-template <int G, int NT, int P>
-__device__ __forceinline__ void put_pair(Turn<NT>& turn, const Codes<G, NT, P>& w, int v)
+template <int G, int NT>
+__device__ __forceinline__ void put_pair(Turn<NT>& turn, const Codes<G, NT>& w)
 {
     const int lane = threadIdx.x & 63, r = lane >> 3, p = lane & 7;
     wave_fence();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        turn.part[t][r][p ^ (r >> 1)] = w.q[v][t][0];
-        turn.part[t][r + 8][p ^ ((r + 8) >> 1)] = w.q[v][t][1];
+        turn.part[t][r][p ^ (r >> 1)] = w.q[t][0];
+        turn.part[t][r + 8][p ^ ((r + 8) >> 1)] = w.q[t][1];
     }
     wave_fence();
 }
 
-// 2 P chunks of a lane's x row as matrix operands, and each group's sum over the row (lane group 0; 0 in the others)
-template <int G, int U>
+// A pair of chunks of a lane's x row as matrix operands, and each group's sum over the row (lane group 0; 0 in the others)
+template <int G>
 struct XRows {
+    static constexpr int U = 2;
     static constexpr int PER = G / 32;                           // MFMAs of a group
     static constexpr int GROUPS = U * 128 / G;
     bf16x8 f[U][4];
     float X[GROUPS];
 
-    // chunks c .. c + U - 1 of the row at byte `at`
+    // chunks c and c + 1 of the row at byte `at`
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, uint32_t at, int c, int K)
     {
         const int g = (threadIdx.x & 63) >> 4;
@@ -430,17 +429,17 @@ struct XRows {
     }
 };
 
-// acc[t] += (x rows) . (weight rows) over the first n chunks.  ahead(v) is called when pair v's codes have
-// left their registers, ahead_scales(i) when the i-th scales have.
-template <int G, int NT, int P, class F, class S>
-__device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G, 2 * P>& x, Codes<G, NT, P>& w, Turn<NT>& turn,
-                                        uint32_t z8, int n, Conv cv, F&& ahead, S&& ahead_scales)
+// acc[t] += (x rows) . (weight rows) over the first n chunks.  ahead() is called when the codes have left their
+// registers, ahead_scales(i) when the i-th scales have.
+template <int G, int NT, class F, class S>
+__device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G>& x, Codes<G, NT>& w, Turn<NT>& turn, uint32_t z8,
+                                        int n, Conv cv, F&& ahead, S&& ahead_scales)
 {
     constexpr int PER = G / 32, GC = 128 / G;                    // MFMAs of a group, groups of a chunk
     const int lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     uint32_t sz[NT][4];      // bf16 scale in the upper half, zero point below
 #pragma unroll
-    for (int u = 0; u < 2 * P; ++u) {
+    for (int u = 0; u < 2; ++u) {
         if (u * GC % 4 == 0) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -450,15 +449,15 @@ __device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G, 2 * P>&
             }
             ahead_scales(u * GC / 4);
         }
-        if (u % 2 == 0) {
-            put_pair(turn, w, u / 2);
-            ahead(u / 2);
+        if (u == 0) {
+            put_pair(turn, w);
+            ahead();
         }
         if (u < n) {
             uint4 q[NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                q[t] = turn.part[t][m][(4 * (u & 1) + g) ^ (m >> 1)];
+                q[t] = turn.part[t][m][(4 * u + g) ^ (m >> 1)];
                 if constexpr (G != 128) q[t] = exchange4(q[t]);
             }
 #pragma unroll
@@ -482,14 +481,21 @@ __device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G, 2 * P>&
     }
 }
 
-constexpr int kWaves = 8;      // most waves of a workgroup
+constexpr int kWaves = 16;     // most waves of a workgroup
 
 // sum over the waves of element idx (row idx / 16, column idx % 16) of column tile t
 template <int NT>
 __device__ __forceinline__ float wave_sum(const float (*red)[NT][256], int waves, int t, int idx)
 {
+    // (eight reads on their way together: those past the last wave's are that one's again, and not added)
     float v = 0.0f;
-    for (int w = 0; w < waves; ++w) v += red[w][t][idx];
+    for (int w0 = 0; w0 < waves; w0 += 8) {
+        float p[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) p[w] = red[min(w0 + w, waves - 1)][t][idx];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += w0 + w < waves ? p[w] : 0.0f;
+    }
     return v;
 }
 
@@ -531,19 +537,22 @@ __device__ __forceinline__ int tile_prefix(const Int4Ffn& a, int ntn, int* s_pre
 }
 
 // The products of up to 16 rows of an expert with 16 NC of its columns (a tile), tiles expert after expert, rows
-// then columns.  A workgroup takes a run of tiles; its W waves share K.  The rows' operands and sums stay in
-// registers from tile to tile, and the next tile's codes are on their way while one is multiplied, so that a
-// workgroup's loads never stop.  K over 128 W U takes several steps a tile, which load the rows each time.
-// 67 tokens, top-4 of 128 experts, d 4096, f 1536, groups of 128 with zero points: 145 us for the gate and up products
-// (5.1 TB/s of codes and scales), 88 for the down one (4.2 TB/s: its tiles are
-// shorter, and each ends with a sum over the waves).
+// then columns.  A workgroup takes a run of tiles; its W waves share K, a pair of chunks each.  The rows' operands and
+// sums stay in registers from tile to tile, and the next tile's codes are on their way while one is multiplied, so that a
+// workgroup's loads never stop.  K over 256 W takes several steps a tile, which load the rows each time.
+// Four waves a SIMD (at most 128 registers): a workgroup's waves go to the SIMDs in turn from the first, so two of six
+// waves each put four on it, and with registers for three the second would wait for the first to end (down product of 64
+// experts, K = 1408: 114 us a pass so, 88 with four).
+// 67 tokens, top-4 of 128 experts, d 4096, f 1536, groups of 128 with zero points: 141 us for the gate and up products
+// (5.3 TB/s of codes and scales; loads alone, multiplied with nothing, 137), 85 for the down one (4.4 TB/s; 75: its tiles
+// are shorter, and each ends with a sum over the waves).  Run again and again the power limit lowers the clock, 153 and 93.
 //   GATE_UP  h = a(g') u': column tiles 0 .. NC - 1 are the gate's, then the up ones.
 //   else     y = h W2^T
-template <int G, int P, int NC, bool GATE_UP>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_rows_kernel(
+template <int G, bool GATE_UP>
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))) void int4_rows_kernel(
     Int4Ffn a, uint16_t* __restrict__ h, float* __restrict__ y)
 {
-    constexpr int NT = GATE_UP ? 2 * NC : NC, U = 2 * P;
+    constexpr int NC = GATE_UP ? 1 : 2, NT = 2, U = 2;
     const int W = blockDim.x >> 6;
     extern __shared__ __align__(16) uint8_t smem[];
     Turn<NT>* turn = reinterpret_cast<Turn<NT>*>(smem);
@@ -581,7 +590,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
     uint32_t xat = 0;
     bool in = true;
     int64_t have = -1;       // row of h whose tile's operands are held
-    XRows<G, U> x;
+    XRows<G> x;
     f32x4 acc[NT];
     int buf = 0;
 
@@ -593,7 +602,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
     };
     const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
     const Conv cv = conv();
-    auto step = [&](Codes<G, NT, P>& c, const Tile& t, int kb, const Where<NT>& p) __attribute__((always_inline)) {
+    auto step = [&](Codes<G, NT>& c, const Tile& t, int kb, const Where<NT>& p) __attribute__((always_inline)) {
         const int c0 = (kb * W + wave) * U, n = min(U, chunks - c0);
         if (have != t.row0 || blocks > 1) {
             if (have != t.row0) {
@@ -616,9 +625,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
 #pragma unroll
             for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
         }
-        product<G, NT, P>(acc, x, c, turn[wave], z8, n, cv,
-                          [&](int v) __attribute__((always_inline)) { load_pair(c, p, v, K); },
-                          [&](int i) __attribute__((always_inline)) { load_scales(c, p, i); });
+        product<G, NT>(acc, x, c, turn[wave], z8, n, cv, [&]() __attribute__((always_inline)) { load_pair(c, p, K); },
+                       [&](int i) __attribute__((always_inline)) { load_scales(c, p, i); });
         if (kb + 1 < blocks) return;
         if (threadIdx.x < 16) ok[buf][m] = in;
         put_acc<NT>(red + buf * W, acc);
@@ -637,7 +645,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2))
         buf ^= 1;
     };
     // a chunk's registers take the next step's codes as soon as they are used
-    Codes<G, NT, P> codes;
+    Codes<G, NT> codes;
     Tile t = tile_at(first), tn = t;
     load_all(codes, where(t, 0, true), K);
     for (int s = 0, at = first, kb = 0; s < steps; ++s) {
@@ -764,7 +772,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
-    Codes<G, NT, 1> w;
+    Codes<G, NT> w;
     uint32_t sz[NT][4];
     const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
     const Conv cv = conv();
@@ -795,8 +803,8 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
             load_scales(w, where_of<G>(wb, row0, c + 2 - u, K, live), u * GC / 4);
         }
         if (u == 0) {
-            put_pair(turn[wave], w, 0);
-            load_pair(w, where_of<G>(wb, row0, c + 2, K, live), 0, K);
+            put_pair(turn[wave], w);
+            load_pair(w, where_of<G>(wb, row0, c + 2, K, live), K);
         }
         uint4 q[NT];
 #pragma unroll
@@ -906,6 +914,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
 }
 
 // ---------------------------------------------------------------- one row at a time
+constexpr int kTokenWaves = 8;
 // A single row of x has no use for a matrix instruction.  Here a lane multiplies the codes where they arrive: eight
 // neighbouring lanes have 256 consecutive codes of a row, 32 each, the same 32 of every row that passes, so that the
 // lane's x stay in registers; a wave instruction is eight rows x 128 bytes.  Two products an instruction
@@ -992,10 +1001,10 @@ __device__ __forceinline__ int expert_of(const Int4Ffn& a, int64_t p, bool flag)
 
 // h = a(g') u' of 16 columns for slot blockIdx.y: eight waves share K in slices of 256, two at a time
 template <int G>
-__global__ __launch_bounds__(64 * kWaves) void int4_gate_up_token_kernel(Int4Ffn a, uint16_t* __restrict__ h)
+__global__ __launch_bounds__(64 * kTokenWaves) void int4_gate_up_token_kernel(Int4Ffn a, uint16_t* __restrict__ h)
 {
     constexpr int U = 2;
-    __shared__ float red[kWaves][32];
+    __shared__ float red[kTokenWaves][32];
     const int64_t p = blockIdx.y;
     const int e = expert_of(a, p, blockIdx.x == 0);
     if (e < 0) return;
@@ -1007,7 +1016,7 @@ __global__ __launch_bounds__(64 * kWaves) void int4_gate_up_token_kernel(Int4Ffn
     const int row = blockIdx.x * 16 + (lane >> 3);
     const Conv cv = conv();
     float acc[4] = {};
-    for (int s0 = wave * U; s0 < slices; s0 += kWaves * U) {
+    for (int s0 = wave * U; s0 < slices; s0 += kTokenWaves * U) {
         Q32 q[U][4];
         X32 x[U];
 #pragma unroll
@@ -1034,7 +1043,7 @@ __global__ __launch_bounds__(64 * kWaves) void int4_gate_up_token_kernel(Int4Ffn
     if (threadIdx.x >= 16) return;
     float g = 0.0f, u = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < kTokenWaves; ++i) {
         g += red[i][threadIdx.x];
         u += red[i][16 + threadIdx.x];
     }
@@ -1048,10 +1057,10 @@ __global__ __launch_bounds__(64 * kWaves) void int4_gate_up_token_kernel(Int4Ffn
 // out[t] = sum_j topk_w_j (h_j W2[e_j]^T) of 16 columns of token blockIdx.y: the slices of all its slots are shared by
 // eight waves, three at a time, a slice's sum times its slot's weight, so that one sum over the waves is the combine
 template <int G>
-__global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h)
+__global__ __launch_bounds__(64 * kTokenWaves) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h)
 {
     constexpr int U = 3;
-    __shared__ float red[kWaves][16];
+    __shared__ float red[kTokenWaves][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t t = blockIdx.y;
     const int K = a.f, slices = (K + 255) / 256, items = a.k * slices;
@@ -1060,17 +1069,17 @@ __global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a,
     const int row = blockIdx.x * 16 + (lane >> 3);
     const Conv cv = conv();
     float acc[2] = {};
-    for (int i0 = wave; i0 < items; i0 += kWaves * U) {
+    for (int i0 = wave; i0 < items; i0 += kTokenWaves * U) {
         Q32 q[U][2];
         X32 x[U];
         float c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = min(i0 + u * kWaves, items - 1);
+            const int i = min(i0 + u * kTokenWaves, items - 1);
             const int j = i / slices;
             const int64_t p = t * a.k + j;
             const int e = expert_of(a, p, false);
-            const bool on = e >= 0 && i0 + u * kWaves < items;
+            const bool on = e >= 0 && i0 + u * kTokenWaves < items;
             c[u] = on ? a.topk_w[p] : 0.0f;
             const int k0 = (i - j * slices) * 256 + 32 * (lane & 7);
             const uint32_t past = on && k0 < K ? 0 : kPast;
@@ -1095,7 +1104,7 @@ __global__ __launch_bounds__(64 * kWaves) void int4_down_token_kernel(Int4Ffn a,
     if (threadIdx.x >= 16) return;
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) v += red[i][threadIdx.x];
+    for (int i = 0; i < kTokenWaves; ++i) v += red[i][threadIdx.x];
     a.out[t * a.d + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
 }
 
@@ -1146,33 +1155,23 @@ int cu_count()
     return n;
 }
 
-template <int G, class GateUp>
-void launch_rows(const Int4Ffn& a, GateUp, uint16_t* h, float* y, hipStream_t s)
+template <int G, bool UP>
+void launch_rows(const Int4Ffn& a, uint16_t* h, float* y, hipStream_t s)
 {
-    constexpr bool UP = GateUp::value;
-    const int N = UP ? a.f : a.d, K = UP ? a.d : a.f, chunks = (K + 127) / 128;
-    const int64_t R = (int64_t)a.T * a.k;
+    constexpr int NT = 2, COLS = UP ? 16 : 32;
+    const int N = UP ? a.f : a.d, K = UP ? a.d : a.f, need = (K + 255) / 256, W = need < kWaves ? need : kWaves;
+    const int64_t R = (int64_t)a.T * a.k, cus = cu_count();
     // tiles of up to 16 rows: no more than the rows, nor than the full ones and one of each expert
-    const int64_t mt = R < R / 16 + a.E ? R : R / 16 + a.E;
-    auto go = [&](auto P_, auto NC_, int waves_per_cu) {
-        constexpr int P = decltype(P_)::value, NC = decltype(NC_)::value, NT = UP ? 2 * NC : NC;
-        const int need = (chunks + 2 * P - 1) / (2 * P), W = need < kWaves ? need : kWaves;
-        const size_t lds = W * (sizeof(Turn<NT>) + 2 * NT * 1024);
-        const int64_t fit = (int64_t)(156 << 10) / (lds + 4 * kMaxExperts + 256), per_cu = fit < waves_per_cu / W ? fit : waves_per_cu / W;
-        const int64_t tiles = mt * ((N + 16 * NC - 1) / (16 * NC)), cap = cu_count() * (per_cu < 1 ? 1 : per_cu);
-        hipLaunchKernelGGL((int4_rows_kernel<G, P, NC, UP>), dim3((unsigned)(tiles < cap ? tiles : cap)), dim3(64 * W), lds, s,
-                           a, h, y);
-    };
-    // Up to 4096 codes of K are one step of eight waves with two pairs of chunks each; up to 2048, one pair each, so
-    // that the workgroup has eight waves there too.  More columns a tile where registers allow it, as many workgroups
-    // as fit.  (The down product of the example above, K = 1536: all of one or two pairs, one to four column tiles and
-    // one to three workgroups a CU take 85 to 94 us, this choice 88.)
-    using std::integral_constant;
-    if (chunks > 2 * kWaves) {
-        go(integral_constant<int, 2>{}, integral_constant<int, UP ? 1 : 2>{}, 8);
-    } else {
-        go(integral_constant<int, 1>{}, integral_constant<int, UP ? 1 : 3>{}, 12);
-    }
+    const int64_t mt = R < R / 16 + a.E ? R : R / 16 + a.E, tiles = mt * ((N + COLS - 1) / COLS);
+    // As many workgroups as fit, 16 waves a CU (64 experts of d 2048, f 1024, 48 tokens of 4: 61 us a pass; with 12 waves
+    // 69); 12 where a workgroup would have fewer than two tiles (8 experts, 48 tokens of 2: 27 us; with 16 waves 28.5).
+    int64_t per_cu = kWaves / W;
+    if (tiles < 2 * cus * per_cu) per_cu = kWaves * 3 / 4 / W;
+    const size_t lds = W * (sizeof(Turn<NT>) + 2 * NT * 1024);
+    const int64_t fit = (int64_t)(156 << 10) / (lds + 4 * kMaxExperts + 256);
+    per_cu = per_cu < 1 ? 1 : per_cu < fit ? per_cu : fit;
+    hipLaunchKernelGGL((int4_rows_kernel<G, UP>), dim3((unsigned)(tiles < cus * per_cu ? tiles : cus * per_cu)), dim3(64 * W),
+                       lds, s, a, h, y);
 }
 
 template <int G>
@@ -1286,18 +1285,16 @@ hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
     if (R <= kTokenSlots && 2 * R <= 3 * a.E) {
         return with_group(a.group, [&](auto g) {
             constexpr int G = decltype(g)::value;
-            hipLaunchKernelGGL((int4_gate_up_token_kernel<G>), dim3(a.f / 16, (unsigned)R), dim3(64 * kWaves), 0, s, a, h);
-            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), dim3(64 * kWaves), 0, s, a, h);
+            hipLaunchKernelGGL((int4_gate_up_token_kernel<G>), dim3(a.f / 16, (unsigned)R), dim3(64 * kTokenWaves), 0, s, a, h);
+            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), dim3(64 * kTokenWaves), 0, s, a, h);
         });
     }
-    using Up = std::true_type;
-    using Down = std::false_type;
     if (R >= (int64_t)kTileMinRows * a.E) {
         e = with_group(a.group, [&](auto g) { launch_tiles<decltype(g)::value>(a, h, hsum, y, s); });
     } else {
         e = with_group(a.group, [&](auto g) {
-            launch_rows<decltype(g)::value>(a, Up{}, h, y, s);
-            launch_rows<decltype(g)::value>(a, Down{}, h, y, s);
+            launch_rows<decltype(g)::value, true>(a, h, y, s);
+            launch_rows<decltype(g)::value, false>(a, h, y, s);
         });
     }
     if (e != hipSuccess) return e;

@@ -483,3 +483,11 @@ def test_the_widest_rows(moe, T):
     _say("int4 wide rows", T)
     x, r, w, out = _big(moe, T, 2, 2 ** 20, 1024, 2 if T < 20 else 1, 128)
     _big_check(x, r, w, out, sorted({0, T // 2, T - 1}))
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,d,f", [(12, 3200, 2688), (30, 2176, 3712), (9, 4096, 1152), (20, 640, 1920)])
+def test_workgroups_of_every_length(moe, T, d, f, group):
+    """K shared by 3 to 16 waves, one step a tile."""
+    c = Ffn(moe, T, 3, d, f, 2, group, True, seed=T)
+    c.check(c.run())

@@ -1195,20 +1195,20 @@ void launch_tiles(const Int4Ffn& a, uint16_t* h, float* hsum, float* y, hipStrea
     go(std::false_type{}, h, hsum);
 }
 
-// Which kernels.  Times of a whole pass, us, in a graph; A: d 4096, f 1536, top-4 of 128; B: d 2048, f 1024, top-2 of 8.
+// Which kernels.  Times of a whole pass, us, in a graph; A: d 4096, f 1536, top-4 of 128; B: d 2048, f 1024, 8 experts;
+// C: d 2048, f 1408, top-6 of 64; D: d 5120, f 2560, top-2 of 16.
 // Slot by slot or rows together: a slot by itself reads its expert's matrices once more, which costs nothing while
-// few slots share one.
-//   slots      A: 32  48  64      B: 8   12
-//   by slot       75  106 147        22  26
-//   rows          87  109 138        25  25
-// so up to 32 slots, and up to one and a half an expert (B's 8 are 1 an expert, 12 are 1.5; with top-4
-// of its 8 experts 16 slots take 27 and 28).
+// few slots share one, or the second reading is from a cache.
+//   slots      A: 16  32  48  64      B, top-2: 8  12  16    B, top-4: 16  24      C: 30  48      D: 32
+//   by slot       40  68  95 122             17  21  24              21  26         43  60        125
+//   rows          49  76 100 118             22  23  23              23  24         51  63        103
+// so up to 48 slots, and up to one and a half an expert.
 // Tiles of 16 or of 64 rows: with 16, each tile reads its matrices anew, from the caches.
 //   rows an expert   A: 16  24  32      B: 32  48  64
 //   tiles of 16         389 484 656        39  46  54
 //   tiles of 64         458 470 485        44  45  46
 // so tiles of 64 from 32 rows an expert on.
-constexpr int kTokenSlots = 32, kTileMinRows = 32;
+constexpr int kTokenSlots = 48, kTileMinRows = 32;
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 

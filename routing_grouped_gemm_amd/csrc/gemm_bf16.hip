@@ -1091,22 +1091,11 @@ __global__ __launch_bounds__(64 * kRW) void router_logits_kernel(const uint16_t*
         }
 }
 
-template <int BM, int BK, int NS, bool B_MN, int EPI, int NW>
-hipError_t launch_m(const MParams& p, int64_t n_rows, hipStream_t s)
-{
-    // host-known bound on the M-tiles: sum ceil(m_e / BM) <= n_rows / BM + E
-    const int64_t bound = (n_rows / BM + p.E) * (int64_t)p.ntn;
-    const int64_t grid = (bound + 7) / 8 * 8;
-    if (grid == 0) return hipSuccess;
-    // K a multiple of BK: the main loop needs no K-tail tests
-    if (p.K % BK == 0)
-        hipLaunchKernelGGL((gemm_grouped_m_kernel<BM, BK, NS, B_MN, EPI, NW, true>), dim3((unsigned)grid),
-                           dim3(64 * NW), 0, s, p);
-    else
-        hipLaunchKernelGGL((gemm_grouped_m_kernel<BM, BK, NS, B_MN, EPI, NW, false>), dim3((unsigned)grid),
-                           dim3(64 * NW), 0, s, p);
-    return hipGetLastError();
-}
+constexpr int kBM = 256;   // M tile of the grouped-M (forward / dgrad) GEMMs
+constexpr int kBMK = 256;  // M tile of the grouped-K (weight gradient) GEMM
+constexpr int kBK = 64;    // K step
+constexpr int kNS = 2;     // LDS pipeline stages
+constexpr int kNW = 8;     // waves per workgroup (two per SIMD)
 
 // workgroups of a persistent launch: one per CU of the current device
 // (a multiple of 8, so that every XCD's tile list has workgroups)
@@ -1117,6 +1106,32 @@ int persistent_grid()
         hipDeviceGetAttribute(&ncu, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || ncu < 8)
         ncu = 256;
     return ncu / 8 * 8;
+}
+
+// Tiles of 64 rows (the same sums in the same order) where even those are no more than a little over one a CU: a
+// launch then lasts as long as one tile does.  Gradient through the gate, 8 experts, d 2048, f 1152, us with tiles of 64
+// and of 256: 1000 rows 24 and 54, 2003 rows 25 and 57; gate and up products of 2003 rows, 312 tiles at most, 42 and 46,
+// of 4000, 630, 68 and 53; 16 experts, d 4096, 1000 rows, 372, 127 and 101.  The bound counts half a tile an expert too
+// many, so it may pass the CUs by a quarter.
+template <bool B_MN, int EPI>
+hipError_t launch_m(const MParams& p, int64_t n_rows, hipStream_t s)
+{
+    auto go = [&](auto BM_, auto NS_, auto KAL_) {
+        constexpr int BM = decltype(BM_)::value;
+        // host-known bound on the M-tiles: sum ceil(m_e / BM) <= n_rows / BM + E
+        const int64_t bound = (n_rows / BM + p.E) * (int64_t)p.ntn;
+        const int64_t grid = (bound + 7) / 8 * 8;
+        if (grid == 0) return hipSuccess;
+        hipLaunchKernelGGL((gemm_grouped_m_kernel<BM, kBK, decltype(NS_)::value, B_MN, EPI, kNW, decltype(KAL_)::value>),
+                           dim3((unsigned)grid), dim3(64 * kNW), 0, s, p);
+        return hipGetLastError();
+    };
+    using std::integral_constant;
+    // K a multiple of BK: the main loop needs no K-tail tests
+    if (p.K % kBK) return go(integral_constant<int, kBM>{}, integral_constant<int, kNS>{}, std::false_type{});
+    if ((n_rows / 64 + p.E) * (int64_t)p.ntn * 4 <= persistent_grid() * (int64_t)5)
+        return go(integral_constant<int, 64>{}, integral_constant<int, tail_stages<64>()>{}, std::true_type{});
+    return go(integral_constant<int, kBM>{}, integral_constant<int, kNS>{}, std::true_type{});
 }
 
 template <int BM, int BK, int NS, int NW>
@@ -1148,12 +1163,6 @@ hipError_t launch_k(const KParams& p, hipStream_t s)
     }
     return hipGetLastError();
 }
-
-constexpr int kBM = 256;   // M tile of the grouped-M (forward / dgrad) GEMMs
-constexpr int kBMK = 256;  // M tile of the grouped-K (weight gradient) GEMM
-constexpr int kBK = 64;    // K step
-constexpr int kNS = 2;     // LDS pipeline stages
-constexpr int kNW = 8;     // waves per workgroup (two per SIMD)
 
 }  // namespace
 
@@ -1191,8 +1200,8 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const Gl
         p.ldc = 2 * f;
         p.H = (uint16_t*)t.h;
         p.ldh = f;
-        if (!plain) return launch_m<kBM, kBK, kNS, false, EPI_GLU_FWD, kNW>(p, g.n_rows, s);
-        return launch_m<kBM, kBK, kNS, false, EPI_SWIGLU_FWD, kNW>(p, g.n_rows, s);
+        if (!plain) return launch_m<false, EPI_GLU_FWD>(p, g.n_rows, s);
+        return launch_m<false, EPI_SWIGLU_FWD>(p, g.n_rows, s);
     case MOE_GEMM_DOWN:  // y = h Wd^T
         p.A = (const uint16_t*)t.h;
         p.lda = f;
@@ -1204,7 +1213,7 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const Gl
         p.ntn = (d + BN - 1) / BN;
         p.C = (uint16_t*)t.y_perm;
         p.ldc = d;
-        return launch_m<kBM, kBK, kNS, false, EPI_STORE, kNW>(p, g.n_rows, s);
+        return launch_m<false, EPI_STORE>(p, g.n_rows, s);
     case MOE_GEMM_DGRAD_DOWN:  // dh = dy Wd (Wd_e stored [d, f] = [K, N]), SwiGLU backward
         p.A = (const uint16_t*)t.dy_perm;
         p.lda = d;
@@ -1218,8 +1227,8 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const Gl
         p.ldc = 2 * f;
         p.G = (const uint16_t*)t.gu;
         p.ldg = 2 * f;
-        if (!plain) return launch_m<kBM, kBK, kNS, true, EPI_GLU_BWD, kNW>(p, g.n_rows, s);
-        return launch_m<kBM, kBK, kNS, true, EPI_SWIGLU_BWD, kNW>(p, g.n_rows, s);
+        if (!plain) return launch_m<true, EPI_GLU_BWD>(p, g.n_rows, s);
+        return launch_m<true, EPI_SWIGLU_BWD>(p, g.n_rows, s);
     case MOE_GEMM_DGRAD_GATE_UP:  // dx = [dg | du] [Wg ; Wu] (W13_e stored [2f, d] = [K, N])
         p.A = (const uint16_t*)t.dgu;
         p.lda = 2 * f;
@@ -1231,7 +1240,7 @@ hipError_t gemm_op_bf16(int op, const moe_gemm_tensors& t, GroupSpec g, const Gl
         p.ntn = (d + BN - 1) / BN;
         p.C = (uint16_t*)t.dx_perm;
         p.ldc = d;
-        return launch_m<kBM, kBK, kNS, true, EPI_STORE, kNW>(p, g.n_rows, s);
+        return launch_m<true, EPI_STORE>(p, g.n_rows, s);
     case MOE_GEMM_WGRAD: {  // dWd_e [d, f] = dy_e^T h_e ; dW13_e [2f, d] = dgu_e^T x_e
         KParams k{};
         k.group_off = g.group_off;

@@ -273,3 +273,45 @@ def test_two_streams_at_once(moe):
     torch.cuda.synchronize()
     for b in bs:
         b.check()
+
+
+@pytest.mark.parametrize("d,f", [(64, 5120), (5120, 64)])
+def test_tiles_of_large_launches(moe, d, f):
+    """Enough tiles for the tallest ones, with every height of a group's last one."""
+    _say("large", d, f)
+    b = Block(moe, [300, 64, 128, 513, 0, 40], d, f, BF, "gelu_tanh", 1.5, 0.2, seed=6)
+    b.forward()
+    b.backward()
+    b.check()
+
+
+@pytest.mark.parametrize("d,f", [(512, 1024), (1024, 448), (448, 1152)])
+@pytest.mark.parametrize("plain", [False, True])
+def test_a_group_alone_has_the_same_bits(moe, d, f, plain):
+    """The height of a launch's tiles changes no bit: a group by itself, and sixteen times over."""
+    m, E, n = moe, 16, 333
+    _say("alone", d, f, plain)
+    g = torch.Generator(DEV).manual_seed(3)
+
+    def make(*shape, s=1.0):
+        return (torch.randn(*shape, generator=g, device=DEV) * s).to(BF)
+    one = dict(x_perm=make(n, d), dy_perm=make(n, d), w13=make(1, 2 * f, d, s=d ** -0.5), w2=make(1, d, f, s=f ** -0.5))
+    gate = m.glu() if plain else m.glu(m.MOE_ACT_GELU, 1.0)      # (a mask is the row's, and these are other rows)
+    outs = []
+    for reps in (1, E):
+        t = {k: v.repeat(reps, *[1] * (v.dim() - 1)).contiguous() for k, v in one.items()}
+        R = n * reps
+        t.update({k: torch.full((R, w), 7.0, dtype=BF, device=DEV)
+                  for k, w in (("gu", 2 * f), ("h", f), ("y_perm", d), ("dgu", 2 * f), ("dx_perm", d))})
+        off = torch.arange(0, R + 1, n, dtype=torch.int32, device=DEV)
+        args = m.gemm_tensors(**t)
+        for op in (m.MOE_GEMM_GATE_UP, m.MOE_GEMM_DOWN, m.MOE_GEMM_DGRAD_DOWN, m.MOE_GEMM_DGRAD_GATE_UP):
+            if plain:
+                m.moe_grouped_gemm_op(op, m.MOE_BF16, args, off, 0, reps, R, d, f)
+            else:
+                m.moe_grouped_glu_op(op, m.MOE_BF16, gate, args, off, 0, reps, R, d, f)
+        outs.append(t)
+    torch.cuda.synchronize()
+    for k in ("gu", "h", "y_perm", "dgu", "dx_perm"):
+        a, b = outs[0][k], outs[1][k].view(E, n, -1)
+        assert bool((a == b).all()), k

@@ -1110,9 +1110,9 @@ int persistent_grid()
 
 // Tiles of 64 rows (the same sums in the same order) where even those are no more than a little over one a CU: a
 // launch then lasts as long as one tile does.  Gradient through the gate, 8 experts, d 2048, f 1152, us with tiles of 64
-// and of 256: 1000 rows 24 and 54, 2003 rows 25 and 57; gate and up products of 2003 rows, 312 tiles at most, 42 and 46,
-// of 4000, 630, 68 and 53; 16 experts, d 4096, 1000 rows, 372, 127 and 101.  The bound counts half a tile an expert too
-// many, so it may pass the CUs by a quarter.
+// and of 256: 1000 rows 24 and 54, 2003 rows 25 and 57; 16 experts, d 4096, f 1536, 2003 rows, 282 tiles at most, 71 and
+// 100; the gate and up products' gradient of the first, 312, 43 to 57 by how the rows fall and 46 to 50; 16 experts, 1000
+// rows, 372, 127 and 101.  The bound counts half a tile an expert too many, so it may pass the CUs by an eighth.
 template <bool B_MN, int EPI>
 hipError_t launch_m(const MParams& p, int64_t n_rows, hipStream_t s)
 {
@@ -1129,7 +1129,7 @@ hipError_t launch_m(const MParams& p, int64_t n_rows, hipStream_t s)
     using std::integral_constant;
     // K a multiple of BK: the main loop needs no K-tail tests
     if (p.K % kBK) return go(integral_constant<int, kBM>{}, integral_constant<int, kNS>{}, std::false_type{});
-    if ((n_rows / 64 + p.E) * (int64_t)p.ntn * 4 <= persistent_grid() * (int64_t)5)
+    if ((n_rows / 64 + p.E) * (int64_t)p.ntn * 8 <= persistent_grid() * (int64_t)9)
         return go(integral_constant<int, 64>{}, integral_constant<int, tail_stages<64>()>{}, std::true_type{});
     return go(integral_constant<int, kBM>{}, integral_constant<int, kNS>{}, std::true_type{});
 }

@@ -51,13 +51,13 @@ __device__ __forceinline__ float drop_factor(const DropSpec& dr, PhiloxKey key, 
     return ((j & 1) ? keep_hi(r, dr.thr) : keep_lo(r, dr.thr)) ? dr.scale : 0.0f;
 }
 
-// Bound by latency at the sizes this path is for, so the next K-step's operands are on their way in registers
-// while one is multiplied, and two LDS stages leave one barrier a K-step (512 rows of 8 experts, d = 128, f = 256:
-// 12 and 15 us for the two forward stages; 64 x 64 tiles with loads between the barriers took 24 and 38).
+// Bound by latency at the sizes this path is for, so the next four K-steps' operands are on their way in registers
+// while one is multiplied, and two LDS stages leave one barrier a K-step (512 rows of 8 experts, d = 128, f = 256: 12 and
+// 10 us for the two forward stages; one K-step ahead 12.5 and 14, 64 x 64 tiles with loads between the barriers 24 and 38).
 template <int EPI, int T>
 __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
 {
-    constexpr int TM = T, TN = T, M = T / 16, TK = 1024 / T;
+    constexpr int TM = T, TN = T, M = T / 16, TK = 1024 / T, D = 4;
     __shared__ __align__(16) float sA[2][TK][TM + 4];
     __shared__ __align__(16) float sB[2][TK][TN + 4];
     __shared__ float sC[TM][TN + 1];
@@ -86,7 +86,8 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
     // columns nb .. nb + 3.  K and N are multiples of 4, so a piece is inside or outside as a whole.
     const int r = tid / (TK / 4), k = 4 * (tid % (TK / 4));
     const int kb = tid / (TN / 4), nb = 4 * (tid % (TN / 4));
-    const float4 zero4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    typedef __attribute__((ext_vector_type(4))) float f32x4;
+    const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     int64_t brow = n0 + r;
     bool b_ok = brow < p.N;
     if (is_gate_up(EPI)) {
@@ -94,22 +95,22 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
         b_ok = n < p.f;
         brow = r < TN / 2 ? n : p.f + n;
     }
-    float4 a4, b4;
-    auto load = [&](int k0) {
-        a4 = r < rows_valid && k0 + k < p.K ? *reinterpret_cast<const float4*>(p.A + (row0 + r) * p.lda + k0 + k) : zero4;
+    f32x4 ar[D], br[D];
+    auto load = [&](int k0, f32x4& a4, f32x4& b4) __attribute__((always_inline)) {
+        a4 = r < rows_valid && k0 + k < p.K ? *reinterpret_cast<const f32x4*>(p.A + (row0 + r) * p.lda + k0 + k) : zero4;
         if (p.b_mn)
-            b4 = k0 + kb < p.K && n0 + nb < p.N ? *reinterpret_cast<const float4*>(Be + (int64_t)(k0 + kb) * p.ldb + n0 + nb)
+            b4 = k0 + kb < p.K && n0 + nb < p.N ? *reinterpret_cast<const f32x4*>(Be + (int64_t)(k0 + kb) * p.ldb + n0 + nb)
                                                 : zero4;
         else
-            b4 = b_ok && k0 + k < p.K ? *reinterpret_cast<const float4*>(Be + brow * p.ldb + k0 + k) : zero4;
+            b4 = b_ok && k0 + k < p.K ? *reinterpret_cast<const f32x4*>(Be + brow * p.ldb + k0 + k) : zero4;
     };
-    auto store = [&](int st) {
+    auto store = [&](int st, f32x4 a4, f32x4 b4) __attribute__((always_inline)) {
         sA[st][k][r] = a4.x;
         sA[st][k + 1][r] = a4.y;
         sA[st][k + 2][r] = a4.z;
         sA[st][k + 3][r] = a4.w;
         if (p.b_mn) {
-            *reinterpret_cast<float4*>(&sB[st][kb][nb]) = b4;
+            *reinterpret_cast<f32x4*>(&sB[st][kb][nb]) = b4;
         } else {
             sB[st][k][r] = b4.x;
             sB[st][k + 1][r] = b4.y;
@@ -118,22 +119,27 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
         }
     };
     float acc[M][M] = {};
-    load(0);
-    for (int k0 = 0, st = 0; k0 < p.K; k0 += TK, st ^= 1) {
-        store(st);
-        __syncthreads();
-        load(k0 + TK);
 #pragma unroll
-        for (int kk = 0; kk < TK; ++kk) {
-            float a[M], b[M];
+    for (int d = 0; d < D; ++d) load(d * TK, ar[d], br[d]);
+    for (int k0 = 0; k0 < p.K; k0 += D * TK) {
 #pragma unroll
-            for (int i = 0; i < M; ++i) a[i] = sA[st][kk][ty * M + i];
+        for (int d = 0; d < D; ++d) {
+            if (k0 + d * TK >= p.K) break;
+            store(d & 1, ar[d], br[d]);
+            __syncthreads();
+            load(k0 + (D + d) * TK, ar[d], br[d]);
 #pragma unroll
-            for (int j = 0; j < M; ++j) b[j] = sB[st][kk][tx * M + j];
+            for (int kk = 0; kk < TK; ++kk) {
+                float a[M], b[M];
 #pragma unroll
-            for (int i = 0; i < M; ++i)
+                for (int i = 0; i < M; ++i) a[i] = sA[d & 1][kk][ty * M + i];
 #pragma unroll
-                for (int j = 0; j < M; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < M; ++j) b[j] = sB[d & 1][kk][tx * M + j];
+#pragma unroll
+                for (int i = 0; i < M; ++i)
+#pragma unroll
+                    for (int j = 0; j < M; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+            }
         }
     }
 #pragma unroll

@@ -13,6 +13,7 @@ namespace moe {
 namespace {
 
 constexpr int TM = 64, TN = 64, TK = 16;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 // GLU: the gate, limit and dropout given at run time (F32M::glu)
 enum { EPI_STORE = 0, EPI_SWIGLU_FWD = 1, EPI_SWIGLU_BWD = 2, EPI_GLU_FWD = 3, EPI_GLU_BWD = 4 };
@@ -86,7 +87,6 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
     // columns nb .. nb + 3.  K and N are multiples of 4, so a piece is inside or outside as a whole.
     const int r = tid / (TK / 4), k = 4 * (tid % (TK / 4));
     const int kb = tid / (TN / 4), nb = 4 * (tid % (TN / 4));
-    typedef __attribute__((ext_vector_type(4))) float f32x4;
     const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
     int64_t brow = n0 + r;
     bool b_ok = brow < p.N;
@@ -95,14 +95,15 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
         b_ok = n < p.f;
         brow = r < TN / 2 ? n : p.f + n;
     }
+    const uint32_t K = p.K;          // (a step past it fits 32 bits)
     f32x4 ar[D], br[D];
-    auto load = [&](int k0, f32x4& a4, f32x4& b4) __attribute__((always_inline)) {
-        a4 = r < rows_valid && k0 + k < p.K ? *reinterpret_cast<const f32x4*>(p.A + (row0 + r) * p.lda + k0 + k) : zero4;
+    auto load = [&](uint32_t k0, f32x4& a4, f32x4& b4) __attribute__((always_inline)) {
+        a4 = r < rows_valid && k0 + k < K ? *reinterpret_cast<const f32x4*>(p.A + (row0 + r) * p.lda + k0 + k) : zero4;
         if (p.b_mn)
-            b4 = k0 + kb < p.K && n0 + nb < p.N ? *reinterpret_cast<const f32x4*>(Be + (int64_t)(k0 + kb) * p.ldb + n0 + nb)
+            b4 = k0 + kb < K && n0 + nb < p.N ? *reinterpret_cast<const f32x4*>(Be + (int64_t)(k0 + kb) * p.ldb + n0 + nb)
                                                 : zero4;
         else
-            b4 = b_ok && k0 + k < p.K ? *reinterpret_cast<const f32x4*>(Be + brow * p.ldb + k0 + k) : zero4;
+            b4 = b_ok && k0 + k < K ? *reinterpret_cast<const f32x4*>(Be + brow * p.ldb + k0 + k) : zero4;
     };
     auto store = [&](int st, f32x4 a4, f32x4 b4) __attribute__((always_inline)) {
         sA[st][k][r] = a4.x;
@@ -121,10 +122,10 @@ __global__ __launch_bounds__(256) void f32_grouped_m_kernel(F32M p)
     float acc[M][M] = {};
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d * TK, ar[d], br[d]);
-    for (int k0 = 0; k0 < p.K; k0 += D * TK) {
+    for (uint32_t k0 = 0; k0 < K; k0 += D * TK) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
-            if (k0 + d * TK >= p.K) break;
+            if (k0 + d * TK >= K) break;
             store(d & 1, ar[d], br[d]);
             __syncthreads();
             load(k0 + (D + d) * TK, ar[d], br[d]);
@@ -216,10 +217,13 @@ struct F32K {
     int64_t n_rows;
 };
 
+// The weight gradients, K the group's rows: the same loop, 64 x 64 tiles (a layer's backward, us, with loads between the
+// barriers and so: 2100 rows of 5 experts, d 132, f 68, 104 and 69; 6000 of 8, d = f = 512, 380 and 316)
 __global__ __launch_bounds__(256) void f32_grouped_k_kernel(F32K p)
 {
-    __shared__ float sA[TK][TM + 4];
-    __shared__ float sB[TK][TN + 4];
+    constexpr int D = 4;
+    __shared__ __align__(16) float sA[2][TK][TM + 4];
+    __shared__ __align__(16) float sB[2][TK][TN + 4];
     const int t0 = p.pr[0].mtn * p.pr[0].ntn;
     const int tiles_e = t0 + (p.nprob > 1 ? p.pr[1].mtn * p.pr[1].ntn : 0);
     const int L = blockIdx.x;
@@ -230,41 +234,51 @@ __global__ __launch_bounds__(256) void f32_grouped_k_kernel(F32K p)
     const F32KProblem& q = p.pr[which];
     const int mt = local / q.ntn, nt = local - (local / q.ntn) * q.ntn;
     const int64_t g0 = group_begin(p.group_off, p.capacity, e, p.n_rows);
-    const int m_e = (int)group_rows(p.group_off, p.capacity, e, p.n_rows);
+    const uint32_t m_e = (uint32_t)group_rows(p.group_off, p.capacity, e, p.n_rows);     // (a step past it fits 32 bits)
     const int m0 = mt * TM, n0 = nt * TN;
     const int tid = threadIdx.x;
     const int tx = tid % 16, ty = tid / 16;
+    // one 16-byte piece of A and of B a thread and K-step (M and N are multiples of 4: inside or outside as a whole)
+    const int kr = tid / 16, c = 4 * (tid % 16);
+    const bool a_ok = m0 + c < q.M, b_ok = n0 + c < q.N;
+    f32x4 ar[D], br[D];
+    auto load = [&](uint32_t k, f32x4& a4, f32x4& b4) __attribute__((always_inline)) {
+        const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+        a4 = a_ok && k < m_e ? *reinterpret_cast<const f32x4*>(q.A + (g0 + k) * q.lda + m0 + c) : zero4;
+        b4 = b_ok && k < m_e ? *reinterpret_cast<const f32x4*>(q.B + (g0 + k) * q.ldb + n0 + c) : zero4;
+    };
     float acc[4][4] = {};
-    for (int k0 = 0; k0 < m_e; k0 += TK) {
-        for (int idx = tid; idx < TM * TK; idx += 256) {
-            const int kk = idx / TM, c = idx % TM;
-            const int k = k0 + kk;
-            sA[kk][c] = (k < m_e && m0 + c < q.M) ? q.A[(g0 + k) * q.lda + m0 + c] : 0.0f;
-            sB[kk][c] = (k < m_e && n0 + c < q.N) ? q.B[(g0 + k) * q.ldb + n0 + c] : 0.0f;
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d * TK + kr, ar[d], br[d]);
+    for (uint32_t k0 = 0; k0 < m_e; k0 += D * TK) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            if (k0 + d * TK >= m_e) break;
+            *reinterpret_cast<f32x4*>(&sA[d & 1][kr][c]) = ar[d];
+            *reinterpret_cast<f32x4*>(&sB[d & 1][kr][c]) = br[d];
+            __syncthreads();
+            load(k0 + (D + d) * TK + kr, ar[d], br[d]);
+#pragma unroll
+            for (int kk = 0; kk < TK; ++kk) {
+                float a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = sA[d & 1][kk][ty * 4 + i];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = sB[d & 1][kk][tx * 4 + j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+            }
         }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < TK; ++kk) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = sA[kk][ty * 4 + i];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = sB[kk][tx * 4 + j];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-        }
-        __syncthreads();
     }
     float* Ce = q.C + (int64_t)e * q.sC;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m < q.M && n < q.N) Ce[(int64_t)m * q.ldc + n] = acc[i][j];
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ty * 4 + i, n = n0 + tx * 4;
+        if (m < q.M && n < q.N)
+            *reinterpret_cast<f32x4*>(Ce + (int64_t)m * q.ldc + n) = f32x4{acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    }
 }
 
 template <int EPI>

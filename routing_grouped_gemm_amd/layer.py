@@ -191,20 +191,26 @@ class MoELayer:
         moe_dequantize_mxfp4(self.w2_q.view(E * d, -1), self.w2_s.view(E * d, -1), self.w2_d.view(E * d, f))
 
     # -------------------------------------------------------------- weights
+    def _check_held(self, name, w, n, dtype, dense=True):
+        # the kernels read n elements at w's address, whatever its shape
+        if w.dtype is not dtype or w.numel() != n or w.device != self.out.device or (dense and not w.is_contiguous()):
+            raise ValueError(f"{name}: expected a {'contiguous ' if dense else ''}{dtype} tensor of {n} elements on "
+                             f"{self.out.device}, got {w.dtype} {tuple(w.shape)} with strides {w.stride()} on {w.device}")
+
     def set_weights(self, w13, w2):
-        """Weights [E, 2f, d] and [E, d, f] (MOE_F32: fp32, otherwise bf16).  For MXFP8
+        """Weights [E, 2f, d] and [E, d, f] (MOE_F32: fp32, otherwise bf16) on the
+        layer's device; refused ones leave the layer with those it had.  For MXFP8
         the forward and backward MXFP8 caches are made here (once per optimizer
-        step), for MXFP4 the codes of both; MXFP4 weights that are refused leave
-        the layer with the ones it had.  Each call makes new caches and a captured
+        step), for MXFP4 the codes of both.  Each call makes new caches and a captured
         graph reads those of its capture: for weights that change under a graph,
         write them into w13 and w2 and call requantize_weights, which works in place.
         INT4: the codes are made here, and the bf16 weights are not kept."""
+        E, f, d = self.G, self.f, self.d
+        # (the quantisers are given a dense copy of weights that are not)
+        dense = self.dtype in (MOE_F32, MOE_BF16)
+        self._check_held("w13", w13, E * 2 * f * d, _ACT[self.dtype], dense)
+        self._check_held("w2", w2, E * d * f, _ACT[self.dtype], dense)
         if self.dtype == MOE_MXFP4:
-            E, f, d = self.G, self.f, self.d
-            for name, w, n in (("w13", w13, E * 2 * f * d), ("w2", w2, E * d * f)):
-                if w.dtype is not torch.bfloat16 or w.numel() != n or w.get_device() != self.x_perm.get_device():
-                    raise ValueError(f"{name}: expected a torch.bfloat16 tensor of {n} elements on {self.x_perm.device}, "
-                                     f"got {w.dtype} {tuple(w.shape)} on {w.device}")
             u8 = dict(dtype=torch.uint8, device=self.device)
             codes = (torch.empty(E, 2 * f, d // 2, **u8), torch.empty(E, 2 * f, d // 32, **u8),
                      torch.empty(E, d, f // 2, **u8), torch.empty(E, d, f // 32, **u8))
@@ -215,11 +221,7 @@ class MoELayer:
                 self._decode_weights()
             return
         if self.dtype == MOE_INT4:
-            E, f, d, g = self.G, self.f, self.d, self.group
-            for name, w, n in (("w13", w13, E * 2 * f * d), ("w2", w2, E * d * f)):
-                if w.dtype is not torch.bfloat16 or w.numel() != n or w.get_device() != self.out.get_device():
-                    raise ValueError(f"{name}: expected a torch.bfloat16 tensor of {n} elements on {self.out.device}, "
-                                     f"got {w.dtype} {tuple(w.shape)} on {w.device}")
+            g = self.group
             made = []
             for w, N, K in ((w13, 2 * f, d), (w2, d, f)):
                 u8 = dict(dtype=torch.uint8, device=self.device)
@@ -235,7 +237,6 @@ class MoELayer:
         self._stages = None
         if self.dtype != MOE_MXFP8:
             return
-        E, f, d = self.G, self.f, self.d
         dev = self.device
         u8 = dict(dtype=torch.uint8, device=dev)
         # forward direction: blocks along the contraction dim of each GEMM
@@ -262,6 +263,10 @@ class MoELayer:
         steps, so the backward decodes them each time it runs."""
         if self.dtype != MOE_MXFP4:
             raise ValueError("set_weights_mxfp4 needs an MXFP4 layer")
+        n13, n2 = self.G * 2 * self.f * self.d, self.G * self.d * self.f
+        for name, w, n in (("w13_q", w13_q, n13 // 2), ("w13_s", w13_s, n13 // 32), ("w2_q", w2_q, n2 // 2),
+                           ("w2_s", w2_s, n2 // 32)):
+            self._check_held(name, w, n, torch.uint8)
         self.w13_q, self.w13_s, self.w2_q, self.w2_s = w13_q, w13_s, w2_q, w2_s
         self.w13 = self.w2 = None   # these codes have no bf16 weights behind them
         self._stages = None

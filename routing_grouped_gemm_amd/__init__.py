@@ -188,6 +188,30 @@ def _dense(name, t, dtype, *shape):
     return t.data_ptr()
 
 
+def _array(name, t, dtype, n):
+    """The data pointer of t (None: NULL; a device pointer passes) after checking that it is a dense `dtype`
+    tensor, of whatever shape, of the n elements at least that a kernel reads or writes there."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} elements, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _byte_array(name, t, n):
+    """_array of n bytes in any one-byte type (8-bit codes and scales)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != 1 or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of {n} bytes, got {t.dtype} {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
+    return t.data_ptr()
+
+
+_I32 = torch.int32
+
+
 def _call(name, stream, tensors, *args):
     """The C entry point `name` on `stream` (None: the current one of the tensors' device), with that
     device current; `tensors` must be on one GPU.  The stream is the last argument."""
@@ -195,7 +219,7 @@ def _call(name, stream, tensors, *args):
     if dev < 0:
         raise ValueError(f"{name}: expected tensors on a GPU, got one on {tensors[0].device}")
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is not None and not isinstance(t, int) and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
     fn = getattr(load(), name)
     if dev == torch.cuda.current_device():
@@ -220,16 +244,21 @@ def moe_route_workspace_bytes(T, E, k):
     return int(load().moe_route_workspace_bytes(T, E, k))
 
 
+def _route_args(logits, k, capacity, topk_idx, topk_w, counts, offsets, dst_row, src_slot):
+    T, E = logits.shape
+    return (_array("logits", logits, torch.float32, T * E), T, E, k, capacity, _array("topk_idx", topk_idx, _I32, T * k),
+            _array("topk_w", topk_w, torch.float32, T * k), _array("counts", counts, _I32, E),
+            _array("offsets", offsets, _I32, E + 1), _array("dst_row", dst_row, _I32, T * k),
+            _array("src_slot", src_slot, _I32, 0), src_slot.numel())
+
+
 def moe_route_topk(logits, k, capacity, topk_idx, topk_w, counts, offsets, dst_row, src_slot, ws,
                    dev_err=None, stream=None):
     """logits [T, E] fp32 -> topk_idx [T,k] i32, topk_w [T,k] f32, counts [E], offsets [E+1],
     dst_row [T*k], src_slot [n_rows] (n_rows = T*k, or E*capacity when padded)."""
-    T, E = logits.shape
-    n_rows = src_slot.numel()
-    rc = load().moe_route_topk(_p(logits), T, E, k, capacity, _p(topk_idx), _p(topk_w),
-                               _p(counts), _p(offsets), _p(dst_row), _p(src_slot), n_rows, _p(ws),
-                               _nbytes(ws), _p(dev_err), _s(stream))
-    _check(rc, "moe_route_topk")
+    _call("moe_route_topk", stream, (logits, topk_idx, topk_w, counts, offsets, dst_row, src_slot, ws, dev_err),
+          *_route_args(logits, k, capacity, topk_idx, topk_w, counts, offsets, dst_row, src_slot), _p(ws), _nbytes(ws),
+          _array("dev_err", dev_err, _I32, 1))
 
 
 ROUTE_NOALLOC_MAX_BYTES = 32 << 20    # MOE_ROUTE_NOALLOC_MAX_BYTES in moe.h
@@ -238,12 +267,9 @@ ROUTE_NOALLOC_MAX_BYTES = 32 << 20    # MOE_ROUTE_NOALLOC_MAX_BYTES in moe.h
 def moe_route_topk_noalloc(logits, k, capacity, topk_idx, topk_w, counts, offsets, dst_row, src_slot,
                            dev_err=None, stream=None):
     """moe_route_topk with the library's fixed per-GPU scratch instead of a workspace."""
-    T, E = logits.shape
-    n_rows = src_slot.numel()
-    rc = load().moe_route_topk_noalloc(_p(logits), T, E, k, capacity, _p(topk_idx), _p(topk_w),
-                                       _p(counts), _p(offsets), _p(dst_row), _p(src_slot), n_rows,
-                                       _p(dev_err), _s(stream))
-    _check(rc, "moe_route_topk_noalloc")
+    _call("moe_route_topk_noalloc", stream, (logits, topk_idx, topk_w, counts, offsets, dst_row, src_slot, dev_err),
+          *_route_args(logits, k, capacity, topk_idx, topk_w, counts, offsets, dst_row, src_slot),
+          _array("dev_err", dev_err, _I32, 1))
 
 
 def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_perm_scales=None,
@@ -264,13 +290,28 @@ def moe_permute(dtype, x, k, dst_row, x_perm, src_slot=None, row_scale=None, x_p
         return
     if torch.is_tensor(src_slot) and src_slot.numel() != n_rows:
         raise ValueError(f"src_slot: expected {n_rows} rows, as x_perm has, got {src_slot.numel()}")
-    rc = load().moe_permute(dtype, _p(x), T, d, k, _p(dst_row), _p(src_slot), _p(row_scale),
-                            n_rows, _p(x_perm), _p(x_perm_scales), _p(dev_err), _s(stream))
-    _check(rc, "moe_permute")
+    if dtype == MOE_MXFP8:
+        t, out, scales = torch.bfloat16, _byte_array("x_perm", x_perm, n_rows * d), \
+            _byte_array("x_perm_scales", x_perm_scales, n_rows * (d // 32))
+    else:
+        t = _float_type(dtype)
+        out, scales = _array("x_perm", x_perm, t, n_rows * d), _p(x_perm_scales)
+    _call("moe_permute", stream, (x, dst_row, x_perm, src_slot, row_scale, x_perm_scales, dev_err), dtype,
+          _array("x", x, t, T * d), T, d, k, _array("dst_row", dst_row, _I32, T * k),
+          _array("src_slot", src_slot, _I32, n_rows), _array("row_scale", row_scale, torch.float32, T * k), n_rows, out,
+          scales, _array("dev_err", dev_err, _I32, 1))
 
 
 def moe_gemm_workspace_bytes(dtype, E, n_rows, d, f):
     return int(load().moe_gemm_workspace_bytes(dtype, E, n_rows, d, f))
+
+
+def _gemm_types(dtype):
+    """Type of a grouped GEMM's activations, and the check of what it multiplies (MXFP8: codes)."""
+    if dtype == MOE_MXFP8:
+        return torch.bfloat16, _byte_array
+    t = _float_type(dtype)
+    return t, lambda name, w, n: _array(name, w, t, n)
 
 
 def moe_grouped_gemm_fwd(dtype, x_perm, w13, w2, group_off, capacity, gu, h, y_perm,
@@ -294,11 +335,15 @@ def moe_grouped_gemm_fwd(dtype, x_perm, w13, w2, group_off, capacity, gu, h, y_p
               _dense("y_perm", y_perm, bf, n_rows, d), _p(ws), _nbytes(ws))
         return
     f = h.shape[1]
-    rc = load().moe_grouped_gemm_fwd(dtype, _p(x_perm), _p(x_perm_scales), _p(w13),
-                                     _p(w13_scales), _p(w2), _p(w2_scales), _p(group_off),
-                                     capacity, E, n_rows, d, f, _p(gu), _p(h), _p(y_perm), _p(ws),
-                                     _nbytes(ws), _s(stream))
-    _check(rc, "moe_grouped_gemm_fwd")
+    off = None if capacity else group_off
+    t, weight = _gemm_types(dtype)
+    _call("moe_grouped_gemm_fwd", stream, (x_perm, x_perm_scales, w13, w13_scales, w2, w2_scales, off, gu, h,
+                                           y_perm, ws), dtype, weight("x_perm", x_perm, n_rows * d),
+          _byte_array("x_perm_scales", x_perm_scales, n_rows * (d // 32)), weight("w13", w13, E * 2 * f * d),
+          _byte_array("w13_scales", w13_scales, E * 2 * f * (d // 32)), weight("w2", w2, E * d * f),
+          _byte_array("w2_scales", w2_scales, E * d * (f // 32)), _array("group_off", off, _I32, E + 1),
+          capacity, E, n_rows, d, f, _array("gu", gu, t, n_rows * 2 * f), _array("h", h, t, n_rows * f),
+          _array("y_perm", y_perm, t, n_rows * d), _p(ws), _nbytes(ws))
 
 
 def moe_grouped_gemm_bwd(dtype, dy_perm, x_perm, gu, h, w13, w2, group_off, capacity, dgu,
@@ -308,12 +353,17 @@ def moe_grouped_gemm_bwd(dtype, dy_perm, x_perm, gu, h, w13, w2, group_off, capa
     E = group_off.numel() - 1
     n_rows, d = dy_perm.shape
     f = h.shape[1]
-    rc = load().moe_grouped_gemm_bwd(dtype, _p(dy_perm), _p(x_perm), _p(x_perm_scales), _p(gu),
-                                     _p(h), _p(w13), _p(w13_scales), _p(w2), _p(w2_scales),
-                                     _p(group_off), capacity, E, n_rows, d, f, _p(dgu),
-                                     _p(dx_perm), _p(dw13), _p(dw2), _p(ws), _nbytes(ws),
-                                     _s(stream))
-    _check(rc, "moe_grouped_gemm_bwd")
+    off = None if capacity else group_off
+    t, weight = _gemm_types(dtype)
+    _call("moe_grouped_gemm_bwd", stream, (dy_perm, x_perm, x_perm_scales, gu, h, w13, w13_scales, w2, w2_scales,
+                                           off, dgu, dx_perm, dw13, dw2, ws), dtype,
+          _array("dy_perm", dy_perm, t, n_rows * d), weight("x_perm", x_perm, n_rows * d),
+          _byte_array("x_perm_scales", x_perm_scales, n_rows * (d // 32)), _array("gu", gu, t, n_rows * 2 * f),
+          _array("h", h, t, n_rows * f), weight("w13", w13, E * 2 * f * d),
+          _byte_array("w13_scales", w13_scales, E * d * (2 * f // 32)), weight("w2", w2, E * d * f),
+          _byte_array("w2_scales", w2_scales, E * f * (d // 32)), _array("group_off", off, _I32, E + 1), capacity,
+          E, n_rows, d, f, _array("dgu", dgu, t, n_rows * 2 * f), _array("dx_perm", dx_perm, t, n_rows * d),
+          _array("dw13", dw13, t, E * 2 * f * d), _array("dw2", dw2, t, E * d * f), _p(ws), _nbytes(ws))
 
 
 def gemm_tensors(**tensors):
@@ -339,9 +389,11 @@ def moe_unpermute_combine(dtype, y_perm, dst_row, weights, k, out, dev_err=None,
     """out[t] = sum_j weights[t*k+j] * y_perm[dst_row[t*k+j]] (weights None: unweighted)."""
     T, d = out.shape
     n_rows = y_perm.shape[0]
-    rc = load().moe_unpermute_combine(dtype, _p(y_perm), _p(dst_row), _p(weights), T, k, d,
-                                      n_rows, _p(out), _p(dev_err), _s(stream))
-    _check(rc, "moe_unpermute_combine")
+    t = _float_type(dtype)
+    _call("moe_unpermute_combine", stream, (out, y_perm, dst_row, weights, dev_err), dtype,
+          _array("y_perm", y_perm, t, n_rows * d), _array("dst_row", dst_row, _I32, T * k),
+          _array("weights", weights, torch.float32, T * k), T, k, d, n_rows, _array("out", out, t, T * d),
+          _array("dev_err", dev_err, _I32, 1))
 
 
 def moe_route_add_shared(n_shared, capacity, topk_idx, topk_w, dst_row, counts, offsets, src_slot,
@@ -350,19 +402,24 @@ def moe_route_add_shared(n_shared, capacity, topk_idx, topk_w, dst_row, counts, 
     """The route of k slots -> the route of k + n_shared slots (shared experts E .. E+n_shared-1)."""
     T, k = topk_idx.shape
     E = counts.numel()
-    rc = load().moe_route_add_shared(T, E, k, n_shared, capacity, _p(topk_idx), _p(topk_w), _p(dst_row),
-                                     _p(counts), _p(offsets), _p(src_slot), src_slot.numel(), _p(topk_idx_out),
-                                     _p(topk_w_out), _p(counts_out), _p(offsets_out), _p(dst_row_out),
-                                     _p(src_slot_out), _s(stream))
-    _check(rc, "moe_route_add_shared")
+    n_rows, K, f32 = src_slot.numel(), k + n_shared, torch.float32
+    _call("moe_route_add_shared", stream, (topk_idx, topk_w, dst_row, counts, offsets, src_slot, topk_idx_out, topk_w_out,
+                                           counts_out, offsets_out, dst_row_out, src_slot_out), T, E, k, n_shared, capacity,
+          _array("topk_idx", topk_idx, _I32, T * k), _array("topk_w", topk_w, f32, T * k),
+          _array("dst_row", dst_row, _I32, T * k), _array("counts", counts, _I32, E),
+          _array("offsets", offsets, _I32, E + 1), _array("src_slot", src_slot, _I32, 0), n_rows,
+          _array("topk_idx_out", topk_idx_out, _I32, T * K), _array("topk_w_out", topk_w_out, f32, T * K),
+          _array("counts_out", counts_out, _I32, E + n_shared), _array("offsets_out", offsets_out, _I32, E + n_shared + 1),
+          _array("dst_row_out", dst_row_out, _I32, T * K),
+          _array("src_slot_out", src_slot_out, _I32, n_rows + n_shared * T))
 
 
 def moe_router_logits(x, w_router, logits, stream=None):
     """logits [T, E] fp32 = x [T, d] bf16 . w_router [E, d] bf16 ^T."""
     T, d = x.shape
     E = w_router.shape[0]
-    rc = load().moe_router_logits(_p(x), _p(w_router), T, E, d, _p(logits), _s(stream))
-    _check(rc, "moe_router_logits")
+    _call("moe_router_logits", stream, (x, w_router, logits), _array("x", x, torch.bfloat16, T * d),
+          _array("w_router", w_router, torch.bfloat16, E * d), T, E, d, _array("logits", logits, torch.float32, T * E))
 
 
 def moe_gate_grad(dout, y_perm, topk_idx, topk_w, dst_row, dlogits, dw=None, dy_perm=None,
@@ -373,9 +430,12 @@ def moe_gate_grad(dout, y_perm, topk_idx, topk_w, dst_row, dlogits, dw=None, dy_
     k = topk_idx.shape[1]
     E = dlogits.shape[1]
     n_rows = y_perm.shape[0]
-    rc = load().moe_gate_grad(_p(dout), _p(y_perm), _p(topk_idx), _p(topk_w), _p(dst_row), T, E, k, d,
-                              n_rows, _p(dlogits), _p(dw), _p(dy_perm), _p(dev_err), _s(stream))
-    _check(rc, "moe_gate_grad")
+    bf, f32 = torch.bfloat16, torch.float32
+    _call("moe_gate_grad", stream, (dout, y_perm, topk_idx, topk_w, dst_row, dlogits, dw, dy_perm, dev_err),
+          _array("dout", dout, bf, T * d), _array("y_perm", y_perm, bf, n_rows * d),
+          _array("topk_idx", topk_idx, _I32, T * k), _array("topk_w", topk_w, f32, T * k),
+          _array("dst_row", dst_row, _I32, T * k), T, E, k, d, n_rows, _array("dlogits", dlogits, f32, T * E),
+          _array("dw", dw, f32, T * k), _array("dy_perm", dy_perm, bf, n_rows * d), _array("dev_err", dev_err, _I32, 1))
 
 
 _FLOAT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
@@ -560,6 +620,8 @@ def moe_balance_loss_bwd(logits, counts, tokens, balance_coef, z_coef, dlogits, 
 def moe_quantize_mxfp8(src, colwise, codes, scales, group_off=None, n_groups=0, stream=None):
     """bf16 src [rows, K] -> E4M3FN codes + E8M0 scales (row-wise or per-group column-wise)."""
     rows, K = src.shape
-    rc = load().moe_quantize_mxfp8(_p(src), rows, K, int(colwise), _p(group_off), n_groups,
-                                   _p(codes), _p(scales), _s(stream))
-    _check(rc, "moe_quantize_mxfp8")
+    # column-wise: each group's rows padded to 128
+    n = K * (rows + 128 * (n_groups if group_off is not None else 1)) if colwise else rows * K
+    _call("moe_quantize_mxfp8", stream, (src, group_off, codes, scales), _array("src", src, torch.bfloat16, rows * K), rows,
+          K, int(colwise), _array("group_off", group_off, _I32, n_groups + 1), n_groups, _byte_array("codes", codes, n),
+          _byte_array("scales", scales, n // 32))

@@ -72,3 +72,104 @@ def test_four_bit_weights_of_another_kind_leave_the_earlier_ones(m, at, how):
     with pytest.raises(ValueError):
         lay.set_weights_mxfp4(*w)
     assert all(a is b for a, b in zip((lay.w13_q, lay.w13_s, lay.w2_q, lay.w2_s), had))
+
+
+# ------------------------------------------------------------------ the calls
+def _calls(m):
+    """name -> (call, its tensors): every tensor as the call wants it, but for being on the CPU."""
+    i32, u8 = torch.int32, torch.uint8
+    R, S = T * K, 1
+
+    def z(dtype, *shape):
+        return torch.zeros(*shape, dtype=dtype)
+    route = dict(topk_idx=z(i32, T, K), topk_w=z(F32, T, K), counts=z(i32, E), offsets=z(i32, E + 1), dst_row=z(i32, R),
+                 src_slot=z(i32, R))
+    out = {}
+    out["moe_route_topk"] = (lambda **v: m.moe_route_topk(k=K, capacity=0, ws=z(u8, 1 << 16), **v),
+                             dict(logits=z(F32, T, E), dev_err=z(i32, 1), **route))
+    out["moe_route_topk_noalloc"] = (lambda **v: m.moe_route_topk_noalloc(k=K, capacity=0, **v),
+                                     dict(logits=z(F32, T, E), dev_err=z(i32, 1), **route))
+    out["moe_route_add_shared"] = (lambda **v: m.moe_route_add_shared(S, 0, **v),
+                                   dict(topk_idx_out=z(i32, T, K + S), topk_w_out=z(F32, T, K + S), counts_out=z(i32, E + S),
+                                        offsets_out=z(i32, E + S + 1), dst_row_out=z(i32, T * (K + S)),
+                                        src_slot_out=z(i32, R + S * T), **route))
+    out["moe_router_logits"] = (m.moe_router_logits, dict(x=z(BF, T, D), w_router=z(BF, E, D), logits=z(F32, T, E)))
+    out["moe_gate_grad"] = (m.moe_gate_grad, dict(dout=z(BF, T, D), y_perm=z(BF, R, D), topk_idx=z(i32, T, K),
+                                                  topk_w=z(F32, T, K), dst_row=z(i32, R), dlogits=z(F32, T, E),
+                                                  dw=z(F32, T, K), dy_perm=z(BF, R, D), dev_err=z(i32, 1)))
+    for name, t in TYPES.items():
+        dt = getattr(m, "MOE_" + name)
+        mx = name == "MXFP8"
+        p = dict(x=z(t, T, D), dst_row=z(i32, R), x_perm=z(u8 if mx else t, R, D), src_slot=z(i32, R), dev_err=z(i32, 1))
+        p.update(dict(x_perm_scales=z(u8, R, D // 32)) if mx else dict(row_scale=z(F32, T, K)))
+        out["moe_permute " + name] = (lambda dt=dt, **v: m.moe_permute(dt, k=K, **v), p)
+        c = u8 if mx else t
+        held = dict(x_perm=z(c, R, D), w13=z(c, E, 2 * F, D), w2=z(c, E, D, F), group_off=z(i32, E + 1))
+        if mx:
+            held.update(x_perm_scales=z(u8, R, D // 32), w13_scales=z(u8, E, 2 * F, D // 32), w2_scales=z(u8, E, D, F // 32))
+        saved = dict(gu=z(t, R, 2 * F), h=z(t, R, F))
+        out["moe_grouped_gemm_fwd " + name] = (
+            lambda dt=dt, **v: m.moe_grouped_gemm_fwd(dt, capacity=0, ws=z(u8, 1 << 20), **v),
+            dict(y_perm=z(t, R, D), **held, **saved))
+        out["moe_grouped_gemm_bwd " + name] = (
+            lambda dt=dt, **v: m.moe_grouped_gemm_bwd(dt, capacity=0, ws=z(u8, 1 << 20), **v),
+            dict(dy_perm=z(t, R, D), dgu=z(t, R, 2 * F), dx_perm=z(t, R, D), dw13=z(t, E, 2 * F, D), dw2=z(t, E, D, F),
+                 **held, **saved))
+        if not mx:
+            out["moe_unpermute_combine " + name] = (
+                lambda dt=dt, **v: m.moe_unpermute_combine(dt, k=K, **v),
+                dict(y_perm=z(t, R, D), dst_row=z(i32, R), weights=z(F32, T, K), out=z(t, T, D), dev_err=z(i32, 1)))
+    for n, cols in ((R * D, 0), (D * (R + 128 * E), 1)):
+        q = dict(src=z(BF, R, D), codes=z(u8, n), scales=z(u8, n // 32))
+        q.update(dict(group_off=z(i32, E + 1)) if cols else {})
+        out["moe_quantize_mxfp8 %d" % cols] = (lambda cols=cols, **v: m.moe_quantize_mxfp8(colwise=cols, n_groups=E * cols, **v), q)
+    return out
+
+
+# the tensors whose shape says how many rows, slots or experts a call has, and where: by dimension
+SIZES = {"moe_route_topk": {"logits": (0, 1)}, "moe_route_topk_noalloc": {"logits": (0, 1)},
+         "moe_route_add_shared": {"topk_idx": (0, 1), "counts": (0,), "src_slot": (0,)},
+         "moe_router_logits": {"x": (0, 1), "w_router": (0,)}, "moe_gate_grad": {"dout": (0, 1), "topk_idx": (1,), "dlogits": ()},
+         "moe_permute": {"x": (0, 1), "x_perm": (0,)}, "moe_grouped_gemm_fwd": {"x_perm": (0, 1), "group_off": (0,), "h": (1,)},
+         "moe_grouped_gemm_bwd": {"dy_perm": (0, 1), "group_off": (0,), "h": (1,)}, "moe_unpermute_combine": {"out": (0, 1)},
+         "moe_quantize_mxfp8": {"src": (0, 1)}}
+# checked by other means than their number of elements
+FREE = {"src_slot": ("moe_route_topk", "moe_route_topk_noalloc"), "y_perm": ("moe_unpermute_combine", "moe_gate_grad")}
+CALLS = ["moe_route_topk", "moe_route_topk_noalloc", "moe_route_add_shared", "moe_router_logits", "moe_gate_grad"] + \
+    [c + n for n in TYPES for c in ("moe_permute ", "moe_grouped_gemm_fwd ", "moe_grouped_gemm_bwd ")] + \
+    ["moe_unpermute_combine F32", "moe_unpermute_combine BF16", "moe_quantize_mxfp8 0", "moe_quantize_mxfp8 1"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_of_another_kind_are_refused(m, name):
+    call, good = _calls(m)[name]
+    with pytest.raises(ValueError, match="on a GPU"):        # all as it should be, but for the place
+        call(**good)
+    for n, t in good.items():
+        bad = {"type": t.to(torch.int64 if t.dtype is torch.int32 else torch.float64),
+               "half": t.half() if t.element_size() != 2 else t.float(), "strided": t.repeat_interleave(2, -1)[..., ::2]}
+        if n not in SIZES[name.split()[0]] and name.split()[0] not in FREE.get(n, ()):
+            bad["short"] = t.flatten()[1:]
+        for how, b in bad.items():
+            if how == "strided" and t.numel() == 1:
+                continue
+            with pytest.raises(ValueError, match="^" + n + ":"):
+                call(**dict(good, **{n: b}))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_more_rows_than_the_other_tensors_hold_are_refused(m, name):
+    """Where a tensor's shape gives a size, one of twice it asks for more of the other tensors than they have."""
+    call, good = _calls(m)[name]
+    for n, dims in SIZES[name.split()[0]].items():
+        for dim in dims:
+            with pytest.raises(ValueError, match="expected a contiguous|expected [0-9]+ rows"):
+                call(**dict(good, **{n: torch.cat([good[n]] * 2, dim)}))
+
+
+def test_group_offsets_of_a_padded_layout_may_be_anything(m):
+    """With a capacity only their number is read."""
+    call, good = _calls(m)["moe_grouped_gemm_fwd BF16"]
+    good["group_off"] = torch.zeros(E + 1, dtype=torch.int64)
+    with pytest.raises(ValueError, match="on a GPU"):
+        m.moe_grouped_gemm_fwd(m.MOE_BF16, capacity=T * K // E, ws=torch.zeros(256, dtype=torch.uint8), **good)

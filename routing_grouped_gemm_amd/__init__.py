@@ -39,9 +39,11 @@ GEMM_TENSOR_FIELDS_F32 = ("dw13_f32", "dw2_f32")   # after ws_bytes: fp32 weight
 
 
 class MoeGemmTensors(ctypes.Structure):
-    """C struct moe_gemm_tensors (device pointers, NULL where unused)."""
+    """C struct moe_gemm_tensors (device pointers, NULL where unused); made by gemm_tensors(), which keeps
+    the tensors with it, so that the calls can check them."""
     _fields_ = [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS] + [("ws_bytes", ctypes.c_size_t)] + \
         [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS_F32]
+    given = checked = None   # the tensors by name; the sizes they were last checked for
 
 
 class MoeGlu(ctypes.Structure):
@@ -375,14 +377,50 @@ def gemm_tensors(**tensors):
     st = MoeGemmTensors(**{n: _p(t) for n, t in tensors.items()})
     if tensors.get("ws") is not None:
         st.ws_bytes = tensors["ws"].numel() * tensors["ws"].element_size()
+    st.given = {n: t for n, t in tensors.items() if torch.is_tensor(t)}
     return st
+
+
+# the operands of each stage
+_STAGE = {MOE_GEMM_GATE_UP: ("x_perm", "x_perm_scales", "w13", "w13_scales", "gu", "h"),
+          MOE_GEMM_DOWN: ("h", "w2", "w2_scales", "y_perm"),
+          MOE_GEMM_DGRAD_DOWN: ("dy_perm", "w2", "w2_scales", "gu", "dgu"),
+          MOE_GEMM_DGRAD_GATE_UP: ("dgu", "w13", "w13_scales", "dx_perm"),
+          MOE_GEMM_WGRAD: ("dy_perm", "h", "dgu", "x_perm", "x_perm_scales", "dw13", "dw2", "dw13_f32", "dw2_f32")}
+
+
+def _stage(name, op, dtype, st, group_off, capacity, E, n_rows, d, f, stream, rng, *gate):
+    """One stage call, the operands that gemm_tensors() was given checked first."""
+    given = st.given or {}
+    used = [n for n in _STAGE.get(op, ()) if n in given]
+    key = op, dtype, E, n_rows, d, f
+    if st.checked != key:
+        size = dict(x_perm=n_rows * d, w13=E * 2 * f * d, w2=E * d * f, gu=n_rows * 2 * f, h=n_rows * f)
+        size.update(y_perm=size["x_perm"], dy_perm=size["x_perm"], dx_perm=size["x_perm"], dgu=size["gu"], dw13=size["w13"],
+                    dw2=size["w2"], dw13_f32=size["w13"], dw2_f32=size["w2"])
+        for n in used:
+            if n.endswith("_scales"):                       # one of 32 elements
+                if dtype in (MOE_MXFP8, MOE_MXFP4):
+                    _byte_array(n, given[n], size[n[:-7]] // 32)
+            elif n.endswith("_f32"):
+                _array(n, given[n], torch.float32, size[n])
+            elif n in ("x_perm", "w13", "w2") and dtype in (MOE_MXFP8, MOE_MXFP4):
+                _byte_array(n, given[n], size[n] // (2 if dtype == MOE_MXFP4 else 1))
+            elif dtype in _FLOAT or dtype in (MOE_MXFP8, MOE_MXFP4):
+                _array(n, given[n], _FLOAT.get(dtype, torch.bfloat16), size[n])
+    off = None if capacity else group_off
+    tensors = [t for t in (*(given[n] for n in used), given.get("ws"), off, rng) if torch.is_tensor(t)]
+    args = op, dtype, *gate, ctypes.byref(st), _array("group_off", off, _I32, E + 1), capacity, E, n_rows, d, f
+    if tensors:
+        _call(name, stream, tensors, *args)
+    else:                                                   # pointers alone
+        _check(getattr(load(), name)(*args, _s(stream)), name)
+    st.checked = key
 
 
 def moe_grouped_gemm_op(op, dtype, tensors, group_off, capacity, E, n_rows, d, f, stream=None):
     """One grouped GEMM stage; tensors is a MoeGemmTensors (gemm_tensors())."""
-    rc = load().moe_grouped_gemm_op(op, dtype, ctypes.byref(tensors), _p(group_off), capacity, E,
-                                    n_rows, d, f, _s(stream))
-    _check(rc, "moe_grouped_gemm_op")
+    _stage("moe_grouped_gemm_op", op, dtype, tensors, group_off, capacity, E, n_rows, d, f, stream, None)
 
 
 def moe_unpermute_combine(dtype, y_perm, dst_row, weights, k, out, dev_err=None, stream=None):
@@ -483,8 +521,8 @@ def glu(act=MOE_ACT_SILU, limit=0.0, p=0.0, rng=None):
 
 def moe_grouped_glu_op(op, dtype, gate, tensors, group_off, capacity, E, n_rows, d, f, stream=None):
     """One grouped GEMM stage of a gated block of the form gate (glu()); tensors is a MoeGemmTensors."""
-    _call("moe_grouped_glu_op", stream, (group_off, gate.rng_tensor), op, dtype, ctypes.byref(gate),
-          ctypes.byref(tensors), _dense("group_off", group_off, torch.int32, E + 1), capacity, E, n_rows, d, f)
+    _stage("moe_grouped_glu_op", op, dtype, tensors, group_off, capacity, E, n_rows, d, f, stream, gate.rng_tensor,
+           ctypes.byref(gate))
 
 
 def moe_grouped_glu_fwd(dtype, gate, x_perm, w13, w2, group_off, capacity, gu, h, y_perm, stream=None):

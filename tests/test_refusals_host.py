@@ -173,3 +173,53 @@ def test_group_offsets_of_a_padded_layout_may_be_anything(m):
     good["group_off"] = torch.zeros(E + 1, dtype=torch.int64)
     with pytest.raises(ValueError, match="on a GPU"):
         m.moe_grouped_gemm_fwd(m.MOE_BF16, capacity=T * K // E, ws=torch.zeros(256, dtype=torch.uint8), **good)
+
+
+# ------------------------------------------------------------------ one stage at a time
+@pytest.mark.parametrize("op", range(5))
+@pytest.mark.parametrize("name", [*TYPES, "MXFP4"])
+def test_operands_of_a_stage_are_refused(m, name, op):
+    """Those that the stage reads or writes, of another type, size or layout; the others may be anything."""
+    if name == "MXFP4" and op > m.MOE_GEMM_DOWN:
+        pytest.skip("no such stage")
+    R, u8 = T * K, torch.uint8
+    t = TYPES.get(name, BF)
+    c, per = {"MXFP8": (u8, 1), "MXFP4": (u8, 2)}.get(name, (t, 1))
+    act, held = dict(dtype=t), dict(dtype=c)
+    good = dict(x_perm=torch.zeros(R, D // per, **held), w13=torch.zeros(E, 2 * F, D // per, **held),
+                w2=torch.zeros(E, D, F // per, **held), gu=torch.zeros(R, 2 * F, **act), h=torch.zeros(R, F, **act),
+                y_perm=torch.zeros(R, D, **act), dy_perm=torch.zeros(R, D, **act), dgu=torch.zeros(R, 2 * F, **act),
+                dx_perm=torch.zeros(R, D, **act), dw13=torch.zeros(E, 2 * F, D, **act), dw2=torch.zeros(E, D, F, **act),
+                ws=torch.zeros(1 << 20, dtype=u8))
+    if c is u8:
+        good.update(x_perm_scales=torch.zeros(R, D // 32, dtype=u8), w13_scales=torch.zeros(E, 2 * F, D // 32, dtype=u8),
+                    w2_scales=torch.zeros(E, D, F // 32, dtype=u8))
+    if name == "BF16" and op == m.MOE_GEMM_WGRAD:
+        good.update(dw13_f32=torch.zeros(E, 2 * F, D), dw2_f32=torch.zeros(E, D, F))
+    off = torch.zeros(E + 1, dtype=torch.int32)
+
+    def run(off=off, **over):
+        st, dt = m.gemm_tensors(**dict(good, **over)), getattr(m, "MOE_" + name)
+        m.moe_grouped_gemm_op(op, dt, st, off, 0, E, R, D, F)
+
+    def gated(off=off, **over):
+        st, dt = m.gemm_tensors(**dict(good, **over)), getattr(m, "MOE_" + name)
+        m.moe_grouped_glu_op(op, dt, m.glu(m.MOE_ACT_GELU), st, off, 0, E, R, D, F)
+    uses = {m.MOE_GEMM_GATE_UP: "x_perm w13 gu h", m.MOE_GEMM_DOWN: "h w2 y_perm", m.MOE_GEMM_DGRAD_DOWN: "dy_perm w2 gu dgu",
+            m.MOE_GEMM_DGRAD_GATE_UP: "dgu w13 dx_perm", m.MOE_GEMM_WGRAD: "dy_perm h dgu x_perm dw13 dw2"}[op].split()
+    uses += [n + "_scales" for n in uses if n + "_scales" in good] + [n for n in good if n.endswith("_f32")]
+    for call in (run, gated):
+        with pytest.raises(ValueError, match="on a GPU"):
+            call()
+        for n in uses:
+            v = good[n]
+            for b in (v.double(), v.half() if v.element_size() != 2 else v.float(), v.flatten()[1:],
+                      v.repeat_interleave(2, -1)[..., ::2]):
+                with pytest.raises(ValueError, match="^" + n + ":"):
+                    call(**{n: b})
+        for n in set(good) - set(uses) - {"ws"}:
+            with pytest.raises(ValueError, match="on a GPU"):
+                call(**{n: good[n].double()[:1]})
+        for b in (off.long(), off[1:]):
+            with pytest.raises(ValueError, match="^group_off:"):
+                call(off=b)

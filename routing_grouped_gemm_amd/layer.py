@@ -131,6 +131,7 @@ class MoELayer:
                                     device=device)
         if dtype == MOE_INT4:
             self._glu = glu(act, limit)
+            self.w13_4 = self.w2_4 = None
             self.out = torch.empty(T, d, dtype=act_dtype, device=device)
             self.int4_ws = torch.empty(moe_int4_workspace_bytes(R, d, f), dtype=torch.uint8, device=device)
             self._bwd_alloc = False
@@ -201,10 +202,10 @@ class MoELayer:
         """Weights [E, 2f, d] and [E, d, f] (MOE_F32: fp32, otherwise bf16) on the
         layer's device; refused ones leave the layer with those it had.  For MXFP8
         the forward and backward MXFP8 caches are made here (once per optimizer
-        step), for MXFP4 the codes of both.  Each call makes new caches and a captured
-        graph reads those of its capture: for weights that change under a graph,
-        write them into w13 and w2 and call requantize_weights, which works in place.
-        INT4: the codes are made here, and the bf16 weights are not kept."""
+        step), for MXFP4 and INT4 the codes of both; an INT4 layer does not keep the
+        bf16 weights.  Each call makes new caches and lets go of the last ones, so a
+        graph that was captured with those is not replayed afterwards: weights that
+        change under a graph go through requantize_weights, which works in place."""
         E, f, d = self.G, self.f, self.d
         # (the quantisers are given a dense copy of weights that are not)
         dense = self.dtype in (MOE_F32, MOE_BF16)
@@ -223,14 +224,12 @@ class MoELayer:
         if self.dtype == MOE_INT4:
             g = self.group
             made = []
-            for w, N, K in ((w13, 2 * f, d), (w2, d, f)):
+            for N, K in ((2 * f, d), (d, f)):
                 u8 = dict(dtype=torch.uint8, device=self.device)
-                codes = torch.empty(E, N, K // 2, **u8)
-                scales = torch.empty(E, N, K // g, dtype=torch.bfloat16, device=self.device)
-                zeros = torch.empty(E, N, K // g, **u8) if self.zeros else None
-                moe_quantize_int4(w.reshape(E * N, K), g, codes.view(E * N, -1), scales.view(E * N, -1),
-                                  None if zeros is None else zeros.view(E * N, -1))
-                made.append((codes, scales, zeros))
+                made.append((torch.empty(E, N, K // 2, **u8),
+                             torch.empty(E, N, K // g, dtype=torch.bfloat16, device=self.device),
+                             torch.empty(E, N, K // g, **u8) if self.zeros else None))
+            self._quantize_int4(w13, w2, *made)
             self.set_weights_int4(*made)
             return
         self.w13, self.w2 = w13, w2
@@ -294,11 +293,30 @@ class MoELayer:
         moe_quantize_mxfp4(w13.reshape(E * 2 * f, d), w13_q.view(E * 2 * f, -1), w13_s.view(E * 2 * f, -1))
         moe_quantize_mxfp4(w2.reshape(E * d, f), w2_q.view(E * d, -1), w2_s.view(E * d, -1))
 
-    def requantize_weights(self):
-        """MXFP8: rebuild the four weight caches (forward and backward direction
-        of w13 and w2) from the bf16 weights in place, as an optimizer step does.
-        MXFP4: rebuild the codes."""
+    def _quantize_int4(self, w13, w2, w13_4, w2_4):
+        for w, (codes, scales, zeros) in ((w13, w13_4), (w2, w2_4)):
+            rows, K = codes.shape[0] * codes.shape[1], 2 * codes.shape[2]
+            moe_quantize_int4(w.reshape(rows, K), self.group, codes.view(rows, -1), scales.view(rows, -1),
+                              None if zeros is None else zeros.view(rows, -1))
+
+    def requantize_weights(self, w13=None, w2=None):
+        """Rebuild in place what the layer's kernels read, as after an optimizer step.  MXFP8: the four
+        weight caches (forward and backward direction of w13 and w2) from the bf16 weights.  MXFP4: the
+        codes.  INT4, whose bf16 weights the layer does not keep: the codes, scales and zero points it
+        holds (with zero points where it holds some) from the w13 and w2 given here."""
         E, f, d = self.G, self.f, self.d
+        if self.dtype not in (MOE_MXFP8, MOE_MXFP4, MOE_INT4):
+            raise ValueError("requantize_weights: fp32 and bf16 layers read the weights themselves")
+        given = self.dtype == MOE_INT4
+        if (w13 is not None) != given or (w2 is not None) != given:
+            raise ValueError("requantize_weights takes w13 and w2 for an INT4 layer, and no tensors for the others")
+        if given:
+            if self.w13_4 is None:
+                raise ValueError("requantize_weights: the layer has no weights yet (set_weights)")
+            self._check_held("w13", w13, E * 2 * f * d, torch.bfloat16, False)
+            self._check_held("w2", w2, E * d * f, torch.bfloat16, False)
+            self._quantize_int4(w13, w2, self.w13_4, self.w2_4)
+            return
         if self.dtype == MOE_MXFP4:
             if self.w13 is None:
                 raise ValueError("requantize_weights: the layer's weights were given in 4 bits")

@@ -35,6 +35,12 @@ _ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_MXFP8: torch.bfloa
         MOE_MXFP4: torch.bfloat16, MOE_INT4: torch.bfloat16}
 
 
+def int4_sizes_ok(T, E, d, f, k):
+    """Whether moe_int4_ffn takes T tokens of k slots (shared experts counted in E and k)."""
+    return (0 <= T and 1 <= k <= 8 and 1 <= E <= 1024 and 1 <= d <= 1 << 20 and 1 <= f <= 1 << 20 and T * k < 1 << 31 and
+            T * d < 1 << 30 and T * k * f < 1 << 30 and d * f < 1 << 31)
+
+
 class MoELayer:
     """n_shared > 0 adds that many shared experts (ungated, every token, weight
     1) as extra groups E .. E+n_shared-1 of the same grouped GEMM: weights are
@@ -67,6 +73,10 @@ class MoELayer:
                 raise ValueError("an INT4 layer has no padded layout")
             if group not in (32, 64, 128) or d % group or f % group:
                 raise ValueError(f"INT4: groups of 32, 64 or 128 that divide d = {d} and f = {f}, got {group}")
+            if not int4_sizes_ok(T, E + n_shared, d, f, k + n_shared):
+                raise ValueError(f"INT4: T = {T}, d = {d}, f = {f}, {k + n_shared} slots of {E + n_shared} experts are past "
+                                 "what moe_int4_ffn takes: T * d and T * k * f below 2^30, d * f below 2^31, d and f at "
+                                 "most 2^20, 8 slots, 1024 experts")
             if out_dropout:
                 raise ValueError("out_dropout: an INT4 layer serves, it has no dropout")
         if not (MOE_ACT_SILU <= act <= MOE_ACT_RELU and 0 <= limit < float("inf")):
@@ -527,10 +537,13 @@ class MoELayer:
     def forward(self, logits, x, weights=None, residual=None, same_mask=False):
         """out [T, d]: the layer's output, dropped by out_dropout and added to residual [T, d] if
         given (whose gradient is dout itself)."""
-        self.route(logits)
         if self.dtype == MOE_INT4:
             if weights is not None or residual is not None:
                 raise ValueError("an INT4 layer takes neither weights nor a residual")
+            if self.w13_4 is None:
+                raise ValueError("forward: the layer has no weights yet (set_weights)")
+        self.route(logits)
+        if self.dtype == MOE_INT4:
             moe_int4_ffn(self._glu, x, self.s_idx, self.s_w, self.s_dst, self.s_src, self.s_off, self.group,
                          self.w13_4, self.w2_4, self.out, self.int4_ws, dev_err=self.dev_err)
             return self.out

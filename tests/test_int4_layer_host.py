@@ -70,3 +70,35 @@ def test_requantize_refusals(m, made):
             MoELayer(T, D, E, F, K, dtype, device="cpu").requantize_weights()
     with pytest.raises(ValueError):
         MoELayer(T, D, E, 128, K, m.MOE_MXFP4, device="cpu").requantize_weights(w13, w2)
+
+
+# T, E, d, f, k at and past each limit
+LIMITS = [(8, 4, 128, 128, 2), (1 << 22, 8, 256, 128, 1), ((1 << 22) - 1, 8, 256, 128, 1), (1 << 20, 8, 128, 128, 8),
+          ((1 << 20) - 1, 8, 128, 128, 8), (1, 8, 1 << 20, 2048, 1), (1, 8, 1 << 20, 1984, 1), (1, 8, 1 << 21, 64, 1),
+          (1, 8, 64, (1 << 20) + 64, 1), (8, 1024, 64, 64, 8), (8, 1025, 64, 64, 8), (8, 16, 64, 64, 9), (1, 8, 64, 1 << 20, 8)]
+
+
+@pytest.mark.parametrize("T,E,d,f,k", LIMITS)
+def test_sizes_past_the_limits_are_refused_when_the_layer_is_made(m, T, E, d, f, k):
+    """As the call refuses them: with good sizes it gets as far as the workspace that is missing here."""
+    import ctypes
+
+    from routing_grouped_gemm_amd import layer
+    P = 0x10000
+    w = ctypes.byref(m.MoeInt4(P, P, None))
+    rc = m.load().moe_int4_ffn(ctypes.byref(m.MoeGlu(0, 0.0, 0.0, None)), P, T, k, P, P, P, P, P, E, d, f, 64, w, w, P, None,
+                               0, None, None)
+    assert rc in (m.MOE_EINVAL, m.MOE_EWORKSPACE)
+    ok = rc == m.MOE_EWORKSPACE
+    assert layer.int4_sizes_ok(T, E, d, f, k) == ok
+    if not ok:
+        for S in ((0, 1) if k > 1 else (0,)):
+            with pytest.raises(ValueError):
+                layer.MoELayer(T, d, E - S, f, k - S, m.MOE_INT4, device="cpu", group=64, n_shared=S)
+
+
+def test_forward_without_weights_is_refused(m):
+    from routing_grouped_gemm_amd.layer import MoELayer
+    lay = MoELayer(T, D, E, F, K, m.MOE_INT4, device="cpu", group=G)
+    with pytest.raises(ValueError, match="weights"):
+        lay.forward(torch.zeros(T, E), torch.zeros(T, D, dtype=BF))

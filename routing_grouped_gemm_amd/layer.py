@@ -54,9 +54,12 @@ class MoELayer:
     fp32, bf16 and INT4.  h_dropout: dropout of the experts' h (fp32, bf16);
     out_dropout: of the layer's output, before the residual that forward may be
     given.  Masks follow from rng, int64 [2, 2] on the device: (seed, step) of the
-    two.  Each forward advances both steps, by a kernel of its own, so that a
-    replayed graph draws new masks; forward(same_mask=True) does not, to
-    recompute activations.  Layers that train together need different seeds.
+    two, written in place if at all.  Each forward advances both steps, by a kernel
+    of its own, so that a replayed graph draws new masks; forward(same_mask=True)
+    does not, to recompute activations.  Layers that train together need different
+    seeds: without one (None) a layer draws its own from torch's default generator,
+    so that torch.manual_seed repeats a run.  Ranks with one seed drop the same
+    places of their own tokens.
     With training set to False nothing is dropped (set it before a forward and
     leave it until its backward).
 
@@ -65,7 +68,7 @@ class MoELayer:
     activations in bf16."""
 
     def __init__(self, T, d, E, f, k, dtype=MOE_BF16, capacity=0, device="cuda", n_shared=0, save=True,
-                 decode_h=False, act=MOE_ACT_SILU, limit=0.0, h_dropout=0.0, out_dropout=0.0, seed=0, group=128,
+                 decode_h=False, act=MOE_ACT_SILU, limit=0.0, h_dropout=0.0, out_dropout=0.0, seed=None, group=128,
                  zeros=False):
         if dtype == MOE_INT4:
             save = False
@@ -100,6 +103,8 @@ class MoELayer:
         self._glu = None
         self.rng = self._rng_step = None
         if h_dropout or out_dropout:
+            if seed is None:
+                seed = int(torch.randint(1 << 62, (), device="cpu"))
             # the two masks of one step are 2^62 steps apart
             self.rng = torch.tensor([[seed, 0], [seed, 1 << 62]], dtype=torch.int64, device=device)
             self._rng_step = self.rng[:, 1]

@@ -515,6 +515,8 @@ def glu(act=MOE_ACT_SILU, limit=0.0, p=0.0, rng=None):
     """A gated block's form: gate MOE_ACT_*, limit on g and u (0: none), dropout of h with probability p and
     rng [2] int64 on the device, (seed, step)."""
     g = MoeGlu(act, limit, p, _rng(rng))
+    if limit > 0 and g.limit == 0:
+        raise ValueError(f"limit = {limit} is 0 in fp32, which would be no limit")
     g.rng_tensor = rng
     return g
 

@@ -19,6 +19,8 @@ and is nearer to the layer without quantisers (with Gaussian operands 23% off
 its dw2 in norm, against 28%; the two lie 15% apart).  decode_h=True makes
 dw2 from the 4-bit copy: the gradient of the forward that ran.
 """
+import ctypes
+
 import torch
 
 from . import (MOE_ACT_RELU, MOE_ACT_SILU, MOE_BF16, MOE_F32, MOE_GEMM_DGRAD_DOWN, MOE_GEMM_DGRAD_GATE_UP,
@@ -82,10 +84,12 @@ class MoELayer:
                                  "most 2^20, 8 slots, 1024 experts")
             if out_dropout:
                 raise ValueError("out_dropout: an INT4 layer serves, it has no dropout")
-        if not (MOE_ACT_SILU <= act <= MOE_ACT_RELU and 0 <= limit < float("inf")):
+        # (as the calls see them, in fp32)
+        L = ctypes.c_float(limit).value
+        if not (MOE_ACT_SILU <= act <= MOE_ACT_RELU and 0 <= L < float("inf") and (L > 0) == (limit > 0)):
             raise ValueError(f"act = {act}, limit = {limit}: expected a MOE_ACT_* and a limit >= 0 (0: none)")
         for name, p in (("h_dropout", h_dropout), ("out_dropout", out_dropout)):
-            if not 0 <= p < 1:
+            if not 0 <= ctypes.c_float(p).value < 1:
                 raise ValueError(f"{name}: expected 0 <= p < 1, got {p}")
         other_gate = act != MOE_ACT_SILU or limit > 0
         if other_gate and dtype not in (MOE_F32, MOE_BF16, MOE_INT4):

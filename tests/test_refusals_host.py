@@ -223,3 +223,18 @@ def test_operands_of_a_stage_are_refused(m, name, op):
         for b in (off.long(), off[1:]):
             with pytest.raises(ValueError, match="^group_off:"):
                 call(off=b)
+
+
+# ------------------------------------------------------------------ numbers that fp32 makes others of
+def test_limits_and_probabilities_are_those_of_fp32(m):
+    """A limit of 0 means none, so one that fp32 holds as 0 is refused, not taken for none; a probability that fp32
+    holds as 1 drops everything."""
+    from routing_grouped_gemm_amd.layer import MoELayer
+    smallest = 2.0 ** -149
+    with pytest.raises(ValueError):
+        m.glu(limit=1e-60)
+    assert m.glu(limit=smallest).limit == smallest and m.glu(limit=0.0).limit == 0
+    for kw in (dict(limit=1e-60), dict(limit=1e39), dict(h_dropout=1 - 1e-12), dict(out_dropout=1 - 1e-12)):
+        with pytest.raises(ValueError):
+            MoELayer(T, D, E, F, K, m.MOE_BF16, device="cpu", **kw)
+    MoELayer(T, D, E, F, K, m.MOE_BF16, device="cpu", limit=smallest, h_dropout=1 - 2.0 ** -24)

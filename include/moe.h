@@ -553,7 +553,8 @@ enum moe_act {
  * out  out        [n].  May be x or residual itself; no other overlap.
  * The backward for x is the same call on the upstream gradient without a
  * residual.  Errors: MOE_EUNSUPPORTED (dtype), MOE_EINVAL (sizes, p, null
- * pointers), MOE_EALIGN (n, pointers; rng 8-byte aligned).
+ * pointers; an rng that is not 8-byte aligned), MOE_EALIGN (n, the other
+ * pointers).
  */
 MOE_API int moe_dropout(int dtype, const void* x, const void* residual, int64_t n, float p,
                         const uint64_t* rng, void* out, moe_stream_t stream);
@@ -594,7 +595,7 @@ typedef struct moe_glu {
  * with g and u as saved (bf16 for MOE_BF16).  The stages that the form does not
  * touch (DOWN, DGRAD_GATE_UP, WGRAD) are the ones of moe_grouped_gemm_op.
  * MOE_EUNSUPPORTED for MOE_MXFP8 and MOE_MXFP4; MOE_EINVAL for a form that is
- * NULL or out of range.
+ * NULL or out of range, its rng included.
  */
 MOE_API int moe_grouped_glu_op(int op, int dtype, const moe_glu* glu, const moe_gemm_tensors* t,
                                const int32_t* group_off, int capacity, int E, int64_t n_rows, int d, int f,
@@ -651,7 +652,7 @@ MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
  * scale in fp32.  Made for few rows an expert, single tokens above all; any T is
  * right.  Rows of many more tokens run faster as MOE_BF16 on moe_dequantize_int4
  * of the weights.
- * in   glu        gate and limit; p must be 0 (MOE_EUNSUPPORTED).
+ * in   glu        gate and limit; p must drop nothing (MOE_EUNSUPPORTED).
  * in   x          [T, d] bf16.
  * in   the route of moe_route_topk (capacity 0), or widened by
  *                 moe_route_add_shared: topk_idx, topk_w, dst_row [T, k],
@@ -663,7 +664,8 @@ MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
  * out  dev_err    optional; MOE_ERR_ROW_RANGE.
  * Which of its kernels run depends on the sizes, and with that the order of the
  * fp32 sums: a token's output may differ in the last bits between batches.
- * A token row with an infinity or a NaN gives NaN.
+ * A token row with an infinity or a NaN gives NaN, and so may one whose x or h
+ * has elements past 2^115: a group's sums hold up to 31 times its elements.
  * Errors: MOE_EINVAL (sizes: k <= 8, E <= 1024; T * d and T * k * f below 2^30,
  * d * f below 2^31, d and f at most 2^20; null pointers), MOE_EUNSUPPORTED (group, p), MOE_EALIGN (d or f not a
  * multiple of group; x, out, codes not 16-byte aligned, scales not 2-byte),

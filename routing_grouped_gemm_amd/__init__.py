@@ -43,7 +43,7 @@ class MoeGemmTensors(ctypes.Structure):
     the tensors with it, so that the calls can check them."""
     _fields_ = [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS] + [("ws_bytes", ctypes.c_size_t)] + \
         [(n, ctypes.c_void_p) for n in GEMM_TENSOR_FIELDS_F32]
-    given = checked = None   # the tensors by name; the sizes they were last checked for
+    given = checked = dev = None   # the tensors by name; the sizes they were last checked for, and their GPU
 
 
 class MoeGlu(ctypes.Structure):
@@ -223,6 +223,11 @@ def _call(name, stream, tensors, *args):
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.get_device() != dev:
             raise ValueError(f"{name}: tensors on {tensors[0].device} and {t.device}")
+    _launch(name, dev, stream, args)
+
+
+def _launch(name, dev, stream, args):
+    """The C entry point `name` on `stream` (None: the current one of the GPU dev), with dev current."""
     fn = getattr(load(), name)
     if dev == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(dev) if stream is None and _raw_stream else _s(stream))
@@ -391,31 +396,49 @@ _STAGE = {MOE_GEMM_GATE_UP: ("x_perm", "x_perm_scales", "w13", "w13_scales", "gu
 
 def _stage(name, op, dtype, st, group_off, capacity, E, n_rows, d, f, stream, rng, *gate):
     """One stage call, the operands that gemm_tensors() was given checked first."""
-    given = st.given or {}
-    used = [n for n in _STAGE.get(op, ()) if n in given]
-    key = op, dtype, E, n_rows, d, f
+    off, key = None if capacity else group_off, (op, dtype, E, n_rows, d, f)
+    off_at = _array("group_off", off, _I32, E + 1)
     if st.checked != key:
-        size = dict(x_perm=n_rows * d, w13=E * 2 * f * d, w2=E * d * f, gu=n_rows * 2 * f, h=n_rows * f)
-        size.update(y_perm=size["x_perm"], dy_perm=size["x_perm"], dx_perm=size["x_perm"], dgu=size["gu"], dw13=size["w13"],
-                    dw2=size["w2"], dw13_f32=size["w13"], dw2_f32=size["w2"])
-        for n in used:
-            if n.endswith("_scales"):                       # one of 32 elements
-                if dtype in (MOE_MXFP8, MOE_MXFP4):
-                    _byte_array(n, given[n], size[n[:-7]] // 32)
-            elif n.endswith("_f32"):
-                _array(n, given[n], torch.float32, size[n])
-            elif n in ("x_perm", "w13", "w2") and dtype in (MOE_MXFP8, MOE_MXFP4):
-                _byte_array(n, given[n], size[n] // (2 if dtype == MOE_MXFP4 else 1))
-            elif dtype in _FLOAT or dtype in (MOE_MXFP8, MOE_MXFP4):
-                _array(n, given[n], _FLOAT.get(dtype, torch.bfloat16), size[n])
-    off = None if capacity else group_off
-    tensors = [t for t in (*(given[n] for n in used), given.get("ws"), off, rng) if torch.is_tensor(t)]
-    args = op, dtype, *gate, ctypes.byref(st), _array("group_off", off, _I32, E + 1), capacity, E, n_rows, d, f
-    if tensors:
-        _call(name, stream, tensors, *args)
-    else:                                                   # pointers alone
-        _check(getattr(load(), name)(*args, _s(stream)), name)
+        st.dev = _check_stage(name, op, dtype, st.given or {}, E, n_rows, d, f)
+    dev = st.dev
+    for t in (off, rng):
+        if torch.is_tensor(t):
+            if dev is None:
+                dev = t.get_device()
+            if t.get_device() != dev or dev < 0:
+                raise ValueError(f"{name}: expected tensors on a GPU, all on one, got one on {t.device}")
+    args = op, dtype, *gate, ctypes.byref(st), off_at, capacity, E, n_rows, d, f
+    _launch(name, torch.cuda.current_device() if dev is None else dev, stream, args)
     st.checked = key
+
+
+def _check_stage(name, op, dtype, given, E, n_rows, d, f):
+    """The GPU of the tensors of `given` that the stage reads and writes (None: there are pointers alone)."""
+    size = dict(x_perm=n_rows * d, w13=E * 2 * f * d, w2=E * d * f, gu=n_rows * 2 * f, h=n_rows * f)
+    size.update(y_perm=size["x_perm"], dy_perm=size["x_perm"], dx_perm=size["x_perm"], dgu=size["gu"], dw13=size["w13"],
+                dw2=size["w2"], dw13_f32=size["w13"], dw2_f32=size["w2"])
+    mx, used = dtype in (MOE_MXFP8, MOE_MXFP4), []
+    for n in (*_STAGE.get(op, ()), "ws"):
+        t = given.get(n)
+        if t is None:
+            continue
+        if n.endswith("_scales"):                           # one of 32 elements
+            if mx:
+                _byte_array(n, t, size[n[:-7]] // 32)
+        elif n.endswith("_f32"):
+            _array(n, t, torch.float32, size[n])
+        elif mx and n in ("x_perm", "w13", "w2"):
+            _byte_array(n, t, size[n] // (2 if dtype == MOE_MXFP4 else 1))
+        elif n != "ws" and (mx or dtype in _FLOAT):
+            _array(n, t, _FLOAT.get(dtype, torch.bfloat16), size[n])
+        used.append(t)
+    if not used:
+        return None
+    dev = used[0].get_device()
+    for t in used:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError(f"{name}: expected tensors on a GPU, all on one, got one on {t.device}")
+    return dev
 
 
 def moe_grouped_gemm_op(op, dtype, tensors, group_off, capacity, E, n_rows, d, f, stream=None):

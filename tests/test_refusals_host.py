@@ -238,3 +238,83 @@ def test_limits_and_probabilities_are_those_of_fp32(m):
         with pytest.raises(ValueError):
             MoELayer(T, D, E, F, K, m.MOE_BF16, device="cpu", **kw)
     MoELayer(T, D, E, F, K, m.MOE_BF16, device="cpu", limit=smallest, h_dropout=1 - 2.0 ** -24)
+
+
+# ------------------------------------------------------------------ what a layer is given
+@pytest.mark.parametrize("name", [*TYPES, "MXFP4"])
+def test_what_a_step_is_given_is_checked(m, name, monkeypatch):
+    """More rows than the layer has, another width, type or layout are refused before anything is launched."""
+    from routing_grouped_gemm_amd import layer
+    t = TYPES.get(name, BF)
+    lay = layer.MoELayer(T, D, E, F, K, getattr(m, "MOE_" + name), device="cpu")
+    ran = []
+    monkeypatch.setattr(layer, "_launch", lambda n, dev, stream, args: ran.append(n))
+    x, logits, w = torch.zeros(T, D, dtype=t), torch.zeros(T, E), torch.zeros(T, K)
+    steps = {"logits": (logits, lay.route), "x": (x, lay.permute),
+             "dout": (x, lambda v: lay._permute(m.MOE_F32 if name == "F32" else m.MOE_BF16, v, lay.y_perm, None, 1)),
+             "weights": (w, lay.combine)}
+    for n, (good, call) in steps.items():
+        bad = [good.double(), good.half(), good.repeat_interleave(2, 1)[:, ::2]]
+        bad += [good[1:]] if n == "weights" else [torch.cat([good, good[:1]]), good[:, 1:].contiguous(), good.flatten()]
+        for b in bad:
+            # (a layer on the CPU launches nothing: a tensor in order gets as far as that)
+            with pytest.raises((ValueError, TypeError), match="^" + n + ":"):
+                call(b)
+        with pytest.raises(ValueError, match="not on a GPU"):
+            call(good)
+    assert not ran
+
+
+def _filled(args):
+    return [a.value if hasattr(a, "value") else a for a in args]
+
+
+@pytest.mark.parametrize("S,C", [(0, 0), (1, 0), (0, 6), (2, 6)])
+@pytest.mark.parametrize("name", [*TYPES, "MXFP4"])
+def test_a_step_hands_on_what_the_calls_would(m, name, S, C, monkeypatch):
+    """The arguments of each C call of a layer's step are those that the checked calls make of the layer's tensors."""
+    from routing_grouped_gemm_amd import layer
+    dt, t = getattr(m, "MOE_" + name), TYPES.get(name, BF)
+    act_dt = m.MOE_F32 if name == "F32" else m.MOE_BF16
+    monkeypatch.setattr(layer, "moe_quantize_mxfp8", lambda *a: None)
+    monkeypatch.setattr(layer, "moe_quantize_mxfp4", lambda *a: None)
+    monkeypatch.setattr(layer, "moe_dequantize_mxfp4", lambda *a: None)
+    lay = layer.MoELayer(T, D, E, F, K, dt, capacity=C, n_shared=S, device="cpu")
+    lay.set_weights(torch.zeros(E + S, 2 * F, D, dtype=t), torch.zeros(E + S, D, F, dtype=t))
+    got, want = [], []
+    monkeypatch.setattr(layer.MoELayer, "_do", lambda self, n, *a: got.append((n, *_filled(a))))
+    monkeypatch.setattr(m, "_call", lambda n, stream, tensors, *a: want.append((n, *_filled(a))))
+    logits, x, dout = torch.zeros(T, E), torch.zeros(T, D, dtype=t), torch.ones(T, D, dtype=t)
+    lay.forward(logits, x)
+    lay.backward(dout)
+    m.moe_route_topk(logits, lay.k, lay.capacity, lay.topk_idx, lay.topk_w, lay.counts, lay.offsets, lay.dst_row,
+                     lay.src_slot, lay.route_ws, lay.dev_err)
+    if S:
+        m.moe_route_add_shared(S, C, lay.topk_idx, lay.topk_w, lay.dst_row, lay.counts, lay.offsets, lay.src_slot,
+                               lay.s_idx, lay.s_w, lay.s_counts, lay.s_off, lay.s_dst, lay.s_src)
+    m.moe_permute(dt, x, lay.K, lay.s_dst, lay.x_perm, src_slot=lay.s_fill, x_perm_scales=lay.x_perm_scales,
+                  dev_err=lay.dev_err)
+    q = name in ("MXFP8", "MXFP4")
+    sc = dict(x_perm_scales=lay.x_perm_scales, w13_scales=lay.w13_s, w2_scales=lay.w2_s) if q else {}
+    m.moe_grouped_gemm_fwd(dt, lay.x_perm, lay.w13_q.view(E + S, 2 * F, -1) if q else lay.w13,
+                           lay.w2_q.view(E + S, D, -1) if q else lay.w2, lay.s_off, lay.g_cap, lay.gu, lay.h, lay.y_perm,
+                           ws=lay.gemm_ws, **sc)
+    m.moe_unpermute_combine(act_dt, lay.y_perm, lay.s_dst, lay.s_w, lay.K, lay.out, dev_err=lay.dev_err)
+    m.moe_permute(act_dt, dout, lay.K, lay.s_dst, lay.dy_perm, src_slot=lay.s_fill, row_scale=lay.s_w, dev_err=lay.dev_err)
+    back = dict(F32=(lay.x_perm, lay.h, lay.w13, lay.w2), BF16=(lay.x_perm, lay.h, lay.w13, lay.w2))
+    if name == "MXFP8":
+        back[name] = (lay.x_perm, lay.h, lay.w13t_q, lay.w2t_q)
+        sc = dict(x_perm_scales=lay.x_perm_scales, w13_scales=lay.w13t_s, w2_scales=lay.w2t_s)
+    elif name == "MXFP4":
+        back[name], sc = (lay.x_perm_d, lay.h_d, lay.w13_d, lay.w2_d), {}
+    xb, h, w13, w2 = back[name]
+    m.moe_grouped_gemm_bwd(m.MOE_BF16 if name == "MXFP4" else dt, lay.dy_perm, xb, lay.gu, h, w13, w2, lay.s_off, lay.g_cap,
+                           lay.dgu, lay.dx_perm, lay.dw13, lay.dw2, ws=lay.bwd_ws if name == "MXFP4" else lay.gemm_ws, **sc)
+    m.moe_unpermute_combine(act_dt, lay.dx_perm, lay.s_dst, None, lay.K, lay.dx, dev_err=lay.dev_err)
+    assert [g[0] for g in got] == [w[0] for w in want]
+    for g, w in zip(got, want):
+        # group offsets that a capacity makes unread are not handed on by the checked calls
+        if C and not S and g[0].startswith("moe_grouped_gemm"):
+            at = g.index(lay.s_off.data_ptr())
+            g, w = g[:at] + g[at + 1:], w[:at] + w[at + 1:]
+        assert g == w, g[0]

@@ -647,9 +647,11 @@ MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
  * The layer's feed-forward over experts in 4-bit integers, for serving: from
  * token rows to combined outputs, the dispatch and the combine included.
  *   h_j = a(g') u' with g | u = x[t] W13[e_j]^T,   out[t] = sum_j topk_w[t, j] * (h_j W2[e_j]^T)
- * Activations are bf16 (h is rounded to bf16), sums fp32; weights are read as they
- * are and not rounded: a group's sum of x * (code - zero) is multiplied by its
- * scale in fp32.  Made for few rows an expert, single tokens above all; any T is
+ * x and out are bf16, sums fp32; weights are read as they are and not rounded: a
+ * group's sum of x * (code - zero) is multiplied by its scale in fp32.  Between
+ * the products h is held in fp16 under a power of two for each row (single
+ * tokens: for 16 columns): eleven significant bits, fewer for elements below
+ * 2^-21 of the row's largest and none below 2^-32.  Made for few rows an expert, single tokens above all; any T is
  * right.  Rows of many more tokens run faster as MOE_BF16 on moe_dequantize_int4
  * of the weights.
  * in   glu        gate and limit; p must drop nothing (MOE_EUNSUPPORTED).
@@ -664,8 +666,8 @@ MOE_API size_t moe_int4_workspace_bytes(int64_t n_rows, int d, int f);
  * out  dev_err    optional; MOE_ERR_ROW_RANGE.
  * Which of its kernels run depends on the sizes, and with that the order of the
  * fp32 sums: a token's output may differ in the last bits between batches.
- * A token row with an infinity or a NaN gives NaN, and so may one whose x or h
- * has elements past 2^115: a group's sums hold up to 31 times its elements.
+ * A token row with an infinity or a NaN gives NaN, and so may one with elements
+ * past 2^115: a group's sums hold up to 31 times its elements.
  * Errors: MOE_EINVAL (sizes: k <= 8, E <= 1024; T * d and T * k * f below 2^30,
  * d * f below 2^31, d and f at most 2^20; null pointers), MOE_EUNSUPPORTED (group, p), MOE_EALIGN (d or f not a
  * multiple of group; x, out, codes not 16-byte aligned, scales not 2-byte),

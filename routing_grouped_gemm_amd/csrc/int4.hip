@@ -23,6 +23,19 @@
 // a 4 x 4 exchange of words among the lane groups gives MFMA i the codes
 // 32i + 8g .. + 7.  Within a word the pairs are (j, j + 4), and x is put in the
 // same order.
+//
+// h between the two products is fp16 with a power of two for each row (or 16
+// columns of it) that puts its largest element into [2^7, 2^8): eleven
+// significant bits.  In bf16, with eight, its rounding costs as much as the
+// output's own, and more where a limit makes many elements of h the same and
+// their errors add up (outputs of 80 random calls against 64 bits: 2.3e-3 to
+// 2.8e-3 of their size off with h in bf16, 1.7e-3 so, their own rounding).
+// The down product's operands are fp16 then: a code at bits 6..9 of 0x4c00 is
+// 16 + q.  Where matrix instructions need a whole row's scale, the first
+// product leaves h in fp32 and a pass of 3 to 5 us a call narrows it.  (Scales
+// of 16 columns from the first product's epilogue, brought to one where the
+// second loads its rows, are dearer: 245 against 239 us for the few-row
+// kernel's example.)
 #include "gemm_common.h"
 
 namespace moe {
@@ -31,6 +44,8 @@ namespace {
 using gemm::bf16x8;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
 // ---------------------------------------------------------------- quantiser
 // A lane takes 8 elements, a group's G / 8 lanes (4, 8 or 16 neighbours) find its extremes together.  Bound by the
@@ -198,50 +213,102 @@ __global__ __launch_bounds__(256) void dequantize_int4_kernel(const uint32_t* __
 }
 
 // ---------------------------------------------------------------- products
-__device__ __forceinline__ bf16x8 as_bf16x8(uint4 v) { return __builtin_bit_cast(bf16x8, v); }
+// The two products' operand types: x of the gate and up products is bf16, h of the down product fp16.  What they have in
+// common is written once, for words of two elements each.
+struct Bf16 {
+    static constexpr uint32_t one = 0x3f803f80u, sixteen = 0x41804180u;
+    static constexpr int at = 3;          // a code's lowest bit in 16 + q
+    static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
+    {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+    }
+    static __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    // three numbers that add up to X exactly, two and one to a word
+    static __device__ __forceinline__ uint2 split(float X)
+    {
+        const uint32_t hi = __float_as_uint(X) & 0xffff0000u;
+        const float r = X - __uint_as_float(hi);
+        const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
+        const uint32_t lo = __float_as_uint(r - __uint_as_float(mid));
+        return make_uint2((hi >> 16) | mid, lo >> 16);
+    }
+};
 
-__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
+struct F16 {
+    static constexpr uint32_t one = 0x3c003c00u, sixteen = 0x4c004c00u;
+    static constexpr int at = 6;
+    static __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
+    {
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), __builtin_bit_cast(f16x2, b), c, false);
+    }
+    static __device__ __forceinline__ f32x4 mfma(uint4 a, uint4 b, f32x4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ uint32_t bits(float v) { return __builtin_bit_cast(unsigned short, (_Float16)v); }
+    // (a group's sum stays below 128 * 2^8; parts below 2^-24, 2^-32 of a row's largest element, are lost)
+    static __device__ __forceinline__ uint2 split(float X)
+    {
+        const float hi = __uint_as_float(__float_as_uint(X) & 0xffffe000u), r = X - hi;
+        const float mid = __uint_as_float(__float_as_uint(r) & 0xffffe000u);
+        return make_uint2(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(hi, mid)),
+                          __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(r - mid, 0.0f)));
+    }
+};
+
+// h's scale: the power of two that puts the magnitude with these bits (the largest of a row) into [2^7, 2^8), and its
+// inverse, both of them normal numbers.  An infinity or a NaN stays one.
+__device__ __forceinline__ float h_scale(uint32_t largest, float& inverse)
 {
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, a), __builtin_bit_cast(bf16x2, b), c, false);
+    const uint32_t e = 261u - (largest >> 23);                  // 127 + 7 - (exponent - 127)
+    const uint32_t c = e > 253u ? 253u : e;
+    inverse = __uint_as_float((254u - c) << 23);
+    return __uint_as_float(c << 23);
 }
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // The constants of a conversion, one in a vector register: with two literals the and-or would be two instructions
 struct Conv {
     uint32_t mask, base;
 };
+template <class T>
 __device__ __forceinline__ Conv conv()
 {
-    Conv c{0x00780078u, 0x41804180u};
+    Conv c{0x000f000fu << T::at, T::sixteen};
     asm("" : "+s"(c.mask));
     asm("" : "+v"(c.base));
     return c;
 }
 
-// the bf16 numbers 16 + q of eight codes: pairs (0,4) (1,5) (2,6) (3,7)
-__device__ __forceinline__ uint4 codes_to_bf16(uint32_t w, Conv c)
+// the numbers 16 + q of eight codes: pairs (0,4) (1,5) (2,6) (3,7)
+template <class T>
+__device__ __forceinline__ uint4 codes_to(uint32_t w, Conv c)
 {
-    return make_uint4(((w << 3) & c.mask) | c.base, ((w >> 1) & c.mask) | c.base, ((w >> 5) & c.mask) | c.base,
-                      ((w >> 9) & c.mask) | c.base);
+    constexpr int at = T::at;
+    return make_uint4(((w << at) & c.mask) | c.base, ((at >= 4 ? w << (at & 3) : w >> 1) & c.mask) | c.base,
+                      ((w >> (8 - at)) & c.mask) | c.base, ((w >> (12 - at)) & c.mask) | c.base);
 }
 
-// The products' zero points come off by a matrix instruction too: X, a row's sum of x over a group, as three bf16
-// numbers that add up to it exactly, times -(16 + z).  x side: lane group 0 has the three (row = lane & 15), the
-// others zeros; weight side: the bf16 number -(16 + z) of the lane's column.  (The same 32-deep instruction as the
+// The products' zero points come off by a matrix instruction too: X, a row's sum of x over a group, as three
+// numbers that add up to it, times -(16 + z).  x side: lane group 0 has the three (row = lane & 15), the
+// others zeros; weight side: the number -(16 + z) of the lane's column.  (The same 32-deep instruction as the
 // products': a 16-deep one would do, but a product that took its result as the sum to add to read it too soon,
 // without the wait states that mixed depths need.)
+template <class T>
 __device__ __forceinline__ uint4 split_sum(float X)
 {
-    const uint32_t hi = __float_as_uint(X) & 0xffff0000u;
-    const float r = X - __uint_as_float(hi);
-    const uint32_t mid = __float_as_uint(r) & 0xffff0000u;
-    const uint32_t lo = __float_as_uint(r - __uint_as_float(mid));
-    return make_uint4((hi >> 16) | mid, lo >> 16, 0, 0);
+    const uint2 v = T::split(X);
+    return make_uint4(v.x, v.y, 0, 0);
 }
 
+template <class T>
 __device__ __forceinline__ f32x4 minus_zeros(uint4 X, uint32_t z)
 {
-    const uint32_t v = 0xc180c180u + z * 0x00080008u;
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(X), as_bf16x8(make_uint4(v, v, v, v)), f32x4{0, 0, 0, 0}, 0, 0, 0);
+    const uint32_t v = (T::sixteen | 0x80008000u) + z * (0x00010001u << T::at);
+    return T::mfma(X, make_uint4(v, v, v, v), f32x4{0, 0, 0, 0});
 }
 
 // eight x in the same order
@@ -387,13 +454,14 @@ __device__ __forceinline__ void put_pair(Turn<NT>& turn, const Codes<G, NT>& w)
     wave_fence();
 }
 
-// A pair of chunks of a lane's x row as matrix operands, and each group's sum over the row (lane group 0; 0 in the others)
-template <int G>
+// A pair of chunks of a lane's row of x (bf16) or h (fp16, in the codes' order already) as matrix operands, and each
+// group's sum over the row (lane group 0; 0 in the others)
+template <int G, class T>
 struct XRows {
     static constexpr int U = 2;
     static constexpr int PER = G / 32;                           // MFMAs of a group
     static constexpr int GROUPS = U * 128 / G;
-    bf16x8 f[U][4];
+    uint4 f[U][4];
     float X[GROUPS];
 
     // chunks c and c + 1 of the row at byte `at`
@@ -416,14 +484,13 @@ struct XRows {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[u][i] = as_bf16x8(pair_order(v[u][i]));
-        const bf16x8 ones = as_bf16x8(make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u));
+            for (int i = 0; i < 4; ++i) f[u][i] = std::is_same_v<T, F16> ? v[u][i] : pair_order(v[u][i]);
+        const uint4 ones = make_uint4(T::one, T::one, T::one, T::one);
 #pragma unroll
         for (int n = 0; n < GROUPS; ++n) {
             f32x4 s = {0, 0, 0, 0};                              // ones on the weight side's place: column = row of x
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, f[(n * PER + i) / 4][(n * PER + i) % 4], s, 0, 0, 0);
+            for (int i = 0; i < PER; ++i) s = T::mfma(ones, f[(n * PER + i) / 4][(n * PER + i) % 4], s);
             X[n] = g == 0 ? s[0] : 0.0f;
         }
     }
@@ -431,8 +498,8 @@ struct XRows {
 
 // acc[t] += (x rows) . (weight rows) over the first n chunks.  ahead() is called when the codes have left their
 // registers, ahead_scales(i) when the i-th scales have.
-template <int G, int NT, class F, class S>
-__device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G>& x, Codes<G, NT>& w, Turn<NT>& turn, uint32_t z8,
+template <int G, int NT, class T, class F, class S>
+__device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G, T>& x, Codes<G, NT>& w, Turn<NT>& turn, uint32_t z8,
                                         int n, Conv cv, F&& ahead, S&& ahead_scales)
 {
     constexpr int PER = G / 32, GC = 128 / G;                    // MFMAs of a group, groups of a chunk
@@ -463,15 +530,13 @@ __device__ __forceinline__ void product(f32x4 (&acc)[NT], const XRows<G>& x, Cod
 #pragma unroll
             for (int b = 0; b < GC; ++b) {
                 const int gi = u * GC + b;
-                const uint4 X = split_sum(x.X[gi]);
+                const uint4 X = split_sum<T>(x.X[gi]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const uint32_t qw[4] = {q[t].x, q[t].y, q[t].z, q[t].w};
-                    f32x4 p = minus_zeros(X, sz[t][gi % 4] & 0xffu);
+                    f32x4 p = minus_zeros<T>(X, sz[t][gi % 4] & 0xffu);
 #pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x.f[u][b * PER + i],
-                                                                    as_bf16x8(codes_to_bf16(qw[b * PER + i], cv)), p, 0, 0, 0);
+                    for (int i = 0; i < PER; ++i) p = T::mfma(x.f[u][b * PER + i], codes_to<T>(qw[b * PER + i], cv), p);
                     const float sc = bf16_hi(sz[t][gi % 4]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) acc[t][r] = fmaf(sc, p[r], acc[t][r]);
@@ -543,21 +608,23 @@ __device__ __forceinline__ int tile_prefix(const Int4Ffn& a, int ntn, int* s_pre
 // Four waves a SIMD (at most 128 registers): a workgroup's waves go to the SIMDs in turn from the first, so two of six
 // waves each put four on it, and with registers for three the second would wait for the first to end (down product of 64
 // experts, K = 1408: 114 us a pass so, 88 with four).
-// 67 tokens, top-4 of 128 experts, d 4096, f 1536, groups of 128 with zero points: 141 us for the gate and up products
-// (5.3 TB/s of codes and scales; loads alone, multiplied with nothing, 137), 85 for the down one (4.4 TB/s; 75: its tiles
-// are shorter, and each ends with a sum over the waves).  Run again and again the power limit lowers the clock, 153 and 93.
-//   GATE_UP  h = a(g') u': column tiles 0 .. NC - 1 are the gate's, then the up ones.
-//   else     y = h W2^T
+// 67 tokens, top-4 of 128 experts, d 4096, f 1536, groups of 128 with zero points, passes apart: 141 us for the gate and up
+// products (5.3 TB/s of codes and scales; loads alone, multiplied with nothing, 137), 91 for the down one (4.1 TB/s; 75: its
+// tiles are shorter, and each ends with a sum over the waves).  Passes back to back take 20% longer in the median, the power
+// limit lowers the clock: 162 and 107.
+//   GATE_UP  h = a(g') u', in fp32: column tiles 0 .. NC - 1 are the gate's, then the up ones.
+//   else     y = h W2^T, h as int4_narrow_kernel leaves it
 template <int G, bool GATE_UP>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))) void int4_rows_kernel(
-    Int4Ffn a, uint16_t* __restrict__ h, float* __restrict__ y)
+    Int4Ffn a, float* __restrict__ h32, const uint16_t* __restrict__ h, const float* __restrict__ hinv, float* __restrict__ y)
 {
+    using T = std::conditional_t<GATE_UP, Bf16, F16>;
     constexpr int NC = GATE_UP ? 1 : 2, NT = 2, U = 2;
     const int W = blockDim.x >> 6;
     extern __shared__ __align__(16) uint8_t smem[];
     Turn<NT>* turn = reinterpret_cast<Turn<NT>*>(smem);
     float (*red)[NT][256] = reinterpret_cast<float (*)[NT][256]>(smem + W * sizeof(Turn<NT>));   // [2 W]
-    __shared__ int ok[2][16];
+    __shared__ float factor[2][16];      // of a row's results: 0 for a foreign one
     __shared__ int s_pref[kMaxExperts + 1];
     const int N = GATE_UP ? a.f : a.d, K = GATE_UP ? a.d : a.f;
     const int ntn = (N + 16 * NC - 1) / (16 * NC);
@@ -588,9 +655,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
     const int steps = (last - first) * blocks;
     const auto xb = GATE_UP ? buf_of(a.x, (int64_t)a.T * a.d * 2) : buf_of(h, R * a.f * 2);
     uint32_t xat = 0;
-    bool in = true;
+    float mine = 1.0f;
     int64_t have = -1;       // row of h whose tile's operands are held
-    XRows<G> x;
+    XRows<G, T> x;
     f32x4 acc[NT];
     int buf = 0;
 
@@ -601,7 +668,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
         return where_of<G>(w_buf(GATE_UP ? a.w13 : a.w2, t.e, GATE_UP ? 2 * N : N, K, G), row, (kb * W + wave) * U, K, live);
     };
     const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
-    const Conv cv = conv();
+    const Conv cv = conv<T>();
     auto step = [&](Codes<G, NT>& c, const Tile& t, int kb, const Where<NT>& p) __attribute__((always_inline)) {
         const int c0 = (kb * W + wave) * U, n = min(U, chunks - c0);
         if (have != t.row0 || blocks > 1) {
@@ -610,12 +677,14 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
                 const int64_t row = t.row0 + min(m, t.valid - 1);
                 if constexpr (GATE_UP) {
                     const int64_t slot = a.src_slot[row];
-                    in = slot >= 0 && slot < R;
+                    const bool in = slot >= 0 && slot < R;
+                    mine = in ? 1.0f : 0.0f;
                     if (slot >= R && a.dev_err && threadIdx.x < 16)
                         atomicOr(a.dev_err, (int)MOE_ERR_ROW_RANGE);
                     xat = in ? (uint32_t)(slot / a.k * a.d * 2) : 0;
                 } else {
                     xat = (uint32_t)(row * a.f * 2);
+                    mine = hinv[row];
                 }
                 have = t.row0;
             }
@@ -625,10 +694,10 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
 #pragma unroll
             for (int i = 0; i < NT; ++i) acc[i] = f32x4{0, 0, 0, 0};
         }
-        product<G, NT>(acc, x, c, turn[wave], z8, n, cv, [&]() __attribute__((always_inline)) { load_pair(c, p, K); },
+        product<G, NT, T>(acc, x, c, turn[wave], z8, n, cv, [&]() __attribute__((always_inline)) { load_pair(c, p, K); },
                        [&](int i) __attribute__((always_inline)) { load_scales(c, p, i); });
         if (kb + 1 < blocks) return;
-        if (threadIdx.x < 16) ok[buf][m] = in;
+        if (threadIdx.x < 16) factor[buf][m] = mine;
         put_acc<NT>(red + buf * W, acc);
         for (int i = threadIdx.x; i < NC * 256; i += 64 * W) {
             const int idx = i & 255, j = i >> 8, r = idx >> 4, col = (t.nt * NC + j) * 16 + (idx & 15);
@@ -637,9 +706,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
             if constexpr (GATE_UP) {
                 const float L = a.glu.limit, g = limit_g(v, L), u = limit_u(wave_sum<NT>(red + buf * W, W, j + NC, idx), L);
                 with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) { v = act_of<decltype(A)::value, true>(g) * u; });
-                h[(t.row0 + r) * a.f + col] = ok[buf][r] ? (uint16_t)f32_to_bf16_bits(v) : 0;
+                h32[(t.row0 + r) * a.f + col] = factor[buf][r] ? v : 0.0f;
             } else {
-                y[(t.row0 + r) * a.d + col] = v;
+                y[(t.row0 + r) * a.d + col] = v * factor[buf][r];
             }
         }
         buf ^= 1;
@@ -666,10 +735,10 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4))
 // a code is converted once for 64 products.  x passes through LDS in chunks of 128, two in turn and one barrier a chunk;
 // codes as in the kernel for few rows.  Bound by the issue of vector instructions, so what a row needs once is not done
 // again for each tile of columns: rows come in the codes' order with their sums (fp32, over each 32), x from
-// int4_order_kernel, h from the gate and up products' tiles.
-// 1000 tokens, top-2 of 8 experts, d 2048, f 1152, groups of 64 with zero points: 54 us for the gate and up products, 33
-// for the down one (350 and 290 TFLOP/s), 5 for the order of x; with order and sums made in every tile and the compiler's
-// order of loads from LDS 62 and 39.  Eight waves a workgroup, which share x among more columns: 71.
+// int4_order_kernel, h from int4_narrow_kernel.
+// 1000 tokens, top-2 of 8 experts, d 2048, f 1152, groups of 64 with zero points: 54 us for the gate and up products, 34
+// for the down one (350 and 280 TFLOP/s), 5 each for the order of x and h's narrowing; with order and sums made in every
+// tile and the compiler's order of loads from LDS 62 and 39.  Eight waves a workgroup, which share x among more columns: 71.
 constexpr int kTileRows = 64, kTileWaves = 4;
 
 struct XStage {
@@ -679,11 +748,11 @@ struct XStage {
 };
 
 // eight elements of a row in the codes' order, and in each of four neighbouring lanes the sum of their 32
+template <class T>
 __device__ __forceinline__ uint4 order_and_sum(uint4 v, float& sum)
 {
-    constexpr uint32_t one = 0x3f803f80u;
     v = pair_order(v);
-    sum = dot2(v.x, one, dot2(v.y, one, dot2(v.z, one, dot2(v.w, one, 0.0f))));
+    sum = T::dot2(v.x, T::one, T::dot2(v.y, T::one, T::dot2(v.z, T::one, T::dot2(v.w, T::one, 0.0f))));
     sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0xB1, 0xF, 0xF, true));
     sum += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(sum), 0x4E, 0xF, 0xF, true));
     return v;
@@ -695,17 +764,69 @@ __global__ __launch_bounds__(256) void int4_order_kernel(const uint4* __restrict
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
         float sum;
-        xo[i] = order_and_sum(x[i], sum);
+        xo[i] = order_and_sum<Bf16>(x[i], sum);
         if (threadIdx.x % 4 == 0) sums[i / 4] = sum;
     }
 }
 
-// rows of x (GATE_UP: of h) and their sums as above; h and hsum alike
+// h in fp32 -> fp16 in the codes' order, a scale for each row and its inverse (hinv), and the sums of what is stored.
+// TPR threads share a row; a thread's first eight elements stay in its registers between the row's largest and the
+// rounding, the others are read again.
+template <int TPR>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void int4_narrow_kernel(const float* __restrict__ h32, int64_t rows, int f,
+                                                                          uint4* __restrict__ h, float* __restrict__ hsum,
+                                                                          float* __restrict__ hinv)
+{
+    constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR;
+    const int lane = threadIdx.x % TPR, n8 = f / 8;
+    if (row >= rows) return;                             // (whole waves; a row of several has its workgroup to itself)
+    const float4* src = reinterpret_cast<const float4*>(h32 + row * f);
+    auto largest_of = [](float4 a, float4 b) __attribute__((always_inline)) {
+        const uint32_t p = max(max(magnitude(a.x), magnitude(a.y)), max(magnitude(a.z), magnitude(a.w)));
+        return max(p, max(max(magnitude(b.x), magnitude(b.y)), max(magnitude(b.z), magnitude(b.w))));
+    };
+    float4 a{}, b{};
+    if (lane < n8) {
+        a = src[2 * lane];
+        b = src[2 * lane + 1];
+    }
+    uint32_t largest = largest_of(a, b);
+    for (int i = lane + TPR; i < n8; i += TPR) largest = max(largest, largest_of(src[2 * i], src[2 * i + 1]));
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) largest = max(largest, (uint32_t)__shfl_xor((int)largest, o, 64));
+    if constexpr (TPR > 64) {
+        __shared__ uint32_t of_wave[TPR / 64];
+        if (threadIdx.x % 64 == 0) of_wave[threadIdx.x / 64] = largest;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) largest = max(largest, of_wave[i]);
+    }
+    float inverse;
+    const float scale = h_scale(largest, inverse);
+    if (lane == 0) hinv[row] = inverse;
+    for (int i = lane; i < n8; i += TPR) {               // (n8 is a multiple of 4: four neighbours stay together)
+        if (i != lane) {
+            a = src[2 * i];
+            b = src[2 * i + 1];
+        }
+        const uint4 v = make_uint4(F16::bits(a.x * scale) | F16::bits(a.y * scale) << 16,
+                                   F16::bits(a.z * scale) | F16::bits(a.w * scale) << 16,
+                                   F16::bits(b.x * scale) | F16::bits(b.y * scale) << 16,
+                                   F16::bits(b.z * scale) | F16::bits(b.w * scale) << 16);
+        float sum;
+        h[row * n8 + i] = order_and_sum<F16>(v, sum);
+        if (lane % 4 == 0) hsum[(row * n8 + i) / 4] = sum;
+    }
+}
+
+// rows of x (else: of h) and their sums as above -> h in fp32 (y)
 template <int G, bool GATE_UP>
 __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu(2))) void int4_tile_kernel(
-    Int4Ffn a, const uint16_t* __restrict__ rows, const float* __restrict__ sums, uint16_t* __restrict__ h,
-    float* __restrict__ hsum, float* __restrict__ y)
+    Int4Ffn a, const uint16_t* __restrict__ rows, const float* __restrict__ sums, const float* __restrict__ hinv,
+    float* __restrict__ result)
 {
+    using T = std::conditional_t<GATE_UP, Bf16, F16>;
     constexpr int NT = 2, NC = GATE_UP ? 1 : 2, MT = kTileRows / 16, GC = 128 / G, PER = G / 32;
     constexpr int XR = kTileRows / (4 * kTileWaves);     // rows that a thread brings in
     extern __shared__ __align__(16) uint8_t smem[];
@@ -757,7 +878,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
         float v = xsum;
         if constexpr (G >= 64) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, true));
         if constexpr (G >= 128) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, true));
-        xs.sum[st][s32 / (G / 32)][sr] = split_sum(v);       // (by each of a group's lanes: no branch among the products)
+        xs.sum[st][s32 / (G / 32)][sr] = split_sum<T>(v);       // (by each of a group's lanes: no branch among the products)
     };
 
     int row0[NT];
@@ -775,7 +896,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     Codes<G, NT> w;
     uint32_t sz[NT][4];
     const uint32_t z8 = (GATE_UP ? a.w13 : a.w2).zeros ? 0 : 8;
-    const Conv cv = conv();
+    const Conv cv = conv<T>();
     if (threadIdx.x < kTileRows) xs.none[threadIdx.x] = make_uint4(0, 0, 0, 0);
     load_all(w, where_of<G>(wb, row0, 0, K, live), K);
 #pragma unroll
@@ -809,13 +930,13 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
         uint4 q[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) q[t] = turn[wave].part[t][m][(4 * u + g) ^ (m >> 1)];
-        bf16x8 xf[2][MT];
+        uint4 xf[2][MT];
         uint4 X[MT];
         auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 if (j % PER == 0) X[mt] = (g == 0 ? xs.sum[u][j / PER] : xs.none)[16 * mt + m];
-                xf[j & 1][mt] = as_bf16x8(xs.part[u][16 * mt + m][(G == 128 ? 4 * g + j : 4 * j + g) ^ m]);
+                xf[j & 1][mt] = xs.part[u][16 * mt + m][(G == 128 ? 4 * g + j : 4 * j + g) ^ m];
             }
         };
         read(0);
@@ -826,7 +947,7 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
         f32x4 p[MT][NT];
         auto begin = [&](int t, int b) __attribute__((always_inline)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) p[mt][t] = minus_zeros(X[mt], sz[t][(u * GC + b) % 4] & 0xffu);
+            for (int mt = 0; mt < MT; ++mt) p[mt][t] = minus_zeros<T>(X[mt], sz[t][(u * GC + b) % 4] & 0xffu);
         };
 #pragma unroll
         for (int t = 0; t < NT; ++t) begin(t, 0);
@@ -837,10 +958,9 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const bf16x8 wf = as_bf16x8(codes_to_bf16(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, cv));
+                const uint4 wf = codes_to<T>(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, cv);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    p[mt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j & 1][mt], wf, p[mt][t], 0, 0, 0);
+                for (int mt = 0; mt < MT; ++mt) p[mt][t] = T::mfma(xf[j & 1][mt], wf, p[mt][t]);
             }
 #pragma unroll
             for (int i = j * XR / 4; i < (j + 1) * XR / 4; ++i) {
@@ -874,10 +994,9 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
     if (chunks & 1) chunk(chunks - 1, std::integral_constant<int, 0>{});
 
     // the tile leaves through LDS as rows (the loop's last barrier has freed it)
-    using Out = std::conditional_t<GATE_UP, uint16_t, float>;
-    constexpr int COLS = 16 * NC * kTileWaves, VEC = 16 / sizeof(Out), PITCH = COLS + VEC;
-    static_assert(kTileRows * PITCH * sizeof(Out) <= sizeof(XStage) + kTileWaves * sizeof(Turn<NT>), "the tile fits");
-    Out* out = reinterpret_cast<Out*>(smem);
+    constexpr int COLS = 16 * NC * kTileWaves, PITCH = COLS + 4;
+    static_assert(kTileRows * PITCH * sizeof(float) <= sizeof(XStage) + kTileWaves * sizeof(Turn<NT>), "the tile fits");
+    float* out = reinterpret_cast<float*>(smem);
     auto stage = [&](auto&& value) __attribute__((always_inline)) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -890,26 +1009,22 @@ __global__ __launch_bounds__(64 * kTileWaves) __attribute__((amdgpu_waves_per_eu
         const float L = a.glu.limit;
         with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) {
             stage([&](int mt, int t, int r) __attribute__((always_inline)) {
-                return (uint16_t)f32_to_bf16_bits(act_of<decltype(A)::value, true>(limit_g(acc[mt][t][r], L)) *
-                                                  limit_u(acc[mt][t + NC][r], L));
+                return act_of<decltype(A)::value, true>(limit_g(acc[mt][t][r], L)) * limit_u(acc[mt][t + NC][r], L);
             });
         });
     } else {
         stage([&](int mt, int t, int r) __attribute__((always_inline)) { return acc[mt][t][r]; });
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < tile.rows_valid * (COLS / VEC); i += 64 * kTileWaves) {
-        const int r = i / (COLS / VEC), c = VEC * (i % (COLS / VEC)), col = tile.nt * COLS + c;
-        if (col >= N) continue;                  // (N is a multiple of 32: four neighbours stay together)
-        uint4 v = *reinterpret_cast<const uint4*>(out + r * PITCH + c);
-        if constexpr (GATE_UP) {
-            float sum;
-            v = order_and_sum(v, sum);
-            if (i % 4 == 0) hsum[(tile.row0 + r) * (N / 32) + col / 32] = sum;
-            *reinterpret_cast<uint4*>(h + (tile.row0 + r) * N + col) = v;
-        } else {
-            *reinterpret_cast<uint4*>(y + (tile.row0 + r) * N + col) = v;
+    for (int i = threadIdx.x; i < tile.rows_valid * (COLS / 4); i += 64 * kTileWaves) {
+        const int r = i / (COLS / 4), c = 4 * (i % (COLS / 4)), col = tile.nt * COLS + c;
+        if (col >= N) continue;
+        float4 v = *reinterpret_cast<const float4*>(out + r * PITCH + c);
+        if constexpr (!GATE_UP) {
+            const float k = hinv[tile.row0 + r];
+            v = make_float4(v.x * k, v.y * k, v.z * k, v.w * k);
         }
+        *reinterpret_cast<float4*>(result + (tile.row0 + r) * N + col) = v;
     }
 }
 
@@ -918,8 +1033,8 @@ constexpr int kTokenWaves = 8;
 // A single row of x has no use for a matrix instruction.  Here a lane multiplies the codes where they arrive: eight
 // neighbouring lanes have 256 consecutive codes of a row, 32 each, the same 32 of every row that passes, so that the
 // lane's x stay in registers; a wave instruction is eight rows x 128 bytes.  Two products an instruction
-// (v_dot2c_f32_bf16) on the same 16 + q operands.  One token, 4 of 128 experts, d 4096, f 1536: 9.0 and 5.3 us for the
-// two kernels, a launch and one chain of load latencies each (its 39 MB take 6.1 us at 6.4 TB/s); with the few-row
+// (v_dot2c_f32_bf16, v_dot2c_f32_f16) on the same 16 + q operands.  One token, 4 of 128 experts, d 4096, f 1536: 9.0 and
+// 4.5 us for the two kernels, a launch and one chain of load latencies each (its 39 MB take 6.1 us at 6.4 TB/s); with the few-row
 // kernel 20 us for the pass.
 // 32 consecutive x of a lane in the codes' order, and their sum
 struct X32 {
@@ -934,34 +1049,73 @@ struct X32 {
     __device__ __forceinline__ void order()
     {
         float a = 0.0f, b = 0.0f;
-        constexpr uint32_t one = 0x3f803f80u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = pair_order(v[i]);
-            a = dot2(v[i].x, one, a);
-            b = dot2(v[i].y, one, b);
-            a = dot2(v[i].z, one, a);
-            b = dot2(v[i].w, one, b);
+            a = Bf16::dot2(v[i].x, Bf16::one, a);
+            b = Bf16::dot2(v[i].y, Bf16::one, b);
+            a = Bf16::dot2(v[i].z, Bf16::one, a);
+            b = Bf16::dot2(v[i].w, Bf16::one, b);
         }
         sum = a + b;
     }
+    // sum x (q - zero) over a lane's 32 codes
+    __device__ __forceinline__ float times(uint4 q, float zero16, Conv cv) const
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 c = codes_to<Bf16>(w[i], cv);
+            a = Bf16::dot2(c.x, v[i].x, a);
+            b = Bf16::dot2(c.y, v[i].y, b);
+            a = Bf16::dot2(c.z, v[i].z, a);
+            b = Bf16::dot2(c.w, v[i].w, b);
+        }
+        return fmaf(-zero16, sum, a + b);
+    }
 };
 
-// sum x (q - zero) over a lane's 32 codes
-__device__ __forceinline__ float dot32(uint4 q, const X32& x, float zero16, Conv cv)
-{
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    float a = 0.0f, b = 0.0f;
+// 32 consecutive h, fp16 with a scale for each 16: the columns that one workgroup of the gate and up products makes
+struct H32 {
+    uint4 v[4];
+    float inv[2], sum;
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t h, __amdgpu_buffer_rsrc_t hinv, uint32_t at, uint32_t past)
+    {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint4 c = codes_to_bf16(w[i], cv);
-        a = dot2(c.x, x.v[i].x, a);
-        b = dot2(c.y, x.v[i].y, b);
-        a = dot2(c.z, x.v[i].z, a);
-        b = dot2(c.w, x.v[i].w, b);
+        for (int i = 0; i < 4; ++i) v[i] = load16(h, (at * 2 | past) + 16 * i);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            inv[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(hinv, (int)((at / 4 | past) + 4 * i), 0, 0));
     }
-    return fmaf(-zero16, x.sum, a + b);
-}
+    // the two halves' sums of products with c, each with its scale
+    template <class F>
+    __device__ __forceinline__ float halves(F&& c) const
+    {
+        float part[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 w = c(i);
+            part[i / 2] = F16::dot2(w.x, v[i].x, part[i / 2]);
+            part[i / 2] = F16::dot2(w.y, v[i].y, part[i / 2]);
+            part[i / 2] = F16::dot2(w.z, v[i].z, part[i / 2]);
+            part[i / 2] = F16::dot2(w.w, v[i].w, part[i / 2]);
+        }
+        return fmaf(part[0], inv[0], part[1] * inv[1]);
+    }
+    __device__ __forceinline__ void order()
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = pair_order(v[i]);
+        sum = halves([](int) __attribute__((always_inline)) { return make_uint4(F16::one, F16::one, F16::one, F16::one); });
+    }
+    __device__ __forceinline__ float times(uint4 q, float zero16, Conv cv) const
+    {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        return fmaf(-zero16, sum, halves([&](int i) __attribute__((always_inline)) { return codes_to<F16>(w[i], cv); }));
+    }
+};
 
 // one load of a lane: its 32 codes of a row, their scale and zero point
 struct Q32 {
@@ -975,9 +1129,10 @@ struct Q32 {
         s = __builtin_amdgcn_raw_buffer_load_b16(w.scales, (int)(at * 2 | past), 0, 0);
         z = __builtin_amdgcn_raw_buffer_load_b8(w.zeros, (int)(at | past), 0, 0);
     }
-    __device__ __forceinline__ float times(const X32& x, uint32_t z8, Conv cv) const
+    template <class X>
+    __device__ __forceinline__ float times(const X& x, uint32_t z8, Conv cv) const
     {
-        return bf16_lo(s) * dot32(q, x, (float)(16 + z8 + z), cv);
+        return bf16_lo(s) * x.times(q, (float)(16 + z8 + z), cv);
     }
 };
 
@@ -999,9 +1154,11 @@ __device__ __forceinline__ int expert_of(const Int4Ffn& a, int64_t p, bool flag)
     return bad || dst < 0 ? -1 : e;
 }
 
-// h = a(g') u' of 16 columns for slot blockIdx.y: eight waves share K in slices of 256, two at a time
+// h = a(g') u' of 16 columns for slot blockIdx.y, with their scale's inverse: eight waves share K in slices of 256, two at
+// a time
 template <int G>
-__global__ __launch_bounds__(64 * kTokenWaves) void int4_gate_up_token_kernel(Int4Ffn a, uint16_t* __restrict__ h)
+__global__ __launch_bounds__(64 * kTokenWaves) void int4_gate_up_token_kernel(Int4Ffn a, uint16_t* __restrict__ h,
+                                                                            float* __restrict__ hinv)
 {
     constexpr int U = 2;
     __shared__ float red[kTokenWaves][32];
@@ -1014,7 +1171,7 @@ __global__ __launch_bounds__(64 * kTokenWaves) void int4_gate_up_token_kernel(In
     const auto xb = buf_of(a.x, (int64_t)a.T * K * 2);
     const uint32_t xat = (uint32_t)(p / a.k * K * 2), z8 = a.w13.zeros ? 0 : 8;
     const int row = blockIdx.x * 16 + (lane >> 3);
-    const Conv cv = conv();
+    const Conv cv = conv<Bf16>();
     float acc[4] = {};
     for (int s0 = wave * U; s0 < slices; s0 += kTokenWaves * U) {
         Q32 q[U][4];
@@ -1051,27 +1208,34 @@ __global__ __launch_bounds__(64 * kTokenWaves) void int4_gate_up_token_kernel(In
     u = limit_u(u, a.glu.limit);
     float v = 0.0f;
     with_act(a.glu.act, [&](auto A) __attribute__((always_inline)) { v = act_of<decltype(A)::value, true>(g) * u; });
-    h[p * a.f + blockIdx.x * 16 + threadIdx.x] = (uint16_t)f32_to_bf16_bits(v);
+    uint32_t largest = magnitude(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) largest = max(largest, neighbour(largest, i));
+    float inverse;
+    const float scale = h_scale(largest, inverse);
+    h[p * a.f + blockIdx.x * 16 + threadIdx.x] = (uint16_t)F16::bits(v * scale);
+    if (threadIdx.x == 0) hinv[p * (a.f / 16) + blockIdx.x] = inverse;
 }
 
 // out[t] = sum_j topk_w_j (h_j W2[e_j]^T) of 16 columns of token blockIdx.y: the slices of all its slots are shared by
 // eight waves, three at a time, a slice's sum times its slot's weight, so that one sum over the waves is the combine
 template <int G>
-__global__ __launch_bounds__(64 * kTokenWaves) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h)
+__global__ __launch_bounds__(64 * kTokenWaves) void int4_down_token_kernel(Int4Ffn a, const uint16_t* __restrict__ h,
+                                                                         const float* __restrict__ hinv)
 {
     constexpr int U = 3;
     __shared__ float red[kTokenWaves][16];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t t = blockIdx.y;
     const int K = a.f, slices = (K + 255) / 256, items = a.k * slices;
-    const auto hb = buf_of(h, (int64_t)a.T * a.k * K * 2);
+    const auto hb = buf_of(h, (int64_t)a.T * a.k * K * 2), ib = buf_of(hinv, (int64_t)a.T * a.k * (K / 16) * 4);
     const uint32_t z8 = a.w2.zeros ? 0 : 8;
     const int row = blockIdx.x * 16 + (lane >> 3);
-    const Conv cv = conv();
+    const Conv cv = conv<F16>();
     float acc[2] = {};
     for (int i0 = wave; i0 < items; i0 += kTokenWaves * U) {
         Q32 q[U][2];
-        X32 x[U];
+        H32 x[U];
         float c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -1086,7 +1250,7 @@ __global__ __launch_bounds__(64 * kTokenWaves) void int4_down_token_kernel(Int4F
             const WBuf w = w_buf(a.w2, max(e, 0), a.d, K, G);
             q[u][0].load(w, row, k0, K, G, past);
             q[u][1].load(w, row + 8, k0, K, G, past);
-            x[u].load(hb, (uint32_t)((p * K + k0) * 2) | past);
+            x[u].load(hb, ib, (uint32_t)(p * K + k0), past);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -1109,7 +1273,7 @@ __global__ __launch_bounds__(64 * kTokenWaves) void int4_down_token_kernel(Int4F
 }
 
 // out[t] = sum_j topk_w[t, j] * y[dst_row[t, j]] over the slots that have an expert and a row, rounded once: y is fp32, as a
-// rounding of it to bf16 would cost more of the result's accuracy than the one of h does.  A thread makes 8 columns.
+// rounding of it to bf16 would cost as much of the result's accuracy as the output's.  A thread makes 8 columns.
 template <int K>
 __global__ __launch_bounds__(256) void int4_combine_kernel(const float4* __restrict__ y, const int32_t* __restrict__ topk_idx,
                                                            const int32_t* __restrict__ dst_row, const float* __restrict__ w,
@@ -1155,8 +1319,17 @@ int cu_count()
     return n;
 }
 
+// Where a pass's h and expert outputs lie in the workspace
+struct Int4Ws {
+    float* h32;       // [R, f]; for single tokens the inverse scales [R, f / 16]
+    uint16_t* h;      // [R, f]
+    float* hsum;      // [R, f / 32]
+    float* hinv;      // [R]
+    float* y;         // [R, d]
+};
+
 template <int G, bool UP>
-void launch_rows(const Int4Ffn& a, uint16_t* h, float* y, hipStream_t s)
+void launch_rows(const Int4Ffn& a, const Int4Ws& w, hipStream_t s)
 {
     constexpr int NT = 2, COLS = UP ? 16 : 32;
     const int N = UP ? a.f : a.d, K = UP ? a.d : a.f, need = (K + 255) / 256, W = need < kWaves ? need : kWaves;
@@ -1171,32 +1344,49 @@ void launch_rows(const Int4Ffn& a, uint16_t* h, float* y, hipStream_t s)
     const int64_t fit = (int64_t)(156 << 10) / (lds + 4 * kMaxExperts + 256);
     per_cu = per_cu < 1 ? 1 : per_cu < fit ? per_cu : fit;
     hipLaunchKernelGGL((int4_rows_kernel<G, UP>), dim3((unsigned)(tiles < cus * per_cu ? tiles : cus * per_cu)), dim3(64 * W),
-                       lds, s, a, h, y);
+                       lds, s, a, w.h32, w.h, w.hinv, w.y);
+}
+
+void launch_narrow(const Int4Ffn& a, const Int4Ws& w, hipStream_t s)
+{
+    const int64_t R = (int64_t)a.T * a.k;
+    // a vector of eight a thread, where a workgroup is that long
+    if (a.f <= 8 * 64)
+        hipLaunchKernelGGL(int4_narrow_kernel<64>, dim3((unsigned)((R + 3) / 4)), dim3(256), 0, s, w.h32, R, a.f, (uint4*)w.h,
+                           w.hsum, w.hinv);
+    else if (a.f <= 8 * 256)
+        hipLaunchKernelGGL(int4_narrow_kernel<256>, dim3((unsigned)R), dim3(256), 0, s, w.h32, R, a.f, (uint4*)w.h, w.hsum,
+                           w.hinv);
+    else
+        hipLaunchKernelGGL(int4_narrow_kernel<1024>, dim3((unsigned)R), dim3(1024), 0, s, w.h32, R, a.f, (uint4*)w.h, w.hsum,
+                           w.hinv);
 }
 
 template <int G>
-void launch_tiles(const Int4Ffn& a, uint16_t* h, float* hsum, float* y, hipStream_t s)
+void launch_tiles(const Int4Ffn& a, const Int4Ws& w, hipStream_t s)
 {
     const int64_t R = (int64_t)a.T * a.k, mt = R / kTileRows + (R < a.E ? R : a.E);
-    auto go = [&](auto UP_, const uint16_t* rows, const float* sums) {
+    auto go = [&](auto UP_, const uint16_t* rows, const float* sums, float* result) {
         constexpr bool UP = decltype(UP_)::value;
         constexpr int COLS = (UP ? 16 : 32) * kTileWaves;
         const int64_t ntn = ((UP ? a.f : a.d) + COLS - 1) / COLS;
         hipLaunchKernelGGL((int4_tile_kernel<G, UP>), dim3((unsigned)((mt * ntn + 7) / 8 * 8)), dim3(64 * kTileWaves),
-                           sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, rows, sums, h, hsum, y);
+                           sizeof(XStage) + kTileWaves * sizeof(Turn<2>), s, a, rows, sums, w.hinv, result);
     };
     // x in the codes' order and its sums lie where y will, which is longer
     const int64_t n8 = (int64_t)a.T * (a.d / 8), blocks = (n8 + 255) / 256;
-    uint16_t* xo = reinterpret_cast<uint16_t*>(y);
+    uint16_t* xo = reinterpret_cast<uint16_t*>(w.y);
     float* xsum = reinterpret_cast<float*>(xo + (int64_t)a.T * a.d);
     hipLaunchKernelGGL(int4_order_kernel, dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)), dim3(256), 0, s,
                        (const uint4*)a.x, n8, (uint4*)xo, xsum);
-    go(std::true_type{}, xo, xsum);
-    go(std::false_type{}, h, hsum);
+    go(std::true_type{}, xo, xsum, w.h32);
+    launch_narrow(a, w, s);
+    go(std::false_type{}, w.h, w.hsum, w.y);
 }
 
 // Which kernels.  Times of a whole pass, us, in a graph; A: d 4096, f 1536, top-4 of 128; B: d 2048, f 1024, 8 experts;
-// C: d 2048, f 1408, top-6 of 64; D: d 5120, f 2560, top-2 of 16.
+// C: d 2048, f 1408, top-6 of 64; D: d 5120, f 2560, top-2 of 16.  (With h in bf16; in fp16 a pass takes 0 to 3 us more
+// by slot, 2 to 5 in rows.)
 // Slot by slot or rows together: a slot by itself reads its expert's matrices once more, which costs nothing while
 // few slots share one, or the second reading is from a cache.
 //   slots      A: 16  32  48  64      B, top-2: 8  12  16    B, top-4: 16  24      C: 30  48      D: 32
@@ -1271,37 +1461,50 @@ hipError_t launch_dequantize_int4(const uint8_t* codes, const uint16_t* scales, 
 
 size_t int4_ws_bytes(int64_t n_rows, int d, int f)
 {
-    return up256((size_t)n_rows * f * 2) + up256((size_t)n_rows * (f / 32) * 4) + up256((size_t)n_rows * d * 4) + 256;
+    const size_t R = (size_t)n_rows;
+    return up256(R * f * 4) + up256(R * f * 2) + up256(R * (f / 32) * 4) + up256(R * 4) + up256(R * d * 4) + 256;
 }
 
 hipError_t launch_int4_ffn(const Int4Ffn& a, hipStream_t s)
 {
     if (a.T == 0) return hipSuccess;
     const int64_t R = (int64_t)a.T * a.k;
-    uint16_t* h = reinterpret_cast<uint16_t*>(a.ws);
-    float* hsum = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.ws) + up256((size_t)R * a.f * 2));
-    float* y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(hsum) + up256((size_t)R * (a.f / 32) * 4));
+    uint8_t* at = reinterpret_cast<uint8_t*>(a.ws);
+    auto take = [&](size_t bytes) {
+        uint8_t* p = at;
+        at += up256(bytes);
+        return p;
+    };
+    Int4Ws w;
+    w.h32 = reinterpret_cast<float*>(take((size_t)R * a.f * 4));
+    w.h = reinterpret_cast<uint16_t*>(take((size_t)R * a.f * 2));
+    w.hsum = reinterpret_cast<float*>(take((size_t)R * (a.f / 32) * 4));
+    w.hinv = reinterpret_cast<float*>(take((size_t)R * 4));
+    w.y = reinterpret_cast<float*>(take((size_t)R * a.d * 4));
     hipError_t e;
     if (R <= kTokenSlots && 2 * R <= 3 * a.E) {
         return with_group(a.group, [&](auto g) {
             constexpr int G = decltype(g)::value;
-            hipLaunchKernelGGL((int4_gate_up_token_kernel<G>), dim3(a.f / 16, (unsigned)R), dim3(64 * kTokenWaves), 0, s, a, h);
-            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), dim3(64 * kTokenWaves), 0, s, a, h);
+            hipLaunchKernelGGL((int4_gate_up_token_kernel<G>), dim3(a.f / 16, (unsigned)R), dim3(64 * kTokenWaves), 0, s, a, w.h,
+                               w.h32);
+            hipLaunchKernelGGL((int4_down_token_kernel<G>), dim3(a.d / 16, (unsigned)a.T), dim3(64 * kTokenWaves), 0, s, a, w.h,
+                               w.h32);
         });
     }
     if (R >= (int64_t)kTileMinRows * a.E) {
-        e = with_group(a.group, [&](auto g) { launch_tiles<decltype(g)::value>(a, h, hsum, y, s); });
+        e = with_group(a.group, [&](auto g) { launch_tiles<decltype(g)::value>(a, w, s); });
     } else {
         e = with_group(a.group, [&](auto g) {
-            launch_rows<decltype(g)::value, true>(a, h, y, s);
-            launch_rows<decltype(g)::value, false>(a, h, y, s);
+            launch_rows<decltype(g)::value, true>(a, w, s);
+            launch_narrow(a, w, s);
+            launch_rows<decltype(g)::value, false>(a, w, s);
         });
     }
     if (e != hipSuccess) return e;
     const int64_t n = (int64_t)a.T * (a.d / 8), blocks = (n + 255) / 256;
     e = with_k(a.k, [&](auto kc) {
         hipLaunchKernelGGL((int4_combine_kernel<decltype(kc)::value>), dim3((unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks)),
-                           dim3(256), 0, s, (const float4*)y, a.topk_idx, a.dst_row, a.topk_w, a.T, a.E, a.d / 8, (uint4*)a.out,
+                           dim3(256), 0, s, (const float4*)w.y, a.topk_idx, a.dst_row, a.topk_w, a.T, a.E, a.d / 8, (uint4*)a.out,
                            a.dev_err);
     });
     if (e != hipSuccess) return e;

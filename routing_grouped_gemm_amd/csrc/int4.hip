@@ -59,8 +59,8 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 //     crosses none if it was not: what is rounded to an integer rounds as the exact quotient does;
 //   - the integer comes from adding 1.5 * 2^23 + 16 (even: ties stay ties of the same parity), four of them share a word
 //     from there on.
-// [49152, 4096] with groups of 128, caches cold: quantised in 91 us (5.6 TB/s; with a division an element 194),
-// decoded in 94 (5.4 TB/s; 119 with one vector a thread and rounding by hand).
+// [49152, 4096] with groups of 128: quantised in 82 us (6.2 TB/s, caches cold or not; with a division an element twice as
+// long), decoded in 109 with the caches cold (4.7 TB/s) and 70 where they hold part of the codes.
 constexpr int kVec = 2;                   // vectors a thread, their loads in flight together
 constexpr int64_t kMaxBlocks = 1 << 20;
 typedef __attribute__((ext_vector_type(4))) uint32_t vu4;
@@ -355,8 +355,8 @@ __device__ __forceinline__ uint4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off)
 
 // A pair of consecutive chunks of 128 codes of NT column tiles on their way: 16 rows x 128 bytes each in two loads,
 // eight neighbouring lanes a row's 128 bytes.  (Each lane loading the codes of its own column, as the matrix operand
-// has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 168 us instead of 145 for the
-// gate and up products of the few-row kernel's example.)
+// has them, touches 16 rows with every 16 lanes: the address path then bounds the kernel, 168 us where turned codes took
+// 145, before later steps, for the gate and up products of the few-row kernel's example.)
 // Scale and zero point: lane 4r + j has those of row r and every fourth group, from the j-th on.
 template <int G, int NT>
 struct Codes {
